@@ -6,20 +6,27 @@ for device memory and streams.
 """
 from ._hla import (  # noqa: F401
     Cache,
+    GdnConfig,
     HlaConfig,
     HlaError,
     cache_bytes,
     decode_workspace_bytes,
     gdn_chunk_transitions,
+    gdn_forward,
+    gdn_step,
+    gdn_workspace_bytes,
+    hla_cache_evict,
     hla_decode_step,
     hla_decode_step_static,
     hla_check_bounded_wait,
     hla_device_status,
+    hla_gate_mass,
     hla_prefill,
     hla_profile_enable,
     hla_profile_read,
     hla_routing,
     lib,
     make_config,
+    make_gdn_config,
     prefill_workspace_bytes,
 )

@@ -27,7 +27,8 @@ HLA_F32 = 0
 HLA_BF16 = 1
 HLA_CACHE_DENSE = 0
 HLA_CACHE_FACTORED = 1
-CACHE_FORMATS = {"dense": HLA_CACHE_DENSE, "factored": HLA_CACHE_FACTORED}
+HLA_CACHE_INT8 = 2
+CACHE_FORMATS = {"dense": HLA_CACHE_DENSE, "factored": HLA_CACHE_FACTORED, "int8": HLA_CACHE_INT8}
 GATE_MODES = {"routed": 0, "one": 1, "zero": 2, "user": 3}
 DECAY_MODES = {"scalar": 0, "channel": 1}
 
@@ -48,7 +49,13 @@ class HlaCache(ctypes.Structure):
                 ("Uf", ctypes.c_void_p), ("df", ctypes.c_void_p), ("rk", ctypes.c_void_p),
                 ("buf_k", ctypes.c_void_p), ("buf_v", ctypes.c_void_p), ("buf_qr", ctypes.c_void_p),
                 ("buf_kr", ctypes.c_void_p), ("buf_alpha", ctypes.c_void_p), ("buf_beta", ctypes.c_void_p),
-                ("n_chunks", ctypes.c_void_p), ("m_partial", ctypes.c_void_p)]
+                ("n_chunks", ctypes.c_void_p), ("m_partial", ctypes.c_void_p), ("mass", ctypes.c_void_p)]
+
+
+class GdnConfig(ctypes.Structure):
+    _fields_ = [("n_seq", ctypes.c_int32), ("Hk", ctypes.c_int32), ("H", ctypes.c_int32), ("dk", ctypes.c_int32),
+                ("dv", ctypes.c_int32), ("dtype", ctypes.c_int32), ("decay_mode", ctypes.c_int32),
+                ("n_slots", ctypes.c_int32)]
 
 
 class HlaError(RuntimeError):
@@ -67,6 +74,14 @@ _SIGS = {
                        ctypes.c_int),
     "hla_cache_slice": ([ctypes.POINTER(HlaCache), ctypes.c_int32, ctypes.c_int32, ctypes.POINTER(HlaCache)],
                         ctypes.c_int),
+    "hla_cache_track_mass": ([ctypes.POINTER(HlaCache), _P, _P], ctypes.c_int),
+    "hla_gate_mass": ([ctypes.POINTER(HlaConfig), _P, _P, _P], ctypes.c_int),
+    "hla_cache_evict": ([ctypes.POINTER(HlaConfig), ctypes.POINTER(HlaCache), ctypes.POINTER(HlaCache),
+                         ctypes.c_int32, ctypes.c_int32, _P, _P], ctypes.c_int),
+    "gdn_workspace_bytes": ([ctypes.POINTER(GdnConfig), ctypes.c_int32], ctypes.c_size_t),
+    "gdn_forward": ([ctypes.POINTER(GdnConfig), _P, _P, _P, _P, _P, _P, ctypes.c_int32, _P, _P, _P, _P, _P,
+                     ctypes.c_size_t, _P], ctypes.c_int),
+    "gdn_step": ([ctypes.POINTER(GdnConfig), _P, _P, _P, _P, _P, _P, _P, _P, _P], ctypes.c_int),
     "hla_prefill_workspace_bytes": ([ctypes.POINTER(HlaConfig)], ctypes.c_size_t),
     "hla_decode_workspace_bytes": ([ctypes.POINTER(HlaConfig), ctypes.c_int32], ctypes.c_size_t),
     "gdn_chunk_transitions": ([ctypes.POINTER(HlaConfig), _P, _P, _P, _P, _P, _P, _P], ctypes.c_int),
@@ -154,6 +169,41 @@ def decode_workspace_bytes(cfg: HlaConfig, max_chunks: int) -> int:
     return int(lib().hla_decode_workspace_bytes(ctypes.byref(cfg), max_chunks))
 
 
+def _arg(t, name, dtype, numel, device):
+    """Device pointer of a tensor argument of the given dtype and size (None stays None)."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: libhla takes CUDA device tensors only (no CPU path)")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the call's other tensors on {device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.numel() != numel:
+        raise ValueError(f"{name}: expected {numel} elements, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _run(device, stream, fn, *args):
+    """Call fn(*args, stream) with `device` current, on its current stream by default."""
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    elif stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+    if device.index == torch.cuda.current_device():
+        _check(fn(*args, stream.cuda_stream))
+    else:
+        with torch.cuda.device(device):
+            _check(fn(*args, stream.cuda_stream))
+
+
+_DTYPES = {HLA_F32: torch.float32, HLA_BF16: torch.bfloat16}
+
+
 class CacheSlice:
     """Sequences [b0, b0 + nb) of a Cache (see Cache.slice)."""
 
@@ -176,6 +226,59 @@ class Cache:
                                     ctypes.byref(self.struct), _stream(stream)))
         self.cfg = cfg
         self.max_chunks = max_chunks
+
+    @classmethod
+    def from_tensors(cls, cfg: HlaConfig, max_chunks: int, **buffers):
+        """A cache over the caller's own tensors, one per field of the C struct that the
+        format uses (include/hla.h has the shapes), with the state that they hold: nothing
+        is copied or cleared.  `mass` is optional (see track_mass)."""
+        if not isinstance(max_chunks, int) or max_chunks < 1 or cache_bytes(cfg, max_chunks) == 0:
+            raise HlaError(HLA_ERR_UNSUPPORTED, "unsupported cache config")
+        B, H, C, d = cfg.B, cfg.H, cfg.C, cfg.dk
+        if cfg.cache_format == HLA_CACHE_FACTORED and not (cfg.dtype == HLA_BF16 and d == 128 and C == 64):
+            raise HlaError(HLA_ERR_UNSUPPORTED, "a factored cache needs bf16, d = 128 and C = 64")
+        dt, f32, i32 = _DTYPES[cfg.dtype], torch.float32, torch.int32
+        n = B * H * max_chunks
+        reps = C // cfg.pool_window if cfg.pool_window else 1
+        want = {"rk": (f32, n * reps * d), "buf_alpha": (f32, B * H * C * (d if cfg.decay_mode else 1)),
+                "buf_beta": (f32, B * H * C), "n_chunks": (i32, B), "m_partial": (i32, B), "mass": (f32, n)}
+        want.update({f: (dt, B * H * C * d) for f in ("buf_k", "buf_v", "buf_qr", "buf_kr")})
+        if cfg.cache_format == HLA_CACHE_FACTORED:
+            want.update({f: (dt, n * C * d) for f in ("Kf", "Wf", "Uf")}, df=(f32, n * (C + 4)))
+        elif cfg.cache_format == HLA_CACHE_INT8:
+            want.update(A=(torch.int8, n * d * d), Bm=(torch.int8, n * d * d), df=(f32, n * 4))
+        else:
+            want.update(A=(dt, n * d * d), Bm=(dt, n * d * d))
+        if set(buffers) - set(want) or set(want) - set(buffers) - {"mass"}:
+            raise ValueError(f"expected the buffers {sorted(set(want) - {'mass'})} (and mass), got {sorted(buffers)}")
+        self = cls.__new__(cls)
+        self.struct = HlaCache()
+        st = self.struct
+        st.max_chunks, st.B, st.H, st.C, st.d, st.dtype = max_chunks, B, H, C, d, cfg.dtype
+        st.format, st.pool_window, st.decay_mode = cfg.cache_format, cfg.pool_window, cfg.decay_mode
+        device = next(iter(buffers.values())).device
+        for name, t in buffers.items():
+            if t is None and name != "mass":
+                raise TypeError(f"{name}: expected a torch.Tensor")
+            setattr(st, name, _arg(t, name, *want[name], device))
+        self.mem = None
+        self.buffers = dict(buffers)  # keeps the memory alive
+        self.cfg = cfg
+        self.max_chunks = max_chunks
+        return self
+
+    def track_mass(self, mass=None, stream=None):
+        """Accumulate every closed chunk's gate weight from now on; returns the
+        [B, H, max_chunks] float32 tensor that holds it (given or made here, zeroed)."""
+        s = self.struct
+        device = self.mem.device if self.mem is not None else self.buffers["rk"].device
+        shape = (s.B, s.H, s.max_chunks)
+        if mass is None:
+            mass = torch.empty(shape, dtype=torch.float32, device=device)
+        p = _arg(mass, "mass", torch.float32, s.B * s.H * s.max_chunks, device)
+        _run(device, stream, lib().hla_cache_track_mass, ctypes.byref(s), p)
+        self.mass = mass
+        return mass
 
     def slice(self, b0: int, nb: int):
         """The cache of sequences [b0, b0 + nb) (shares this cache's memory)."""
@@ -210,6 +313,72 @@ def hla_gate_support(cfg, gates, mass_out=None, support_out=None, stream=None):
     """Routing mass and effective support per query chunk from a gate matrix."""
     _check(lib().hla_gate_support(ctypes.byref(cfg), _ptr(gates), _ptr(mass_out), _ptr(support_out),
                                   _stream(stream)))
+
+
+def hla_gate_mass(cfg, gates, mass_out, stream=None):
+    """Weight that every chunk carried over a prompt, from its gate matrix."""
+    n = (cfg.T + cfg.C - 1) // cfg.C if cfg.C > 0 else 0
+    bh = cfg.B * cfg.H
+    g = _arg(gates, "gates", torch.float32, bh * n * n, gates.device)
+    m = _arg(mass_out, "mass_out", torch.float32, bh * n, gates.device)
+    _run(gates.device, stream, lib().hla_gate_mass, ctypes.byref(cfg), g, m)
+    return mass_out
+
+
+def hla_cache_evict(cfg, src, dst, keep, recent, kept_out, stream=None):
+    """Keep per (sequence, head) the `recent` last chunks of `src` and the heaviest others,
+    `keep` in all; `dst` is `src` (in place) or another cache."""
+    p = _arg(kept_out, "kept_out", torch.int32, cfg.B * cfg.H * keep, kept_out.device)
+    _run(kept_out.device, stream, lib().hla_cache_evict, ctypes.byref(cfg), ctypes.byref(src.struct),
+         ctypes.byref(dst.struct), keep, recent, p)
+    return kept_out
+
+
+def make_gdn_config(n_seq, H, d=128, dtype="bf16", Hk=None, n_slots=None, decay="scalar") -> GdnConfig:
+    dt = {"bf16": HLA_BF16, "f32": HLA_F32, torch.bfloat16: HLA_BF16, torch.float32: HLA_F32}[dtype]
+    dm = DECAY_MODES[decay] if isinstance(decay, str) else int(decay)
+    return GdnConfig(n_seq, H if Hk is None else Hk, H, d, d, dt, dm, n_seq if n_slots is None else n_slots)
+
+
+def gdn_workspace_bytes(cfg: GdnConfig, T: int) -> int:
+    return int(lib().gdn_workspace_bytes(ctypes.byref(cfg), T))
+
+
+def _gdn_args(cfg, T, q, k, v, alpha, beta, o):
+    dt, dev, d = _DTYPES.get(cfg.dtype, q.dtype), q.device, cfg.dk
+    return (_arg(q, "q", dt, T * cfg.Hk * d, dev), _arg(k, "k", dt, T * cfg.Hk * d, dev),
+            _arg(v, "v", dt, T * cfg.H * d, dev),
+            _arg(alpha, "alpha", torch.float32, T * cfg.H * (d if cfg.decay_mode else 1), dev),
+            _arg(beta, "beta", torch.float32, T * cfg.H, dev), _arg(o, "o", dt, T * cfg.H * d, dev))
+
+
+def gdn_forward(cfg: GdnConfig, q, k, v, alpha, beta, cu_seqlens, o, state_in=None, state_out=None, slots=None,
+                workspace=None, stream=None):
+    """Ragged sequences through the gated delta rule, states in and out (include/hla.h)."""
+    T, dev = v.shape[0], q.device
+    pq, pk, pv, pa, pb, po = _gdn_args(cfg, T, q, k, v, alpha, beta, o)
+    ns = cfg.n_slots * cfg.H * cfg.dv * cfg.dk
+    if workspace is None:
+        workspace = torch.empty(max(gdn_workspace_bytes(cfg, T), 256), dtype=torch.uint8, device=dev)
+        if stream is not None:
+            workspace.record_stream(stream)
+    nb = workspace.numel() * workspace.element_size()
+    _run(dev, stream, lib().gdn_forward, ctypes.byref(cfg), pq, pk, pv, pa, pb,
+         _arg(cu_seqlens, "cu_seqlens", torch.int32, cfg.n_seq + 1, dev), T,
+         _arg(slots, "slots", torch.int32, cfg.n_seq, dev), _arg(state_in, "state_in", torch.float32, ns, dev),
+         _arg(state_out, "state_out", torch.float32, ns, dev), po,
+         _arg(workspace, "workspace", workspace.dtype, workspace.numel(), dev), nb)
+    return o
+
+
+def gdn_step(cfg: GdnConfig, q, k, v, alpha, beta, state, o, slots=None, stream=None):
+    """One token per sequence through the gated delta rule, the states updated in place."""
+    dev = q.device
+    pq, pk, pv, pa, pb, po = _gdn_args(cfg, cfg.n_seq, q, k, v, alpha, beta, o)
+    _run(dev, stream, lib().gdn_step, ctypes.byref(cfg), pq, pk, pv, pa, pb,
+         _arg(slots, "slots", torch.int32, cfg.n_seq, dev),
+         _arg(state, "state", torch.float32, cfg.n_slots * cfg.H * cfg.dv * cfg.dk, dev), po)
+    return o
 
 
 def hla_prefill(cfg, q, k, v, alpha, beta, o, q_route=None, k_route=None, user_gates=None, gates_out=None,

@@ -129,6 +129,7 @@ __global__ void __launch_bounds__(128) decode_main_kernel(DecodeArgs a) {
         const int pos = cnt + before + __popc(bal & ((1u << (tid & 31)) - 1u));
         act_idx[pos] = j;
         act_g[pos] = g;
+        if (a.mass != nullptr) a.mass[(long)bh * a.max_chunks + j] += g;
       }
       cnt += total;
       __syncthreads();
@@ -142,14 +143,37 @@ __global__ void __launch_bounds__(128) decode_main_kernel(DecodeArgs a) {
   for (int p = cnt - 1; p >= 0; --p) {
     const int j = act_idx[p];
     const float g = act_g[p];
-    const Tio* A = (const Tio*)a.A + ((long)bh * a.max_chunks + j) * (long)D * D + (long)tid * D;
-    const Tio* Bm = (const Tio*)a.Bm + ((long)bh * a.max_chunks + j) * (long)D * D + (long)tid * D;
     float ax = 0.0f, bx = 0.0f;
+    if (a.format == HLA_CACHE_INT8) {
+      // A_j x = a_j x + sA (QA x), B_j x = sB (QB x): codes of row tid
+      const long slot = (long)bh * a.max_chunks + j;
+      const char4* A = (const char4*)((const int8_t*)a.A + slot * D * D + (long)tid * D);
+      const char4* Bm = (const char4*)((const int8_t*)a.Bm + slot * D * D + (long)tid * D);
+#pragma unroll 4
+      for (int c = 0; c < D / 4; ++c) {
+        const char4 qa = A[c], qb = Bm[c];
+        const float* xc = &xs[cur][4 * c];
+        ax = fmaf((float)qa.x, xc[0], ax);
+        ax = fmaf((float)qa.y, xc[1], ax);
+        ax = fmaf((float)qa.z, xc[2], ax);
+        ax = fmaf((float)qa.w, xc[3], ax);
+        bx = fmaf((float)qb.x, xc[0], bx);
+        bx = fmaf((float)qb.y, xc[1], bx);
+        bx = fmaf((float)qb.z, xc[2], bx);
+        bx = fmaf((float)qb.w, xc[3], bx);
+      }
+      const float4 sc = *(const float4*)(a.df + slot * 4);
+      ax = fmaf(sc.x, xs[cur][tid], sc.y * ax);
+      bx *= sc.z;
+    } else {
+      const Tio* A = (const Tio*)a.A + ((long)bh * a.max_chunks + j) * (long)D * D + (long)tid * D;
+      const Tio* Bm = (const Tio*)a.Bm + ((long)bh * a.max_chunks + j) * (long)D * D + (long)tid * D;
 #pragma unroll 8
-    for (int c = 0; c < D; ++c) {
-      const float xc = xs[cur][c];
-      ax = fmaf(ldf(A + c), xc, ax);
-      bx = fmaf(ldf(Bm + c), xc, bx);
+      for (int c = 0; c < D; ++c) {
+        const float xc = xs[cur][c];
+        ax = fmaf(ldf(A + c), xc, ax);
+        bx = fmaf(ldf(Bm + c), xc, bx);
+      }
     }
     y = fmaf(g, bx, y);
     xs[cur ^ 1][tid] = (1.0f - g) * xs[cur][tid] + g * ax;
@@ -172,6 +196,8 @@ __device__ __forceinline__ void close_pool(const DecodeArgs& a) {
     if (tid == 0) report_device_error(kErrCacheFull);
     return;
   }
+  // the new chunk has carried no weight yet
+  if (tid == 0 && a.mass != nullptr) a.mass[(long)bh * a.max_chunks + n] = 0.0f;
   const route::Consts K = route::make_consts();
   const float inv_tau = __fdiv_rn(1.0f, a.tau);
   // one pool over the chunk, or one per window of C / W tokens
@@ -336,12 +362,36 @@ static cudaError_t launch_close(const DecodeArgs& a, cudaStream_t s) {
   t.df = a.df;
   t.ab_chunk_stride = a.max_chunks;
   t.ab_chunk_offset = 0;
+  if (a.format == HLA_CACHE_INT8) {  // by way of the scratch, then into codes
+    t.A = a.scratch_A;
+    t.Bm = a.scratch_B;
+    t.ab_chunk_stride = 1;
+    t.close_scratch = 1;
+  }
   t.close_m = a.m_partial;
   t.close_n = a.n_chunks;
   // the transition kernel never writes past max_chunks; the pool kernel flags it.
   // Chunks longer than one 64-token WY tile close by the token rule (no workspace).
   cudaError_t e = (a.C > 64 || a.alpha_vec) ? launch_transitions_token(t, s) : launch_transitions(t, s);
   if (e != cudaSuccess) return e;
+  if (a.format == HLA_CACHE_INT8) {
+    Cache8Args c{};
+    c.B = a.B;
+    c.H = a.H;
+    c.C = a.C;
+    c.d = D;
+    c.dtype = a.dtype;
+    c.max_chunks = a.max_chunks;
+    c.A = a.scratch_A;
+    c.Bm = a.scratch_B;
+    c.qa = const_cast<void*>(a.A);
+    c.qb = const_cast<void*>(a.Bm);
+    c.scales = a.df;
+    c.close_m = a.m_partial;
+    c.close_n = a.n_chunks;
+    e = launch_cache8(c, true, s);
+    if (e != cudaSuccess) return e;
+  }
   // the pool and counters kernels are programmatic dependents of the kernel before each
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -363,7 +413,7 @@ static cudaError_t launch_close(const DecodeArgs& a, cudaStream_t s) {
 
 cudaError_t launch_decode_main(const DecodeArgs& a, cudaStream_t s) {
   if (a.format == HLA_CACHE_FACTORED) return launch_decode_stream_factored(a, s);
-  if (a.d == 128 && a.dtype == HLA_BF16) return launch_decode_stream(a, s);
+  if (a.d == 128 && a.dtype == HLA_BF16 && a.format == HLA_CACHE_DENSE) return launch_decode_stream(a, s);
   if (a.d == 128) return a.dtype == HLA_BF16 ? launch_main<128, __nv_bfloat16>(a, s) : launch_main<128, float>(a, s);
   return a.dtype == HLA_BF16 ? launch_main<64, __nv_bfloat16>(a, s) : launch_main<64, float>(a, s);
 }

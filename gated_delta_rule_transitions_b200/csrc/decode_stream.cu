@@ -178,6 +178,7 @@ __device__ __forceinline__ int decode_prologue(const DecodeArgs& a, int bh, int 
         const int pos = cnt + before + __popc(bal & ((1u << (tid & 31)) - 1u));
         act_idx[pos] = j;
         act_g[pos] = g;
+        if (a.mass != nullptr) a.mass[(long)bh * a.max_chunks + j] += g;
       }
       cnt += total;
       tc::bar_sync(1, kCompute);
@@ -319,6 +320,7 @@ __global__ void __launch_bounds__(kThreads, 3)
           const int pos = cnt + before + __popc(bal & ((1u << (tid & 31)) - 1u));
           act_idx[pos] = j;
           act_g[pos] = g;
+          if (a.mass != nullptr) a.mass[(long)bh * a.max_chunks + j] += g;
         }
         cnt += total;
         tc::bar_sync(1, kCompute);

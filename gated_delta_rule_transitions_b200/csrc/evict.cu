@@ -1,0 +1,249 @@
+// Eviction of cached chunks by accumulated gate weight.
+//
+// HLA summary page, "Methodology in Plain English" para. 4 (chunks with little routing
+// weight are left out; leaving a chunk out is exact, it acts as the identity) and "Main
+// Findings" (the per-chunk affine states are what a decode cache holds): a cache that has
+// reached its budget drops, per (sequence, head), the chunks whose gates have carried the
+// least weight so far:
+//   mass_j = sum over query tokens t of the gate of t's chunk on chunk j.
+// Three kernels:
+//   gate_mass_kernel   column sums of a gate matrix, each row weighted by its chunk's tokens;
+//   evict_select       one CTA per (sequence, head): the `recent` last chunks stay, the
+//                      others compete by (mass descending, index ascending): a radix select
+//                      over the 32 key bits, 8 at a time, then an ordered compaction;
+//   evict_move         moves every per-chunk array to its place.  A thread owns 16 bytes of
+//                      the chunk and takes the kept chunks in ascending order; entry i comes
+//                      from a chunk kept[i] >= i, and reads run ahead of writes, so the move
+//                      is safe in place without any barrier.
+#include "common.cuh"
+#include "kernels.cuh"
+
+namespace hla {
+
+namespace {
+
+// ---- mass from a gate matrix -----------------------------------------------------------
+
+constexpr int kMassCols = 32;   // columns per CTA: one 128-byte segment of a row
+constexpr int kMassWarps = 16;  // rows in flight per CTA
+
+__global__ void __launch_bounds__(32 * kMassWarps) gate_mass_kernel(const float* __restrict__ gates, int N, int ncols,
+                                                                     int C, int T, float thr, float* __restrict__ mass,
+                                                                     long mass_stride) {
+  __shared__ float part[kMassWarps][kMassCols];
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int tiles = (ncols + kMassCols - 1) / kMassCols;
+  const long bh = blockIdx.x / tiles;
+  const int j0 = (int)(blockIdx.x % tiles) * kMassCols;
+  const int j = j0 + lane;
+  const float* G = gates + bh * (long)N * N;
+  float acc = 0.0f;
+  // rows i > j hold a weight on chunk j; row i stands for the tokens of chunk i
+#pragma unroll 8
+  for (int i = j0 + 1 + w; i < N; i += kMassWarps) {
+    if (j < i) {
+      const float g = __ldg(G + (long)i * N + j);
+      if (thr <= 0.0f || g >= thr) acc = fmaf((float)min(C, T - i * C), g, acc);
+    }
+  }
+  part[w][lane] = acc;
+  __syncthreads();
+  if (w == 0 && j < ncols) {
+    float s = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kMassWarps; ++k) s += part[k][lane];
+    mass[bh * mass_stride + j] = s;
+  }
+}
+
+// ---- selection ------------------------------------------------------------------------
+
+constexpr int kSelThreads = 256;
+
+// Order-preserving key of a weight: larger weight, larger key (a NaN counts as no weight).
+__device__ __forceinline__ uint32_t mass_key(float m) {
+  if (m != m) return 0u;
+  const uint32_t u = __float_as_uint(m + 0.0f);  // -0 counts as +0
+  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+
+// Exclusive prefix of `flag` over the CTA's threads, in thread order; total in *sum.
+__device__ __forceinline__ int block_prefix(bool flag, int* wsum, int* sum) {
+  const unsigned bal = __ballot_sync(0xFFFFFFFFu, flag);
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  __syncthreads();
+  if (lane == 0) wsum[w] = __popc(bal);
+  __syncthreads();
+  int before = 0, all = 0;
+#pragma unroll
+  for (int k = 0; k < kSelThreads / 32; ++k) {
+    if (k < w) before += wsum[k];
+    all += wsum[k];
+  }
+  *sum = all;
+  return before + __popc(bal & ((1u << lane) - 1u));
+}
+
+__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictArgs a) {
+  __shared__ int hist[256];
+  __shared__ int wsum[kSelThreads / 32];
+  __shared__ int pick[2];  // digit, how many of the wanted lie above it
+  const long bh = blockIdx.x;
+  const int b = (int)(bh / a.H);
+  const int tid = threadIdx.x;
+  const int n = max(0, min(a.n_src[b], a.src_chunks));
+  int32_t* kept = a.kept + bh * a.keep;
+  const float* mass = a.mass + bh * a.src_chunks;
+  if (n <= a.keep) {
+    for (int i = tid; i < a.keep; i += kSelThreads) kept[i] = i < n ? i : -1;
+    return;
+  }
+  const int old = n - a.recent;        // chunks that compete
+  int want = a.keep - a.recent;        // how many of them stay (< old)
+  // the key of the last one that stays (`prefix`), and how many with that key stay (`want`)
+  uint32_t prefix = 0, mask = 0;
+  if (want > 0) {
+    for (int shift = 24; shift >= 0; shift -= 8) {
+      hist[tid] = 0;
+      __syncthreads();
+      for (int j = tid; j < old; j += kSelThreads) {
+        const uint32_t key = mass_key(mass[j]);
+        if ((key & mask) == prefix) atomicAdd(&hist[(key >> shift) & 255u], 1);
+      }
+      __syncthreads();
+      // thread = digit: how many keys have a larger one
+      int above = 0;
+      for (int d = tid + 1; d < 256; ++d) above += hist[d];
+      if (above < want && above + hist[tid] >= want) {
+        pick[0] = tid;
+        pick[1] = above;
+      }
+      __syncthreads();
+      prefix |= (uint32_t)pick[0] << shift;
+      mask |= 255u << shift;
+      want -= pick[1];
+      __syncthreads();
+    }
+  }
+  // ascending compaction: larger keys, the first `want` of the equal ones, the recent ones
+  int pos = 0, equal_before = 0;
+  for (int j0 = 0; j0 < n; j0 += kSelThreads) {
+    const int j = j0 + tid;
+    bool larger = j >= old && j < n, equal = false;
+    if (j < old && a.keep > a.recent) {
+      const uint32_t key = mass_key(mass[j]);
+      larger = key > prefix;
+      equal = key == prefix;
+    }
+    int eq_total, total;
+    const int eq = equal_before + block_prefix(equal, wsum, &eq_total);
+    const bool stays = larger || (equal && eq < want);
+    const int at = pos + block_prefix(stays, wsum, &total);
+    if (stays) kept[at] = j;
+    equal_before += eq_total;
+    pos += total;
+  }
+}
+
+// ---- moving ---------------------------------------------------------------------------
+
+constexpr int kMoveThreads = 128;
+constexpr int kMoveBatch = 8;
+
+// One 16-byte column of one array, over the kept chunks [i0, i1) in ascending order.
+__device__ __forceinline__ void move_column(const uint4* src, uint4* dst, long pitch, const int32_t* kept, int i0,
+                                            int i1, bool in_place) {
+  for (int i = i0; i < i1; i += kMoveBatch) {
+    uint4 r[kMoveBatch];
+    int j[kMoveBatch];
+#pragma unroll
+    for (int u = 0; u < kMoveBatch; ++u) {
+      j[u] = i + u < i1 ? kept[i + u] : -1;
+      if (in_place && j[u] == i + u) j[u] = -1;  // already there
+      if (j[u] >= 0) r[u] = src[(long)j[u] * pitch];
+    }
+#pragma unroll
+    for (int u = 0; u < kMoveBatch; ++u)
+      if (j[u] >= 0) dst[(long)(i + u) * pitch] = r[u];
+  }
+}
+
+// grid (B H (column blocks + 1), splits of the kept list).  The last column block of a
+// (sequence, head) finishes it: the weights move with their chunks, the open chunk and
+// the counters go along to another cache, and the count changes.  Nothing here but that
+// last step reads the counts (the list ends at its first -1), so it may change them.
+__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(EvictArgs a, unsigned blocks) {
+  const long bh = blockIdx.x / (blocks + 1);
+  const unsigned blk = blockIdx.x % (blocks + 1);
+  const int tid = threadIdx.x;
+  const int32_t* kept = a.kept + bh * a.keep;
+  if (blk < blocks) {
+    const int per = (a.keep + gridDim.y - 1) / gridDim.y;
+    const int i0 = min(a.keep, (int)blockIdx.y * per), i1 = min(a.keep, i0 + per);
+    // this thread's 16-byte column among all arrays' columns
+    long col = (long)blk * kMoveThreads + tid;
+    for (int x = 0; x < a.n_arrays; ++x) {
+      const long cols = a.chunk_bytes[x] / 16;
+      if (col < cols) {
+        move_column((const uint4*)a.src[x] + bh * a.src_chunks * cols + col,
+                    (uint4*)a.dst[x] + bh * a.dst_chunks * cols + col, cols, kept, i0, i1, a.in_place);
+        return;
+      }
+      col -= cols;
+    }
+    return;
+  }
+  if (blockIdx.y != 0) return;
+  const int b = (int)(bh / a.H), h = (int)(bh % a.H);
+  if (a.mass_dst != nullptr) {
+    const float* src = a.mass + bh * a.src_chunks;
+    float* dst = a.mass_dst + bh * a.dst_chunks;
+    for (int i0 = 0; i0 < a.keep; i0 += kMoveThreads) {
+      const int i = i0 + tid;
+      const int j = i < a.keep ? kept[i] : -1;
+      const float m = j >= 0 ? src[j] : 0.0f;
+      __syncthreads();  // in place: this round's reads before its writes
+      if (j >= 0) dst[i] = m;
+    }
+  }
+  if (!a.in_place) {
+    for (int x = 0; x < a.n_open; ++x) {
+      const long cols = a.open_bytes[x] / 16;
+      const uint4* s4 = (const uint4*)a.open_src[x] + bh * cols;
+      uint4* d4 = (uint4*)a.open_dst[x] + bh * cols;
+      for (long c = tid; c < cols; c += kMoveThreads) d4[c] = s4[c];
+    }
+    if (h == 0 && tid == 0) a.m_dst[b] = a.m_src[b];
+  }
+  if (h == 0 && tid == 0) a.n_dst[b] = min(max(0, min(a.n_src[b], a.src_chunks)), a.keep);
+}
+
+}  // namespace
+
+cudaError_t launch_gate_mass(const float* gates, int B, int H, int N, int ncols, int C, int T, float thr, float* mass,
+                             long mass_stride, cudaStream_t s) {
+  const long blocks = (long)B * H * ((ncols + kMassCols - 1) / kMassCols);
+  if (blocks <= 0) return cudaSuccess;
+  if (blocks >= (1L << 31)) return cudaErrorNotSupported;
+  gate_mass_kernel<<<(unsigned)blocks, 32 * kMassWarps, 0, s>>>(gates, N, ncols, C, T, thr, mass, mass_stride);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_evict(const EvictArgs& a, cudaStream_t s) {
+  const long BH = (long)a.B * a.H;
+  long cols = 0;
+  for (int x = 0; x < a.n_arrays; ++x) cols += a.chunk_bytes[x] / 16;
+  const long blocks = (cols + kMoveThreads - 1) / kMoveThreads;
+  if (BH * (blocks + 1) >= (1L << 31)) return cudaErrorNotSupported;
+  evict_select_kernel<<<(unsigned)BH, kSelThreads, 0, s>>>(a);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  // into another cache the kept list can be split as well
+  unsigned split = 1;
+  if (!a.in_place)
+    while (blocks * BH * split < 8L * num_sms() && (long)split * 2 * kMoveBatch <= a.keep) split *= 2;
+  evict_move_kernel<<<dim3((unsigned)(BH * (blocks + 1)), split), kMoveThreads, 0, s>>>(a, (unsigned)blocks);
+  return cudaGetLastError();
+}
+
+}  // namespace hla

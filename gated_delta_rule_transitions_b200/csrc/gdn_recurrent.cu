@@ -1,0 +1,260 @@
+// The gated delta rule token by token, with a state that is carried in and out
+// (float32 arithmetic on CUDA cores): the one-token step of a decode batch, and the
+// ragged forward of every type, head dim and decay.
+//
+// HLA summary page, "Methodology in Plain English" para. 1: the per-token affine rule
+//   S <- S Diag(alpha_t);  u_t = beta_t (v_t - S k_t);  S <- S + u_t k_t^T;  o_t = S q_t
+// (alpha_t one decay per head, or one per key channel).  Rows of S evolve on their own.
+//
+// A CTA of 128 threads holds 16 R rows of one (sequence, head)'s state in registers:
+// 8 threads per R rows, thread g of a group on the columns 32 m + 4 g + u (u < 4), so
+// that state loads and stores are 128-byte segments and the dot products over a row are
+// three shuffles.  Keys, queries, values and decays of 8 or 16 tokens at a time come in by
+// cp.async as they are stored (two buffers: the next tokens land while these are worked
+// on); outputs leave through shared memory.
+#include "common.cuh"
+#include "kernels.cuh"
+
+namespace hla {
+
+HLA_DEFINE_ERROR_WORD(gdn_recurrent)
+
+namespace {
+
+constexpr int kThreads = 128;
+// Tokens per staged segment: two segments of the widest rows fit in 48 KiB.
+template <typename Tio, bool kChan>
+constexpr int seg_len() { return sizeof(Tio) == 4 || kChan ? 8 : 16; }
+constexpr unsigned kFull = 0xFFFFFFFFu;
+
+__device__ __forceinline__ void cp16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src)
+               : "memory");
+}
+__device__ __forceinline__ void cp4(void* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src)
+               : "memory");
+}
+
+// Four consecutive values as two float pairs.
+__device__ __forceinline__ void ld4(const float* p, float2& lo, float2& hi) {
+  const float4 w = *(const float4*)p;
+  lo = make_float2(w.x, w.y);
+  hi = make_float2(w.z, w.w);
+}
+__device__ __forceinline__ void ld4(const __nv_bfloat16* p, float2& lo, float2& hi) {
+  const uint2 w = *(const uint2*)p;
+  lo = make_float2(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u));
+  hi = make_float2(__uint_as_float(w.y << 16), __uint_as_float(w.y & 0xFFFF0000u));
+}
+
+__device__ __forceinline__ float group_sum(float v) {
+  v += __shfl_xor_sync(kFull, v, 1);
+  v += __shfl_xor_sync(kFull, v, 2);
+  v += __shfl_xor_sync(kFull, v, 4);
+  return v;
+}
+
+template <int D, int R, typename Tio, bool kChan>
+struct Stage {
+  static constexpr int kSeg = seg_len<Tio, kChan>();
+  Tio k[kSeg][D];
+  Tio q[kSeg][D];
+  Tio v[kSeg][16 * R];
+  float a[kSeg][kChan ? D : 1];
+  float b[kSeg];
+};
+
+template <int D, int R, typename Tio, bool kChan>
+__global__ void __launch_bounds__(kThreads) gdn_recurrent_kernel(GdnArgs a) {
+  constexpr int kRows = 16 * R;
+  constexpr int kSplit = D / kRows;   // CTAs per (sequence, head)
+  constexpr int M = D / 32;           // 4-column groups per thread
+  constexpr int kVec = 16 / (int)sizeof(Tio);
+  constexpr int kSeg = seg_len<Tio, kChan>();
+  __shared__ __align__(16) Stage<D, R, Tio, kChan> st[2];
+  __shared__ float os[kSeg][kRows];
+  const int tid = threadIdx.x;
+  const int split = blockIdx.x % kSplit;
+  const long sh = blockIdx.x / kSplit;
+  const int h = (int)(sh % a.H);
+  const int seq = (int)(sh / a.H);
+  const int hk = h / (a.H / a.Hk);
+  const int p = tid >> 3, g = tid & 7;
+  const int row0 = split * kRows + p * R;  // this group's rows row0 .. row0 + R - 1
+
+  // the sequence's tokens and its state; what the device arrays cannot mean is refused
+  // (nothing is read or written for that sequence)
+  int t0 = seq, t1 = seq + 1;
+  if (a.cu != nullptr) {
+    t0 = a.cu[seq];
+    t1 = a.cu[seq + 1];
+  }
+  int slot = seq;
+  if (a.slots != nullptr) {
+    slot = a.slots[seq];
+    if (slot < 0) return;  // padding of the batch
+    bool twice = false;    // an earlier sequence has the same state
+    for (int i = tid; i < seq; i += kThreads) twice |= a.slots[i] == slot;
+    if (__syncthreads_or(twice) || slot >= a.n_slots) {
+      if (tid == 0) report_device_error(kErrBadIndex);
+      return;
+    }
+  }
+  if (t0 < 0 || t1 < t0 || t1 > a.T) {
+    if (tid == 0) report_device_error(kErrBadIndex);
+    return;
+  }
+
+  const Tio* kin = (const Tio*)a.k + ((long)t0 * a.Hk + hk) * D;
+  const Tio* qin = (const Tio*)a.q + ((long)t0 * a.Hk + hk) * D;
+  const Tio* vin = (const Tio*)a.v + ((long)t0 * a.H + h) * D + split * kRows;
+  Tio* out = (Tio*)a.o + ((long)t0 * a.H + h) * D + split * kRows;
+  const float* ain = a.alpha + ((long)t0 * a.H + h) * (kChan ? D : 1);
+  const float* bin = a.beta + (long)t0 * a.H + h;
+  const int len = t1 - t0;
+
+  // tokens [s0, s0 + kSeg) into buffer w
+  auto stage = [&](int s0, int w) {
+    const int ns = min(kSeg, len - s0);
+    for (int e = tid; e < ns * (D / kVec); e += kThreads) {
+      const int t = e / (D / kVec), c = (e % (D / kVec)) * kVec;
+      const long row = (long)(s0 + t) * a.Hk * D + c;
+      cp16(&st[w].k[t][c], kin + row);
+      cp16(&st[w].q[t][c], qin + row);
+    }
+    for (int e = tid; e < ns * (kRows / kVec); e += kThreads) {
+      const int t = e / (kRows / kVec), c = (e % (kRows / kVec)) * kVec;
+      cp16(&st[w].v[t][c], vin + (long)(s0 + t) * a.H * D + c);
+    }
+    if (kChan) {
+      for (int e = tid; e < ns * (D / 4); e += kThreads) {
+        const int t = e / (D / 4), c = (e % (D / 4)) * 4;
+        cp16(&st[w].a[t][c], ain + (long)(s0 + t) * a.H * D + c);
+      }
+    } else if (tid >= 32 && tid < 32 + ns) {
+      cp4(&st[w].a[tid - 32][0], ain + (long)(s0 + tid - 32) * a.H);
+    }
+    if (tid < ns) cp4(&st[w].b[tid], bin + (long)(s0 + tid) * a.H);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  if (len > 0) stage(0, 0);
+
+  // the state: x[r][2 m + e] = columns 32 m + 4 g + 2 e, + 1 of row row0 + r
+  const long off = (((long)slot * a.H + h) * D + row0) * D + 4 * g;
+  float2 x[R][2 * M];
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+      float4 w = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (a.state_in != nullptr) w = *(const float4*)(a.state_in + off + (long)r * D + 32 * m);
+      x[r][2 * m] = make_float2(w.x, w.y);
+      x[r][2 * m + 1] = make_float2(w.z, w.w);
+    }
+
+  int w = 0;
+  for (int s0 = 0; s0 < len; s0 += kSeg, w ^= 1) {
+    const int ns = min(kSeg, len - s0);
+    if (s0 + kSeg < len) {
+      stage(s0 + kSeg, w ^ 1);
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+    } else {
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+    }
+    __syncthreads();
+    for (int t = 0; t < ns; ++t) {
+      float2 kr[2 * M];
+#pragma unroll
+      for (int m = 0; m < M; ++m) ld4(&st[w].k[t][32 * m + 4 * g], kr[2 * m], kr[2 * m + 1]);
+      if (kChan) {
+#pragma unroll
+        for (int m = 0; m < M; ++m) {
+          const float4 al = *(const float4*)&st[w].a[t][32 * m + 4 * g];
+#pragma unroll
+          for (int r = 0; r < R; ++r) {
+            x[r][2 * m] = __fmul2_rn(x[r][2 * m], make_float2(al.x, al.y));
+            x[r][2 * m + 1] = __fmul2_rn(x[r][2 * m + 1], make_float2(al.z, al.w));
+          }
+        }
+      }
+      const float at = kChan ? 1.0f : st[w].a[t][0];
+      const float bt = st[w].b[t];
+      float u[R];
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        float2 d0 = make_float2(0.0f, 0.0f), d1 = d0;
+#pragma unroll
+        for (int m = 0; m < M; ++m) {
+          d0 = __ffma2_rn(x[r][2 * m], kr[2 * m], d0);
+          d1 = __ffma2_rn(x[r][2 * m + 1], kr[2 * m + 1], d1);
+        }
+        u[r] = (d0.x + d0.y) + (d1.x + d1.y);
+      }
+#pragma unroll
+      for (int r = 0; r < R; ++r) u[r] = bt * (ldf(&st[w].v[t][p * R + r]) - at * group_sum(u[r]));
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const float2 ur = make_float2(u[r], u[r]), ar = make_float2(at, at);
+#pragma unroll
+        for (int j = 0; j < 2 * M; ++j)
+          x[r][j] = kChan ? __ffma2_rn(ur, kr[j], x[r][j]) : __ffma2_rn(ur, kr[j], __fmul2_rn(ar, x[r][j]));
+      }
+#pragma unroll
+      for (int m = 0; m < M; ++m) ld4(&st[w].q[t][32 * m + 4 * g], kr[2 * m], kr[2 * m + 1]);
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        float2 d0 = make_float2(0.0f, 0.0f), d1 = d0;
+#pragma unroll
+        for (int m = 0; m < M; ++m) {
+          d0 = __ffma2_rn(x[r][2 * m], kr[2 * m], d0);
+          d1 = __ffma2_rn(x[r][2 * m + 1], kr[2 * m + 1], d1);
+        }
+        const float y = group_sum((d0.x + d0.y) + (d1.x + d1.y));
+        if (g == r) os[t][p * R + r] = y;
+      }
+    }
+    __syncthreads();  // the segment's outputs are in shared memory and its buffer is free
+    for (int e = tid; e < ns * kRows; e += kThreads) {
+      const int t = e / kRows, r = e % kRows;
+      stf(out + (long)(s0 + t) * a.H * D + r, os[t][r]);
+    }
+  }
+  if (a.state_out == nullptr || (len == 0 && a.state_out == a.state_in)) return;
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int m = 0; m < M; ++m)
+      *(float4*)(a.state_out + off + (long)r * D + 32 * m) =
+          make_float4(x[r][2 * m].x, x[r][2 * m].y, x[r][2 * m + 1].x, x[r][2 * m + 1].y);
+}
+
+template <int D, int R, typename Tio>
+cudaError_t launch_r(const GdnArgs& a, cudaStream_t s) {
+  const long blocks = (long)a.n_seq * a.H * (D / (16 * R));
+  if (blocks >= (1L << 31)) return cudaErrorNotSupported;
+  if (a.alpha_vec)
+    gdn_recurrent_kernel<D, R, Tio, true><<<(unsigned)blocks, kThreads, 0, s>>>(a);
+  else
+    gdn_recurrent_kernel<D, R, Tio, false><<<(unsigned)blocks, kThreads, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+template <int D, typename Tio>
+cudaError_t launch_d(const GdnArgs& a, cudaStream_t s) {
+  // few (sequence, head) pairs: one row per group, so that four times as many CTAs share
+  // the work and each token's chain is shorter
+  const long pairs = (long)a.n_seq * a.H;
+  return pairs * (D / 64) >= 2L * num_sms() ? launch_r<D, 4, Tio>(a, s) : launch_r<D, 1, Tio>(a, s);
+}
+
+}  // namespace
+
+cudaError_t launch_gdn_recurrent(const GdnArgs& a, cudaStream_t s) {
+  if (a.n_seq <= 0) return cudaSuccess;
+  if (a.d == 128)
+    return a.dtype == HLA_BF16 ? launch_d<128, __nv_bfloat16>(a, s) : launch_d<128, float>(a, s);
+  return a.dtype == HLA_BF16 ? launch_d<64, __nv_bfloat16>(a, s) : launch_d<64, float>(a, s);
+}
+
+}  // namespace hla

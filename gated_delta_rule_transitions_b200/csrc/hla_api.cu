@@ -46,7 +46,8 @@ hla_status check_cfg(const hla_config* c, bool need_T) {
   if (c->dtype != HLA_F32 && c->dtype != HLA_BF16) return fail(HLA_ERR_UNSUPPORTED, "dtype %d unsupported", c->dtype);
   if (c->gate_mode < HLA_GATES_ROUTED || c->gate_mode > HLA_GATES_USER)
     return fail(HLA_ERR_INVALID_ARG, "gate_mode %d invalid", c->gate_mode);
-  if (c->cache_format != HLA_CACHE_DENSE && c->cache_format != HLA_CACHE_FACTORED)
+  if (c->cache_format != HLA_CACHE_DENSE && c->cache_format != HLA_CACHE_FACTORED &&
+      c->cache_format != HLA_CACHE_INT8)
     return fail(HLA_ERR_INVALID_ARG, "cache_format %d invalid", c->cache_format);
   if (c->decay_mode != HLA_DECAY_SCALAR && c->decay_mode != HLA_DECAY_CHANNEL)
     return fail(HLA_ERR_INVALID_ARG, "decay_mode %d invalid", c->decay_mode);
@@ -69,6 +70,12 @@ hla_status check_cfg(const hla_config* c, bool need_T) {
 hla_status need_ptr(const void* p, const char* name) {
   if (p == nullptr) return fail(HLA_ERR_INVALID_ARG, "%s is NULL", name);
   if (!aligned16(p)) return fail(HLA_ERR_INVALID_ARG, "%s is not 16-byte aligned", name);
+  return HLA_OK;
+}
+
+hla_status need_ptr4(const void* p, const char* name) {
+  if (p == nullptr) return fail(HLA_ERR_INVALID_ARG, "%s is NULL", name);
+  if (((uintptr_t)p & 3u) != 0) return fail(HLA_ERR_INVALID_ARG, "%s is not 4-byte aligned", name);
   return HLA_OK;
 }
 
@@ -195,6 +202,10 @@ CacheLayout cache_layout(const hla_config* c, int32_t maxc) {
     L.Wf = take(B * H * (size_t)maxc * C * d * es);
     L.Uf = take(B * H * (size_t)maxc * C * d * es);
     L.df = take(B * H * (size_t)maxc * df_stride(C) * 4);
+  } else if (c->cache_format == HLA_CACHE_INT8) {
+    L.A = take(B * H * (size_t)maxc * d * d);
+    L.Bm = take(B * H * (size_t)maxc * d * d);
+    L.df = take(B * H * (size_t)maxc * 4 * 4);
   } else {
     L.A = take(B * H * (size_t)maxc * d * d * es);
     L.Bm = take(B * H * (size_t)maxc * d * d * es);
@@ -212,6 +223,11 @@ CacheLayout cache_layout(const hla_config* c, int32_t maxc) {
   return L;
 }
 
+// One transition per (sequence, head), in the dtype.
+size_t close_scratch_bytes(const hla_config* c) {
+  return align256((size_t)c->B * c->H * c->dk * c->dk * esize(c->dtype));
+}
+
 hla_status check_cache(const hla_config* c, const hla_cache* k) {
   if (k == nullptr) return fail(HLA_ERR_INVALID_ARG, "cache is NULL");
   if (k->B != c->B || k->H != c->H || k->C != c->C || k->d != c->dk || k->dtype != c->dtype ||
@@ -226,7 +242,9 @@ hla_status check_cache(const hla_config* c, const hla_cache* k) {
   } else {
     HLA_TRY(need_ptr(k->A, "cache A"));
     HLA_TRY(need_ptr(k->Bm, "cache B"));
+    if (k->format == HLA_CACHE_INT8) HLA_TRY(need_ptr(k->df, "cache scales"));
   }
+  if (((uintptr_t)k->mass & 3u) != 0) return fail(HLA_ERR_INVALID_ARG, "cache mass misaligned");
   // the per-sequence counters are read and written as single int32 values, so a
   // slice starting at any sequence is valid
   for (const int32_t* p : {k->n_chunks, k->m_partial})
@@ -402,6 +420,7 @@ hla_status hla_cache_init(const hla_config* cfg, int32_t max_chunks, void* mem, 
   } else {
     c.A = base + L.A;
     c.Bm = base + L.Bm;
+    if (cfg->cache_format == HLA_CACHE_INT8) c.df = (float*)(base + L.df);
   }
   c.rk = (float*)(base + L.rk);
   c.buf_k = base + L.bk;
@@ -435,10 +454,15 @@ hla_status hla_cache_slice(const hla_cache* cache, int32_t b0, int32_t nb, hla_c
     v.Wf = (char*)cache->Wf + off * H * mc * C * d * es;
     v.Uf = (char*)cache->Uf + off * H * mc * C * d * es;
     v.df = (float*)((char*)cache->df + off * H * mc * df_stride(C) * 4);
+  } else if (cache->format == HLA_CACHE_INT8) {
+    v.A = (char*)cache->A + off * H * mc * d * d;
+    v.Bm = (char*)cache->Bm + off * H * mc * d * d;
+    v.df = cache->df + off * H * mc * 4;
   } else {
     v.A = (char*)cache->A + off * H * mc * d * d * es;
     v.Bm = (char*)cache->Bm + off * H * mc * d * d * es;
   }
+  if (cache->mass != nullptr) v.mass = cache->mass + off * H * mc;
   const size_t reps = cache->pool_window > 0 ? (size_t)(cache->C / cache->pool_window) : 1;
   v.rk = (float*)((char*)cache->rk + off * H * mc * reps * d * 4);
   v.buf_k = (char*)cache->buf_k + off * H * C * d * es;
@@ -454,6 +478,19 @@ hla_status hla_cache_slice(const hla_cache* cache, int32_t b0, int32_t nb, hla_c
   return HLA_OK;
 }
 
+hla_status hla_cache_track_mass(hla_cache* cache, float* mass, hla_stream_t stream) {
+  g_msg[0] = 0;
+  if (cache == nullptr) return fail(HLA_ERR_INVALID_ARG, "cache is NULL");
+  if (cache->B <= 0 || cache->H <= 0 || cache->max_chunks <= 0)
+    return fail(HLA_ERR_INVALID_ARG, "cache is not initialised");
+  if (((uintptr_t)mass & 3u) != 0) return fail(HLA_ERR_INVALID_ARG, "mass misaligned");
+  if (mass != nullptr)
+    HLA_CUDA(cudaMemsetAsync(mass, 0, (size_t)cache->B * cache->H * cache->max_chunks * 4, (cudaStream_t)stream),
+             "hla_cache_track_mass memset");
+  cache->mass = mass;
+  return HLA_OK;
+}
+
 size_t hla_prefill_workspace_bytes(const hla_config* cfg) {
   if (check_cfg(cfg, true) != HLA_OK) return 0;
   return prefill_layout(cfg).total;
@@ -463,7 +500,10 @@ size_t hla_decode_workspace_bytes(const hla_config* cfg, int32_t max_chunks) {
   if (check_cfg(cfg, false) != HLA_OK || max_chunks <= 0) return 0;
   const size_t n = (size_t)cfg->B * cfg->H * max_chunks;
   // active lists and gates [B,H,max_chunks], then one list length per (sequence, head)
-  return align256(n * 4) + align256(n * 4) + align256((size_t)cfg->B * cfg->H * 4);
+  size_t bytes = align256(n * 4) + align256(n * 4) + align256((size_t)cfg->B * cfg->H * 4);
+  // an 8-bit cache: the closing chunk's A and B before they are rounded
+  if (cfg->cache_format == HLA_CACHE_INT8) bytes += 2 * close_scratch_bytes(cfg);
+  return bytes;
 }
 
 hla_status gdn_chunk_transitions(const hla_config* cfg, const void* k, const void* v, const float* alpha,
@@ -615,6 +655,170 @@ hla_status hla_gate_support(const hla_config* cfg, const float* gates, float* ma
   return HLA_OK;
 }
 
+hla_status hla_gate_mass(const hla_config* cfg, const float* gates, float* mass_out, hla_stream_t stream) {
+  g_msg[0] = 0;
+  HLA_TRY(check_cfg(cfg, true));
+  HLA_TRY(need_ptr(gates, "gates"));
+  HLA_TRY(need_ptr(mass_out, "mass_out"));
+  const int N = (cfg->T + cfg->C - 1) / cfg->C;
+  HLA_CUDA(hla::launch_gate_mass(gates, cfg->B, cfg->H, N, N, cfg->C, cfg->T, cfg->skip_threshold, mass_out, N,
+                                 (cudaStream_t)stream),
+           "gate mass launch");
+  return HLA_OK;
+}
+
+hla_status hla_cache_evict(const hla_config* cfg, const hla_cache* src, hla_cache* dst, int32_t keep, int32_t recent,
+                           int32_t* kept_out, hla_stream_t stream) {
+  g_msg[0] = 0;
+  HLA_TRY(check_cfg(cfg, false));
+  HLA_TRY(check_cache(cfg, src));
+  HLA_TRY(check_cache(cfg, dst));
+  if (src->mass == nullptr) return fail(HLA_ERR_INVALID_ARG, "the source cache's mass is not tracked");
+  if (keep < 1 || keep > dst->max_chunks)
+    return fail(HLA_ERR_INVALID_ARG, "keep = %d outside [1, %d]", keep, dst->max_chunks);
+  if (recent < 0 || recent > keep) return fail(HLA_ERR_INVALID_ARG, "recent = %d outside [0, %d]", recent, keep);
+  HLA_TRY(need_ptr(kept_out, "kept_out"));
+  hla::EvictArgs e{};
+  e.B = cfg->B;
+  e.H = cfg->H;
+  e.src_chunks = src->max_chunks;
+  e.dst_chunks = dst->max_chunks;
+  e.keep = keep;
+  e.recent = recent;
+  e.mass = src->mass;
+  e.mass_dst = dst->mass;
+  e.kept = kept_out;
+  e.n_src = src->n_chunks;
+  e.n_dst = dst->n_chunks;
+  e.m_src = src->m_partial;
+  e.m_dst = dst->m_partial;
+  const long d = cfg->dk, C = cfg->C, es = (long)esize(cfg->dtype);
+  auto chunk_array = [&](const void* s, void* t, long bytes) {
+    e.src[e.n_arrays] = s;
+    e.dst[e.n_arrays] = t;
+    e.chunk_bytes[e.n_arrays++] = bytes;
+  };
+  auto open_array = [&](const void* s, void* t, long bytes) {
+    e.open_src[e.n_open] = s;
+    e.open_dst[e.n_open] = t;
+    e.open_bytes[e.n_open++] = bytes;
+  };
+  if (src->format == HLA_CACHE_FACTORED) {
+    chunk_array(src->Kf, dst->Kf, C * d * es);
+    chunk_array(src->Wf, dst->Wf, C * d * es);
+    chunk_array(src->Uf, dst->Uf, C * d * es);
+    chunk_array(src->df, dst->df, (long)df_stride((size_t)C) * 4);
+  } else {
+    const long el = src->format == HLA_CACHE_INT8 ? 1 : es;
+    chunk_array(src->A, dst->A, d * d * el);
+    chunk_array(src->Bm, dst->Bm, d * d * el);
+    if (src->format == HLA_CACHE_INT8) chunk_array(src->df, dst->df, 16);
+  }
+  chunk_array(src->rk, dst->rk, (long)key_reps(cfg) * d * 4);
+  open_array(src->buf_k, dst->buf_k, C * d * es);
+  open_array(src->buf_v, dst->buf_v, C * d * es);
+  open_array(src->buf_qr, dst->buf_qr, C * d * es);
+  open_array(src->buf_kr, dst->buf_kr, C * d * es);
+  open_array(src->buf_alpha, dst->buf_alpha, C * (chan(cfg) ? d : 1) * 4);
+  open_array(src->buf_beta, dst->buf_beta, C * 4);
+  // in place: every array is the source's own (a mixture of own and shared ones is not)
+  int same = 0;
+  for (int x = 0; x < e.n_arrays; ++x) same += e.src[x] == e.dst[x];
+  for (int x = 0; x < e.n_open; ++x) same += e.open_src[x] == e.open_dst[x];
+  same += (src->n_chunks == dst->n_chunks) + (src->m_partial == dst->m_partial) + (src->mass == dst->mass);
+  const int all = e.n_arrays + e.n_open + 3;
+  if (same != 0 && (same != all || src->max_chunks != dst->max_chunks))
+    return fail(HLA_ERR_INVALID_ARG, "dst shares %d of %d arrays with src (it is src itself, or has its own)", same,
+                all);
+  e.in_place = same != 0;
+  HLA_CUDA(hla::launch_evict(e, (cudaStream_t)stream), "evict launch");
+  return HLA_OK;
+}
+
+// Shape checks common to the calls on carried states.
+static hla_status check_gdn(const gdn_config* c) {
+  if (c == nullptr) return fail(HLA_ERR_INVALID_ARG, "cfg is NULL");
+  if (c->n_seq <= 0 || c->H <= 0 || c->Hk <= 0 || c->n_slots <= 0)
+    return fail(HLA_ERR_INVALID_ARG, "n_seq, Hk, H and n_slots must be positive (n_seq=%d Hk=%d H=%d n_slots=%d)",
+                c->n_seq, c->Hk, c->H, c->n_slots);
+  if (c->H % c->Hk != 0) return fail(HLA_ERR_INVALID_ARG, "Hk = %d does not divide H = %d", c->Hk, c->H);
+  if (c->dk != c->dv) return fail(HLA_ERR_UNSUPPORTED, "dk != dv (%d, %d) unsupported", c->dk, c->dv);
+  if (c->dk != 64 && c->dk != 128) return fail(HLA_ERR_UNSUPPORTED, "head dim %d unsupported (64, 128)", c->dk);
+  if (c->dtype != HLA_F32 && c->dtype != HLA_BF16) return fail(HLA_ERR_UNSUPPORTED, "dtype %d unsupported", c->dtype);
+  if (c->decay_mode != HLA_DECAY_SCALAR && c->decay_mode != HLA_DECAY_CHANNEL)
+    return fail(HLA_ERR_INVALID_ARG, "decay_mode %d invalid", c->decay_mode);
+  if ((double)c->n_seq * c->H * (c->dk / 16) >= 2147483647.0)
+    return fail(HLA_ERR_UNSUPPORTED, "too many sequences and heads");
+  return HLA_OK;
+}
+
+size_t gdn_workspace_bytes(const gdn_config* cfg, int32_t T) {
+  if (check_gdn(cfg) != HLA_OK || T <= 0) return 0;
+  return 256;
+}
+
+static hla_status gdn_run(const gdn_config* cfg, const void* q, const void* k, const void* v, const float* alpha,
+                          const float* beta, const int32_t* cu, int32_t T, const int32_t* slots,
+                          const float* state_in, float* state_out, void* o, cudaStream_t s) {
+  HLA_TRY(need_ptr(q, "q"));
+  HLA_TRY(need_ptr(k, "k"));
+  HLA_TRY(need_ptr(v, "v"));
+  // one value per token and head is read by itself: a view that starts at any token is fine
+  HLA_TRY(cfg->decay_mode == HLA_DECAY_CHANNEL ? need_ptr(alpha, "alpha") : need_ptr4(alpha, "alpha"));
+  HLA_TRY(need_ptr4(beta, "beta"));
+  HLA_TRY(need_ptr(o, "o"));
+  if (((uintptr_t)cu & 3u) != 0 || ((uintptr_t)slots & 3u) != 0)
+    return fail(HLA_ERR_INVALID_ARG, "cu_seqlens or slots misaligned");
+  if (slots == nullptr && cfg->n_slots < cfg->n_seq)
+    return fail(HLA_ERR_INVALID_ARG, "%d states for %d sequences and no slots", cfg->n_slots, cfg->n_seq);
+  hla::GdnArgs a{};
+  a.n_seq = cfg->n_seq;
+  a.Hk = cfg->Hk;
+  a.H = cfg->H;
+  a.d = cfg->dk;
+  a.dtype = cfg->dtype;
+  a.alpha_vec = cfg->decay_mode == HLA_DECAY_CHANNEL;
+  a.n_slots = cfg->n_slots;
+  a.T = T;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.alpha = alpha;
+  a.beta = beta;
+  a.cu = cu;
+  a.slots = slots;
+  a.state_in = state_in;
+  a.state_out = state_out;
+  a.o = o;
+  HLA_CUDA(hla::launch_gdn_recurrent(a, s), "gated delta rule launch");
+  return HLA_OK;
+}
+
+hla_status gdn_forward(const gdn_config* cfg, const void* q, const void* k, const void* v, const float* alpha,
+                       const float* beta, const int32_t* cu_seqlens, int32_t T, const int32_t* slots,
+                       const float* state_in, float* state_out, void* o, void* workspace, size_t workspace_bytes,
+                       hla_stream_t stream) {
+  g_msg[0] = 0;
+  HLA_TRY(check_gdn(cfg));
+  if (T <= 0) return fail(HLA_ERR_INVALID_ARG, "T must be positive (T=%d)", T);
+  if (cu_seqlens == nullptr) return fail(HLA_ERR_INVALID_ARG, "cu_seqlens is NULL");
+  HLA_TRY(opt_ptr(state_in, "state_in"));
+  HLA_TRY(opt_ptr(state_out, "state_out"));
+  HLA_TRY(need_ptr(workspace, "workspace"));
+  if (((uintptr_t)workspace & 255u) != 0) return fail(HLA_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+  const size_t need = gdn_workspace_bytes(cfg, T);
+  if (workspace_bytes < need) return fail(HLA_ERR_WORKSPACE, "workspace too small: %zu < %zu", workspace_bytes, need);
+  return gdn_run(cfg, q, k, v, alpha, beta, cu_seqlens, T, slots, state_in, state_out, o, (cudaStream_t)stream);
+}
+
+hla_status gdn_step(const gdn_config* cfg, const void* q, const void* k, const void* v, const float* alpha,
+                    const float* beta, const int32_t* slots, float* state, void* o, hla_stream_t stream) {
+  g_msg[0] = 0;
+  HLA_TRY(check_gdn(cfg));
+  HLA_TRY(need_ptr(state, "state"));
+  return gdn_run(cfg, q, k, v, alpha, beta, nullptr, cfg->n_seq, slots, state, state, o, (cudaStream_t)stream);
+}
+
 hla_status hla_prefill(const hla_config* cfg, const void* q, const void* k, const void* v, const float* alpha,
                        const float* beta, const void* q_route, const void* k_route, const float* user_gates,
                        void* o, float* gates_out, int32_t* active_idx_out, int32_t* active_cnt_out,
@@ -639,6 +843,8 @@ hla_status hla_prefill(const hla_config* cfg, const void* q, const void* k, cons
     HLA_TRY(check_cache(cfg, cache_out));
     if (cache_out->max_chunks < Nc)
       return fail(HLA_ERR_WORKSPACE, "cache holds %d chunks, prompt has %d", cache_out->max_chunks, Nc);
+    if (cache_out->mass != nullptr && gates_out == nullptr)
+      return fail(HLA_ERR_INVALID_ARG, "a cache whose mass is tracked needs gates_out");
   }
   const PrefillWs w = prefill_layout(cfg);
   HLA_TRY(need_ptr(workspace, "workspace"));
@@ -860,7 +1066,29 @@ hla_status hla_prefill(const hla_config* cfg, const void* q, const void* k, cons
     dc.n_chunks = cache_out->n_chunks;
     dc.m_partial = cache_out->m_partial;
     const bool factored = cache_out->format == HLA_CACHE_FACTORED;
-    StageScope _sc(HLA_STAGE_CACHE, s, factored ? 2 : 1);
+    const bool int8 = cache_out->format == HLA_CACHE_INT8;
+    StageScope _sc(HLA_STAGE_CACHE, s, 1 + (factored || int8) + (cache_out->mass != nullptr));
+    if (cache_out->mass != nullptr)
+      HLA_CUDA(hla::launch_gate_mass(gates_out, cfg->B, cfg->H, N, Nc, cfg->C, cfg->T, cfg->skip_threshold,
+                                     cache_out->mass, cache_out->max_chunks, s),
+               "gate mass launch");
+    if (int8) {
+      hla::Cache8Args c8{};
+      c8.B = cfg->B;
+      c8.H = cfg->H;
+      c8.C = cfg->C;
+      c8.d = cfg->dk;
+      c8.dtype = cfg->dtype;
+      c8.Nc = Nc;
+      c8.max_chunks = cache_out->max_chunks;
+      c8.A = A_chunk;
+      c8.Bm = B_chunk;
+      c8.src_stride = chunk_stride;
+      c8.qa = cache_out->A;
+      c8.qb = cache_out->Bm;
+      c8.scales = cache_out->df;
+      HLA_CUDA(hla::launch_cache8(c8, false, s), "8-bit cache fill launch");
+    }
     HLA_CUDA(hla::launch_cache_fill(dc, rk, qr, kr, k, v, alpha, beta, cfg->T, s), "cache fill launch");
     if (factored && Nc > 0) {
       hla::FactorFillArgs f{};
@@ -932,6 +1160,7 @@ hla_status hla_decode_step(const hla_config* cfg, hla_cache* cache, const void* 
   a.Wf = cache->Wf;
   a.Uf = cache->Uf;
   a.df = cache->df;
+  a.mass = cache->mass;
   a.rk = cache->rk;
   a.buf_k = cache->buf_k;
   a.buf_v = cache->buf_v;
@@ -945,6 +1174,10 @@ hla_status hla_decode_step(const hla_config* cfg, hla_cache* cache, const void* 
   a.act_idx = (int32_t*)workspace;
   a.act_g = (float*)((char*)workspace + align256(n * 4));
   a.act_cnt = (int32_t*)((char*)workspace + 2 * align256(n * 4));
+  if (cache->format == HLA_CACHE_INT8) {
+    a.scratch_A = (char*)a.act_cnt + align256((size_t)cfg->B * cfg->H * 4);
+    a.scratch_B = (char*)a.scratch_A + close_scratch_bytes(cfg);
+  }
   cudaStream_t s = (cudaStream_t)stream;
   {
     // the dense bf16 cache with d = 128 gates in one kernel and streams in another
@@ -953,7 +1186,7 @@ hla_status hla_decode_step(const hla_config* cfg, hla_cache* cache, const void* 
     HLA_CUDA(hla::launch_decode_main(a, s), "decode launch");
   }
   {
-    StageScope _sc(HLA_STAGE_DECODE_CLOSE, s, 3);
+    StageScope _sc(HLA_STAGE_DECODE_CLOSE, s, cache->format == HLA_CACHE_INT8 ? 4 : 3);
     HLA_CUDA(hla::launch_decode_close(a, s), "decode close launch");
   }
   return HLA_OK;
@@ -1089,10 +1322,17 @@ hla_status hla_device_status(int32_t clear, uint32_t* code_out) {
   word |= w;
   HLA_CUDA(hla::read_error_word_chan_prep(&w, clear != 0), "hla_device_status read");
   word |= w;
+  HLA_CUDA(hla::read_error_word_gdn_recurrent(&w, clear != 0), "hla_device_status read");
+  word |= w;
   if (code_out) *code_out = word;
   if (word & (hla::kErrMbarTimeout | hla::kErrTmemAlloc))
     return fail(HLA_ERR_TIMEOUT, "a bounded device wait expired (code 0x%x)", word);
   if (word & hla::kErrCacheFull) return fail(HLA_ERR_WORKSPACE, "a decode step found the cache full (code 0x%x)", word);
+  if (word & hla::kErrBadIndex)
+    return fail(HLA_ERR_INVALID_ARG,
+                "a gated delta rule call left a sequence out: its bounds are not within the tokens, or its state "
+                "slot is outside the states or an earlier sequence's (code 0x%x)",
+                word);
   if (word & hla::kErrDecayRange)
     return fail(HLA_ERR_UNSUPPORTED,
                 "a channel decayed below e^-80 within one 64-token sub-chunk: outside the range of the "

@@ -52,6 +52,7 @@ struct TransArgs {
   float* ell;            // [B,H,N,C] fp32 or null
   const int32_t* close_m;   // decode close: per-b m_partial (before the step) or null
   const int32_t* close_n;   // decode close: per-b n_chunks or null
+  int close_scratch;        // decode close: A/B of (b, h) to matrix b * H + h (ab_chunk_stride 1)
   // decode close into a factored cache: K, Wb, Ub ([.., chunk_stride, C, d]) and the
   // scales ([.., chunk_stride, C + 4]) of the closed chunk instead of A/B
   void* Kf;
@@ -175,10 +176,13 @@ struct DecodeArgs {
   const void* A;
   const void* Bm;
   int format;          // hla_cache_format
+  float* mass;         // [B,H,max_chunks] accumulated gate weight, or null
+  void* scratch_A;     // 8-bit cache: [B,H,d,d] (dtype), the closing chunk's transition
+  void* scratch_B;
   void* Kf;            // factored: [B,H,max_chunks,C,d]
   void* Wf;
   void* Uf;
-  float* df;           // factored: [B,H,max_chunks,C+4]
+  float* df;           // factored: [B,H,max_chunks,C+4]; 8-bit: [B,H,max_chunks,4]
   float* rk;           // [B,H,max_chunks,max(win,1),d]
   void* buf_k;
   void* buf_v;
@@ -192,6 +196,56 @@ struct DecodeArgs {
   int32_t* act_idx;  // [B,H,max_chunks]
   float* act_g;      // [B,H,max_chunks]
   int32_t* act_cnt;  // [B,H]: length of each active list (dense-cache streaming kernels)
+};
+
+// Chunk transitions into an 8-bit cache: the prefill hand-off (every complete chunk of
+// A, Bm [B,H,src_stride,d,d]) or the decode close (A, Bm [B,H,d,d]).
+struct Cache8Args {
+  int B, H, C, d, dtype, Nc, max_chunks;
+  const void* A;          // (dtype)
+  const void* Bm;
+  long src_stride;
+  void* qa;               // [B,H,max_chunks,d,d] int8
+  void* qb;
+  float* scales;          // [B,H,max_chunks,4]: mean diagonal of A, scale of A, scale of B, 0
+  const int32_t* close_m; // decode close
+  const int32_t* close_n;
+};
+
+// Eviction of cached chunks: every array's chunks [B,H,src_chunks] -> [B,H,dst_chunks].
+struct EvictArgs {
+  int B, H, src_chunks, dst_chunks, keep, recent;
+  bool in_place;
+  const float* mass;      // [B,H,src_chunks]
+  float* mass_dst;        // [B,H,dst_chunks] or null
+  int32_t* kept;          // [B,H,keep]
+  const int32_t* n_src;   // [B]
+  int32_t* n_dst;
+  const int32_t* m_src;
+  int32_t* m_dst;
+  int n_arrays;           // per-chunk arrays (bytes per chunk, multiples of 16)
+  const void* src[5];
+  void* dst[5];
+  long chunk_bytes[5];
+  int n_open;             // open-chunk arrays (bytes per (sequence, head)), other cache only
+  const void* open_src[6];
+  void* open_dst[6];
+  long open_bytes[6];
+};
+
+// The gated delta rule with a carried state (float32 [n_slots,H,d,d], [v][k]).
+struct GdnArgs {
+  int n_seq, Hk, H, d, dtype, alpha_vec, n_slots, T;
+  const void* q;          // [T,Hk,d]
+  const void* k;
+  const void* v;          // [T,H,d]
+  const float* alpha;     // [T,H] or [T,H,d]
+  const float* beta;      // [T,H]
+  const int32_t* cu;      // [n_seq+1] or null (token i belongs to sequence i)
+  const int32_t* slots;   // [n_seq] or null (state i belongs to sequence i)
+  const float* state_in;  // or null (zero)
+  float* state_out;       // or null
+  void* o;                // [T,H,d]
 };
 
 cudaError_t launch_pools(const void* x0, const void* x1, float* r0, float* r1, int B, int T, int H, int d,
@@ -229,6 +283,12 @@ cudaError_t launch_transitions_token(const TransArgs& a, cudaStream_t s);
 cudaError_t launch_readout_token(const ReadoutTokenArgs& a, cudaStream_t s);
 cudaError_t launch_gate_support(const float* gates, int B, int H, int N, float thr, float* mass_out,
                                 float* support_out, cudaStream_t s);
+cudaError_t launch_gate_mass(const float* gates, int B, int H, int N, int ncols, int C, int T, float thr, float* mass,
+                             long mass_stride, cudaStream_t s);
+cudaError_t launch_evict(const EvictArgs& a, cudaStream_t s);
+cudaError_t launch_cache8(const Cache8Args& a, bool close, cudaStream_t s);
+cudaError_t launch_gdn_recurrent(const GdnArgs& a, cudaStream_t s);
+cudaError_t read_error_word_gdn_recurrent(unsigned int* out, bool clear);
 cudaError_t launch_wait_check(uint64_t limit_ns, bool complete, cudaStream_t s);
 
 }  // namespace hla

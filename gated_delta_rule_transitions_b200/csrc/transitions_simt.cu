@@ -47,7 +47,7 @@ __global__ void __launch_bounds__(256) transitions_simt_kernel(TransArgs a) {
   if (a.close_m != nullptr) {
     // decode close: only sequences whose open chunk becomes full this step
     if (a.close_m[b] + 1 != C) return;
-    chunk_out = a.close_n[b];
+    chunk_out = a.close_scratch ? 0 : a.close_n[b];
     if (chunk_out >= a.ab_chunk_stride) return;  // cache full (flagged by the pool kernel)
   }
   const int t0 = c * C;

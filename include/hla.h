@@ -104,11 +104,20 @@ typedef enum { HLA_DECAY_SCALAR = 0, HLA_DECAY_CHANNEL = 1 } hla_decay_mode;
 /* Storage of the closed chunks' transitions in a decode cache. */
 typedef enum {
   HLA_CACHE_DENSE = 0,    /* A_j, B_j as d x d matrices (2 d^2 elements per chunk)        */
-  HLA_CACHE_FACTORED = 1  /* the WY factors K_j, Wb_j, Ub_j (C x d each) and D_j, gamma_C:
+  HLA_CACHE_FACTORED = 1, /* the WY factors K_j, Wb_j, Ub_j (C x d each) and D_j, gamma_C:
                              A_j = gamma_C I - Wb_j^T D_j K_j, B_j = Ub_j^T D_j K_j
                              (3 C d elements; 25 % fewer bytes at C = 64, d = 128).
                              bf16 with d = 128 and C = 64 only (above C = 2d/3 the
                              factors are larger than A_j, B_j). */
+  HLA_CACHE_INT8 = 2      /* A_j, B_j in 8 bits with scales per chunk and head:
+                             A_j ~ a_j I + sA_j QA_j, B_j ~ sB_j QB_j, QA and QB d x d
+                             int8 codes in [-127, 127], a_j the mean of A_j's diagonal,
+                             a scale the largest magnitude / 127 (so an entry is off by
+                             at most half a scale): half of the bf16 bytes, a quarter
+                             of the float32 ones.  Every dtype, head dim, chunk size,
+                             window and decay.  Only what is read back later is in 8
+                             bits: a prefill composes its own prompt from the unrounded
+                             transitions. */
 } hla_cache_format;
 
 typedef struct hla_config {
@@ -138,16 +147,20 @@ typedef struct hla_config {
  * Decode cache of B sequences (all pointers are device memory carved out of one
  * caller-owned block by hla_cache_init):
  *   A, Bm        [B, H, max_chunks, d, d]  dtype  -- transitions of closed chunks
- *                (HLA_CACHE_DENSE; NULL otherwise)
+ *                (HLA_CACHE_DENSE; HLA_CACHE_INT8: the int8 codes QA, QB; NULL otherwise)
  *   Kf, Wf, Uf   [B, H, max_chunks, C, d]  dtype  -- K_j, Wb_j, Ub_j of closed chunks
  *   df           [B, H, max_chunks, C + 4] float32 -- gamma_C / gamma_t (t < C), then
- *                gamma_C, then padding (HLA_CACHE_FACTORED; all NULL otherwise)
+ *                gamma_C, then padding (HLA_CACHE_FACTORED).  HLA_CACHE_INT8:
+ *                df is [B, H, max_chunks, 4]: a_j, sA_j, sB_j, 0 (Kf, Wf, Uf NULL).
+ *                NULL otherwise
  *   rk           [B, H, max_chunks, W, d]  float32 -- key pools of closed chunks (W = 1,
  *                or C / pool_window window pools)
  *   buf_k, buf_v, buf_qr, buf_kr  [B, H, C, d] dtype -- tokens of the open chunk
  *   buf_alpha, buf_beta           [B, H, C]  float32 (buf_alpha [B, H, C, d] if CHANNEL)
  *   n_chunks     [B] int32 -- closed chunks per sequence
  *   m_partial    [B] int32 -- tokens in the open chunk (0 .. C-1 between calls)
+ *   mass         [B, H, max_chunks] float32 or NULL -- accumulated gate weight of the
+ *                closed chunks (caller-owned, see hla_cache_track_mass)
  * The cache is the resumable decode state ("Main Findings": per-chunk affine
  * states replace the KV cache): A/B take 2 d^2 elements per closed chunk.
  */
@@ -172,6 +185,7 @@ typedef struct hla_cache {
   float* buf_beta;
   int32_t* n_chunks;
   int32_t* m_partial;
+  float* mass;
 } hla_cache;
 
 /* Message for the last non-OK status returned on this thread ("" if none). */
@@ -193,6 +207,14 @@ hla_status hla_cache_init(const hla_config* cfg, int32_t max_chunks, void* mem, 
  * prefilled one at a time into one cache, after which hla_decode_step advances
  * them together from their own positions.  Errors: INVALID_ARG. */
 hla_status hla_cache_slice(const hla_cache* cache, int32_t b0, int32_t nb, hla_cache* out);
+
+/* Track the gate weight that every closed chunk of the cache carries: sets cache->mass
+ * to mass (device, [B, H, max_chunks] float32, caller-owned, kept as long as the cache is
+ * used) and enqueues its zeroing on stream.  From then on hla_decode_step adds the gate of
+ * every chunk it keeps, a chunk that closes starts at 0, and hla_prefill into the cache
+ * (which then needs gates_out) writes hla_gate_mass of the prompt.  mass == NULL stops
+ * tracking.  Errors: INVALID_ARG, CUDA. */
+hla_status hla_cache_track_mass(hla_cache* cache, float* mass, hla_stream_t stream);
 
 /* Workspace bytes that hla_prefill needs for cfg (0 for an unsupported config). */
 size_t hla_prefill_workspace_bytes(const hla_config* cfg);
@@ -252,6 +274,87 @@ hla_status hla_gate_support(const hla_config* cfg, const float* gates, float* ma
                             hla_stream_t stream);
 
 /*
+ * hla_gate_mass -- weight that every chunk has carried over a prompt (Methodology para. 4:
+ * a chunk's weight decides whether it is read at all).  Over the query chunks i > j kept by
+ * cfg->skip_threshold, each standing for its n_i tokens (n_i = C; the last chunk T - iC):
+ *   mass_j = sum_{i > j} n_i g_ij.
+ * In:  gates [B,H,N,N] float32 (device), N = ceil(T/C), as written by hla_routing or
+ *      hla_prefill; only entries j < i are read.
+ * Out: mass_out [B,H,N] float32 (device); the last entry is 0.
+ * float32 sums in a fixed order (the same bits every time).
+ * Errors: INVALID_ARG, UNSUPPORTED, CUDA.
+ */
+hla_status hla_gate_mass(const hla_config* cfg, const float* gates, float* mass_out, hla_stream_t stream);
+
+/*
+ * hla_cache_evict -- bound a cache: per (sequence, head) keep the chunks that matter
+ * (Methodology para. 4: leaving a chunk out is exact, it acts as the identity).
+ * A sequence with n_chunks <= keep keeps all.  Otherwise each of its heads keeps the
+ * `recent` last chunks and, of the others, the keep - recent with the largest src->mass
+ * (equal weights: the lower index stays; a NaN counts as the least), in their order.
+ * dst may be src (the chunks move up in place) or another cache of the same config with
+ * memory of its own and max_chunks >= keep (a smaller serving cache, say): then the open
+ * chunk and the counters are copied too.  dst->mass, where it is tracked, gets the kept
+ * chunks' weights.  Entries of dst beyond the kept chunks are left as they were.
+ * In:  src (its mass must be tracked), keep in [1, dst->max_chunks], recent in [0, keep].
+ * Out: kept_out [B,H,keep] int32 (device): the kept chunks' old indices, ascending, then -1.
+ * Any cache format.  Deterministic, no workspace.
+ * Errors: INVALID_ARG, UNSUPPORTED, CUDA.
+ */
+hla_status hla_cache_evict(const hla_config* cfg, const hla_cache* src, hla_cache* dst, int32_t keep,
+                           int32_t recent, int32_t* kept_out, hla_stream_t stream);
+
+/*
+ * The gated delta rule itself (Methodology para. 1), with a state that is carried from
+ * call to call instead of a cache of chunk transitions: what a native Gated DeltaNet layer
+ * serves from, and what HLA reduces to with every gate one.  Per sequence and head
+ *   S <- S Diag(alpha_t);  u_t = beta_t (v_t - S k_t);  S <- S + u_t k_t^T;  o_t = S q_t.
+ * Key/query heads may be fewer than value heads: value head h uses key head h / (H / Hk).
+ * States are float32 [n_slots, H, d_v, d_k]; sequence i uses slot slots[i] (NULL: slot i).
+ * A negative slot marks padding of a batch: that entry is left out, its outputs and state
+ * stay as they were.  A slot >= n_slots, a slot that an earlier sequence of the call has,
+ * or sequence bounds that fall or leave [0, T] leave that sequence out too and record code
+ * 0x10, reported by hla_device_status.
+ */
+typedef struct gdn_config {
+  int32_t n_seq;      /* sequences of the call                            */
+  int32_t Hk, H;      /* key/query heads and value heads; Hk divides H    */
+  int32_t dk, dv;     /* head dims, equal, 64 or 128                      */
+  int32_t dtype;      /* hla_dtype of q, k, v, o                          */
+  int32_t decay_mode; /* hla_decay_mode                                   */
+  int32_t n_slots;    /* states in the state arrays                       */
+} gdn_config;
+
+/* Workspace bytes that gdn_forward needs for T tokens (0 for an unsupported config; some
+ * configs need none and get 256). */
+size_t gdn_workspace_bytes(const gdn_config* cfg, int32_t T);
+
+/*
+ * gdn_forward -- ragged sequences of any length through the rule, states in and out.
+ * In:  q, k [T,Hk,d], v [T,H,d] dtype; alpha [T,H] (CHANNEL: [T,H,d]) and beta [T,H]
+ *      float32, alpha in [0,1] (these two, where scalar, only 4-byte aligned); cu_seqlens [n_seq + 1] int32 (device): sequence i is rows
+ *      cu_seqlens[i] .. cu_seqlens[i+1] - 1 (an empty one passes its state on);
+ *      slots [n_seq] int32 (device) or NULL; state_in or NULL (zero states).
+ * Out: o [T,H,d] dtype (rows of no sequence are left as they were); state_out or NULL.
+ *      state_out may be state_in; otherwise the two must not overlap.
+ * workspace: device, >= gdn_workspace_bytes(cfg, T), 256-byte aligned.
+ * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, CUDA.
+ */
+hla_status gdn_forward(const gdn_config* cfg, const void* q, const void* k, const void* v, const float* alpha,
+                       const float* beta, const int32_t* cu_seqlens, int32_t T, const int32_t* slots,
+                       const float* state_in, float* state_out, void* o, void* workspace,
+                       size_t workspace_bytes, hla_stream_t stream);
+
+/*
+ * gdn_step -- one token per sequence, the states updated in place (decode).
+ * In:  q, k [n_seq,Hk,d], v [n_seq,H,d] dtype; alpha [n_seq,H] (CHANNEL: [n_seq,H,d]) and
+ *      beta [n_seq,H] float32; slots [n_seq] int32 (device) or NULL.
+ * In/out: state.  Out: o [n_seq,H,d] dtype.  Errors: INVALID_ARG, UNSUPPORTED, CUDA.
+ */
+hla_status gdn_step(const gdn_config* cfg, const void* q, const void* k, const void* v, const float* alpha,
+                    const float* beta, const int32_t* slots, float* state, void* o, hla_stream_t stream);
+
+/*
  * hla_prefill -- HLA over a whole prompt (Key Contributions 3; Methodology paras. 1-4).
  * In:  q, k, v [B,T,H,d] dtype; alpha, beta [B,T,H] float32;
  *      q_route, k_route [B,T,H,d] dtype or NULL (NULL: q, k);
@@ -259,7 +362,8 @@ hla_status hla_gate_support(const hla_config* cfg, const float* gates, float* ma
  * Out: o [B,T,H,d] dtype.  Optional (NULL to skip): gates_out, active_idx_out,
  *      active_cnt_out as in hla_routing; cache_out -- an initialised cache with
  *      max_chunks >= T/C, filled with A/B/rk of every complete chunk, the final
- *      partial chunk's tokens and the counters.
+ *      partial chunk's tokens and the counters (and, where its mass is tracked, the
+ *      weight that each chunk carried over the prompt: gates_out must be given then).
  * workspace: device, >= hla_prefill_workspace_bytes(cfg), 256-byte aligned.
  * Path: routing on a library side stream (forked from and joined back to `stream`
  * by events) beside the chunk transitions; then the composition and the read-out.
@@ -343,7 +447,8 @@ hla_status hla_decode_step_static(const hla_config* cfg, hla_cache* cache, const
  * hla_device_status synchronises the device, reads and (if clear != 0) resets that
  * word; it returns HLA_ERR_TIMEOUT if a wait expired since the last reset (code bit
  * 0x1, or 0x2 for a tensor-memory allocation), HLA_ERR_WORKSPACE if a decode step
- * found its cache full (0x4), HLA_ERR_UNSUPPORTED if a prefill with a decay per
+ * found its cache full (0x4), HLA_ERR_INVALID_ARG if a gdn_forward or gdn_step left a
+ * sequence out for its bounds or its state slot (0x10), HLA_ERR_UNSUPPORTED if a prefill with a decay per
  * channel left the tensor-core range described at hla_prefill (0x8), else HLA_OK (or
  * HLA_ERR_CUDA).  *code_out (may be NULL) receives the raw word.
  */

@@ -1,0 +1,279 @@
+"""The gated delta rule with a carried state (gdn_step, gdn_forward) against its definition
+in 64 bits.
+
+Tolerances.  Every token's update of a state row is a float32 dot product of d terms and a
+rank-one correction: with d / 8 terms in sequence and a handful of operations more it is off
+by less than (d / 8 + 8) 2^-24 of the row's size, and the rule contracts what it carries, so
+T tokens add up to at most min(T, 64) such errors (alpha averages 0.95: an error's weight
+after 64 tokens is below 4 %).  The tensor-core form (bf16, d = 128) holds each factor of its
+products as two bf16 numbers: each product is off by at most 2 x 2^-17 relative, at most six
+products stand between a state and the next, which makes 12 x 2^-17 = 9.2e-5 as the bound for
+one chunk if every error pointed the same way; rounding errors of independent elements add as
+their root, so 2e-5 is asked for.  An output is rounded once to its type on top."""
+import pytest
+import torch
+
+from tests import _serving as R
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def hla():
+    import gated_delta_rule_transitions_b200 as m
+    m.lib()
+    return m._hla
+
+
+def state_tol(T, d, dtype, chunked):
+    f32 = min(T, 64) * (d / 8 + 8) * 2.0 ** -24
+    return max(f32, 2e-5) if chunked else f32
+
+
+def cuda(*xs):
+    return [x.cuda() for x in xs]
+
+
+@pytest.mark.parametrize("n,Hk,H,d,dtype,channel", [
+    (1, 1, 1, 128, "bf16", False), (1, 16, 16, 128, "bf16", False), (5, 2, 6, 128, "f32", False),
+    (3, 1, 3, 64, "bf16", True), (40, 4, 16, 128, "bf16", True), (41, 8, 8, 64, "f32", False),
+    (2, 2, 2, 128, "f32", True), (70, 2, 4, 64, "f32", True),
+])
+def test_step(hla, n, Hk, H, d, dtype, channel):
+    gen = torch.Generator().manual_seed(n * 1000 + H)
+    dt = R.DT[dtype]
+    q, k, v, al, be = R.tokens(gen, n, Hk, H, d, dt, channel)
+    S0 = 0.3 * torch.randn(n, H, d, d, generator=gen)
+    cfg = hla.make_gdn_config(n, H, d, dtype, Hk=Hk, decay="channel" if channel else "scalar")
+    S, o = S0.cuda(), torch.zeros(n, H, d, dtype=dt, device="cuda")
+    hla.gdn_step(cfg, *cuda(q, k, v, al, be), S, o)
+    ro, rS = R.gdn_reference(q, k, v, al, be, [(i, i + 1) for i in range(n)], S0)
+    tol = state_tol(1, d, dt, False)
+    assert R.rel(S.cpu(), rS) <= tol
+    assert R.rel(o.cpu(), ro) <= tol + R.half_step(dt)
+    assert hla.hla_device_status() == (0, 0)
+
+
+LENS = [[1], [63], [64], [65], [130], [1, 0, 64, 3, 127, 128, 129, 0, 40], [0, 5], [333, 2], [200] * 3]
+
+
+@pytest.mark.parametrize("lens", LENS, ids=str)
+@pytest.mark.parametrize("Hk,H,d,dtype,channel", [
+    (2, 4, 128, "bf16", False), (1, 1, 128, "bf16", False), (2, 2, 128, "bf16", True), (1, 3, 64, "bf16", False),
+    (2, 2, 128, "f32", False), (1, 2, 64, "f32", True),
+])
+def test_forward(hla, lens, Hk, H, d, dtype, channel):
+    gen = torch.Generator().manual_seed(sum(lens) * 7 + H)
+    dt, T, n = R.DT[dtype], sum(lens) + 3, len(lens)  # three rows belong to no sequence
+    q, k, v, al, be = R.tokens(gen, T, Hk, H, d, dt, channel)
+    # what stands behind the last sequence is no number
+    for x in (q, k, v, al, be):
+        x[sum(lens):] = float("nan")
+    cu = torch.tensor([0] + lens).cumsum(0).to(torch.int32)
+    slots = torch.randperm(n + 2, generator=gen)[:n].to(torch.int32)
+    S0 = 0.3 * torch.randn(n + 2, H, d, d, generator=gen)
+    cfg = hla.make_gdn_config(n, H, d, dtype, Hk=Hk, n_slots=n + 2, decay="channel" if channel else "scalar")
+    o = torch.full((T, H, d), 7.0, dtype=dt, device="cuda")
+    Sin, Sout = S0.cuda(), torch.full((n + 2, H, d, d), 5.0, device="cuda")
+    dev = cuda(q, k, v, al, be, cu)
+    hla.gdn_forward(cfg, *dev, o, state_in=Sin, state_out=Sout, slots=slots.cuda())
+    bounds = [(int(cu[i]), int(cu[i + 1])) for i in range(n)]
+    ro, rS = R.gdn_reference(q, k, v, al, be, bounds, S0[slots.long()])
+    tol = state_tol(max(lens), d, dt, dtype == "bf16" and d == 128 and not channel)
+    got = Sout.cpu()
+    for i, s in enumerate(slots.tolist()):
+        if lens[i] == 0:
+            assert torch.equal(got[s], S0[s])
+        else:
+            assert R.rel(got[s], rS[i]) <= tol, (i, lens[i])
+    other = [s for s in range(n + 2) if s not in slots.tolist()]
+    assert torch.equal(got[other], torch.full_like(got[other], 5.0))
+    end = sum(lens)
+    for i, (a, e) in enumerate(bounds):
+        if e > a:
+            assert R.rel(o[a:e].cpu(), ro[a:e]) <= tol + R.half_step(dt), (i, lens[i])
+    assert torch.equal(o[end:].cpu(), torch.full_like(o[end:].cpu(), 7.0))
+    # in place, twice: the same bits both times
+    again = []
+    for _ in range(2):
+        S, o2 = S0.cuda(), torch.full_like(o, 7.0)
+        hla.gdn_forward(cfg, *dev, o2, state_in=S, state_out=S, slots=slots.cuda())
+        again.append((S, o2))
+        assert torch.equal(S[slots.long()], Sout[slots.long()]) and torch.equal(o2, o)
+    assert torch.equal(again[0][0], again[1][0])
+    assert hla.hla_device_status() == (0, 0)
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("f32", 64)])
+def test_zero_state_and_no_state_out(hla, dtype, d):
+    gen = torch.Generator().manual_seed(3)
+    dt, T, H = R.DT[dtype], 150, 2
+    args = cuda(*R.tokens(gen, T, H, H, d, dt))
+    cu = torch.tensor([0, 70, 150], dtype=torch.int32, device="cuda")
+    cfg = hla.make_gdn_config(2, H, d, dtype)
+    zero = torch.zeros(2, H, d, d, device="cuda")
+    o1, o2, S = torch.empty_like(args[2]), torch.empty_like(args[2]), torch.empty_like(zero)
+    hla.gdn_forward(cfg, *args, cu, o1, state_in=zero, state_out=S)
+    hla.gdn_forward(cfg, *args, cu, o2)
+    assert torch.equal(o1, o2)
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("f32", 128), ("bf16", 64)])
+def test_split_prompt_and_steps_agree_with_one_call(hla, dtype, d):
+    """A prompt in pieces (state carried by the caller), then token by token: the same
+    states as in one call."""
+    gen = torch.Generator().manual_seed(11)
+    dt, T, H = R.DT[dtype], 229, 3
+    q, k, v, al, be = cuda(*R.tokens(gen, T, H, H, d, dt))
+    cfg = hla.make_gdn_config(1, H, d, dtype)
+    bounds = lambda n: torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    o, S = torch.empty_like(v), torch.zeros(1, H, d, d, device="cuda")
+    hla.gdn_forward(cfg, q, k, v, al, be, bounds(T), o, state_in=S, state_out=S)
+    o2, S2 = torch.empty_like(v), torch.zeros(1, H, d, d, device="cuda")
+    for a, e in ((0, 100), (100, 101), (101, 220)):
+        part = o2[a:e].contiguous()
+        hla.gdn_forward(cfg, *(x[a:e].contiguous() for x in (q, k, v, al, be)), bounds(e - a), part, state_in=S2,
+                        state_out=S2)
+        o2[a:e] = part
+    for t in range(220, T):
+        hla.gdn_step(cfg, *(x[t:t + 1].contiguous() for x in (q, k, v, al, be)), S2, o2[t:t + 1])
+    tol = 2 * state_tol(T, d, dt, dtype == "bf16" and d == 128)
+    assert R.rel(S2, S) <= tol
+    assert R.rel(o2, o) <= tol + 2 * R.half_step(dt)
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("f32", 64)])
+def test_padding_bad_slots_and_bad_bounds_are_left_out(hla, dtype, d):
+    """Slots below zero are padding; a slot out of range or twice, and bounds outside the
+    tokens, leave their sequence out and are reported; the others are not touched by it."""
+    gen = torch.Generator().manual_seed(5)
+    dt, H, n = R.DT[dtype], 2, 6
+    q, k, v, al, be = R.tokens(gen, n, H, H, d, dt)
+    S0 = torch.randn(4, H, d, d, generator=gen)
+    slots = torch.tensor([2, -1, 0, 2, 9, 1], dtype=torch.int32)  # 3: slot twice, 4: out of range
+    cfg = hla.make_gdn_config(n, H, d, dtype, n_slots=4)
+    S, o = S0.cuda(), torch.full((n, H, d), 7.0, dtype=dt, device="cuda")
+    hla.gdn_step(cfg, *cuda(q, k, v, al, be), S, o, slots=slots.cuda())
+    st, code = hla.hla_device_status()
+    assert st == hla.HLA_ERR_INVALID_ARG and code == 16
+    good = [0, 2, 5]
+    ro, rS = R.gdn_reference(*(x[good] for x in (q, k, v, al, be)), [(i, i + 1) for i in range(3)],
+                             S0[slots[good].long()])
+    tol = state_tol(1, d, dt, False)
+    assert R.rel(S.cpu()[slots[good].long()], rS) <= tol and torch.equal(S.cpu()[3], S0[3])
+    assert R.rel(o.cpu()[good], ro) <= tol + R.half_step(dt)
+    assert torch.equal(o.cpu()[[1, 3, 4]], torch.full((3, H, d), 7.0, dtype=dt))
+    # bounds: the second sequence's run backwards, the third's leave the tokens
+    T = 200
+    q, k, v, al, be = R.tokens(gen, T, H, H, d, dt)
+    cu = torch.tensor([0, 120, 90, 150, 300], dtype=torch.int32)
+    cfg = hla.make_gdn_config(4, H, d, dtype)
+    S, o = S0.cuda(), torch.full((T, H, d), 7.0, dtype=dt, device="cuda")
+    hla.gdn_forward(cfg, *cuda(q, k, v, al, be, cu), o, state_in=S, state_out=S)
+    st, code = hla.hla_device_status()
+    assert st == hla.HLA_ERR_INVALID_ARG and code == 16
+    ro, rS = R.gdn_reference(q, k, v, al, be, [(0, 120)], S0[:1])
+    tol = state_tol(120, d, dt, dtype == "bf16" and d == 128)
+    assert R.rel(S.cpu()[:1], rS) <= tol and torch.equal(S.cpu()[[1, 3]], S0[[1, 3]])
+    assert R.rel(o.cpu()[:90], ro[:90]) <= tol + R.half_step(dt)
+    assert torch.equal(o.cpu()[150:], torch.full((50, H, d), 7.0, dtype=dt))
+    assert hla.hla_device_status() == (0, 0)
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("f32", 64)])
+def test_extreme_decays_and_writes(hla, dtype, d):
+    """Decays of exactly one, exactly zero and far below; writes of zero and one."""
+    gen = torch.Generator().manual_seed(8)
+    dt, T, H = R.DT[dtype], 140, 2
+    q, k, v, al, be = R.tokens(gen, T, H, H, d, dt)
+    al[::3], be[::5], be[1::5] = 1.0, 0.0, 1.0
+    al[40], al[41], al[100, 0], al[130] = 0.0, 1e-30, 1e-3, 0.5
+    cu = torch.tensor([0, T], dtype=torch.int32)
+    S0 = torch.randn(1, H, d, d, generator=gen)
+    cfg = hla.make_gdn_config(1, H, d, dtype)
+    S, o = S0.cuda(), torch.empty(T, H, d, dtype=dt, device="cuda")
+    hla.gdn_forward(cfg, *cuda(q, k, v, al, be, cu), o, state_in=S, state_out=S)
+    ro, rS = R.gdn_reference(q, k, v, al, be, [(0, T)], S0)
+    tol = state_tol(T, d, dt, dtype == "bf16" and d == 128)
+    assert R.rel(S.cpu(), rS) <= tol and R.rel(o.cpu(), ro) <= tol + R.half_step(dt)
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("f32", 64)])
+def test_repeated_keys(hla, dtype, d):
+    """Every token writes to the same key (the triangular system at its stiffest)."""
+    gen = torch.Generator().manual_seed(9)
+    dt, T, H = R.DT[dtype], 192, 1
+    q, k, v, al, be = R.tokens(gen, T, H, H, d, dt)
+    k[:] = k[:1]
+    be[:] = 0.95
+    al[:] = 0.999
+    cu = torch.tensor([0, T], dtype=torch.int32)
+    S0 = torch.randn(1, H, d, d, generator=gen)
+    cfg = hla.make_gdn_config(1, H, d, dtype)
+    S, o = S0.cuda(), torch.empty(T, H, d, dtype=dt, device="cuda")
+    hla.gdn_forward(cfg, *cuda(q, k, v, al, be, cu), o, state_in=S, state_out=S)
+    ro, rS = R.gdn_reference(q, k, v, al, be, [(0, T)], S0)
+    tol = state_tol(T, d, dt, dtype == "bf16" and d == 128)
+    assert R.rel(S.cpu(), rS) <= tol and R.rel(o.cpu(), ro) <= tol + R.half_step(dt)
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("f32", 64)])
+def test_captured_and_side_stream(hla, dtype, d):
+    """Captured into a graph and replayed on new inputs, and on a stream of its own."""
+    gen = torch.Generator().manual_seed(21)
+    dt, T, H = R.DT[dtype], 300, 2
+    toks = [cuda(*R.tokens(gen, T, H, H, d, dt)) for _ in range(2)]
+    cu = torch.tensor([0, 130, 300], dtype=torch.int32, device="cuda")
+    cfg = hla.make_gdn_config(2, H, d, dtype)
+    ws = torch.empty(hla.gdn_workspace_bytes(cfg, T), dtype=torch.uint8, device="cuda")
+
+    def eager(tok):
+        S, o = torch.zeros(2, H, d, d, device="cuda"), torch.empty_like(tok[2])
+        hla.gdn_forward(cfg, *tok, cu, o, state_out=S, workspace=ws)
+        o1 = torch.empty_like(tok[2][:2])
+        hla.gdn_step(cfg, *(x[:2].contiguous() for x in tok), S, o1)
+        return o, S, o1
+
+    want = [eager(t) for t in toks]
+    torch.cuda.synchronize()
+    buf = [x.clone() for x in toks[0]]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = eager(buf)
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want[0]))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = eager(buf)
+    for i in (1, 0):
+        for b, x in zip(buf, toks[i]):
+            b.copy_(x)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want[i]))
+
+
+def test_two_calls_on_two_streams(hla):
+    """Two calls at once, each with a workspace and states of its own."""
+    gen = torch.Generator().manual_seed(4)
+    T, H, d = 700, 4, 128
+    cfg = hla.make_gdn_config(1, H, d, "bf16")
+    toks = [cuda(*R.tokens(gen, T, H, H, d, R.BF16)) for _ in range(2)]
+    cu = torch.tensor([0, T], dtype=torch.int32, device="cuda")
+
+    def call(tok, stream=None):
+        S, o = torch.zeros(1, H, d, d, device="cuda"), torch.empty_like(tok[2])
+        ws = torch.empty(hla.gdn_workspace_bytes(cfg, T), dtype=torch.uint8, device="cuda")
+        torch.cuda.synchronize()
+        for _ in range(3):
+            hla.gdn_forward(cfg, *tok, cu, o, state_out=S, workspace=ws, stream=stream)
+        return o, S, ws
+
+    want = [call(t) for t in toks]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [call(t, s) for t, s in zip(toks, streams)]
+    torch.cuda.synchronize()
+    for g, w in zip(got, want):
+        assert torch.equal(g[0], w[0]) and torch.equal(g[1], w[1])
