@@ -622,6 +622,156 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (tid == 0 && *abort_s) report_device_error(kErrMbarTimeout);
 }
 
+// ---------------------------------------------------------------------------------
+// 8-bit cache (A_j ~ a_j I + sA QA, B_j ~ sB QB, int8 codes): the chain's two products
+// in whole numbers.  The running x is held in float32; before each chunk it is written
+// as a fixed-point number of 24 bits relative to its largest entry,
+//   x_c = 2^(e - 22) N_c,  |N_c| <= 2^22,  N_c = d0 + 2^8 d1 + 2^16 d2  (signed bytes),
+// so that QA x and QB x are three exact dot products of bytes each (dp4a, 32-bit sums:
+// at most 128 x 127 x 128 < 2^21) and the only error beside float32's own is the fixed
+// point's half unit, 2^-23 of the largest entry.  That is 0.75 instructions a stored
+// value and no conversion, against two and a half (convert, multiply-add) in float32,
+// which would not keep up with HBM.
+//
+// A unit of the ring is one chunk: 16 KiB of QA, 16 KiB of QB (128 rows of 128 bytes, one
+// 128-byte-swizzled box each) and its four scales; thread = row.
+constexpr int kU8Tile = kD * kD;                    // 16 KiB of codes
+constexpr int kU8Unit = 2 * kU8Tile;                // 32 KiB
+constexpr int kU8Units = 3;
+constexpr uint32_t kU8Tx = kU8Unit + 16;
+
+// x as digits: plane k of `xd` is byte k of every N_c; returns the unit 2^(e - 22).
+// A zero x has digits and unit zero; one with an infinity or a NaN has unit NaN.
+__device__ __forceinline__ float write_digits(float x, uint32_t* mx, uint8_t* xd) {
+  const int tid = threadIdx.x;
+  const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(x) & 0x7FFFFFFFu);
+  if ((tid & 31) == 0) mx[tid >> 5] = m;
+  tc::bar_sync(1, kCompute);
+  const uint4 m4 = *(const uint4*)mx;
+  const uint32_t big = max(max(m4.x, m4.y), max(m4.z, m4.w));
+  // |x| < 2^e; below 2^-100 the fixed point stays where it is
+  const int e = max((int)(big >> 23) - 126, -100);
+  const float up = __uint_as_float((uint32_t)(127 + 22 - e) << 23);
+  const int n = __float2int_rn(x * up);
+  const int d0 = (int)(int8_t)n;
+  const int n1 = (n - d0) >> 8;
+  const int d1 = (int)(int8_t)n1;
+  xd[tid] = (uint8_t)d0;
+  xd[kD + tid] = (uint8_t)d1;
+  xd[2 * kD + tid] = (uint8_t)((n1 - d1) >> 8);
+  if (big >= 0x7F800000u) return __uint_as_float(0x7FC00000u);
+  return __uint_as_float((uint32_t)(127 - 22 + e) << 23);
+}
+
+__device__ __forceinline__ float join_digits(int s0, int s1, int s2, float unit) {
+  return fmaf((float)s2, 65536.0f, fmaf((float)s1, 256.0f, (float)s0)) * unit;
+}
+
+__global__ void __launch_bounds__(kThreads, 2)
+    decode_stream8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                          DecodeArgs a) {
+  // the gate kernel's programmatic dependent, like decode_stream_kernel
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* ring = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  float4* sc_s = (float4*)(ring + kU8Units * kU8Unit);  // [kU8Units] a, sA, sB, 0
+  uint8_t* xd = (uint8_t*)(sc_s + kU8Units);             // [2][3][kD] digits of x
+  uint32_t* mx = (uint32_t*)(xd + 2 * 3 * kD);           // [2][4]
+  uint64_t* full = (uint64_t*)(mx + 8);
+  uint64_t* empty = full + kU8Units;
+  float* rq = (float*)(empty + kU8Units);    // [kD] (not used: the gates are done)
+  float* red = rq + kD;                      // [4]
+  int* wcount = (int*)(red + 4);             // [4]
+  volatile int* abort_s = (volatile int*)(wcount + 4);
+
+  const int bh = blockIdx.x;
+  const int b = bh / a.H;
+  const int tid = threadIdx.x;
+  const int n = a.n_chunks[b];
+  const int m = a.m_partial[b];
+  const int32_t* act_idx = a.act_idx + (long)bh * a.max_chunks;
+  const float* act_g = a.act_g + (long)bh * a.max_chunks;
+  const int cnt = a.act_cnt[bh];
+
+  if (tid == 0) {
+    for (int u = 0; u < kU8Units; ++u) {
+      tc::mbar_init(&full[u], 1);
+      tc::mbar_init(&empty[u], 1);
+    }
+    *abort_s = 0;
+    tc::mbar_fence_init();
+    tc::fence_async_smem();
+  }
+  __syncthreads();
+
+  if (tid >= kCompute) {
+    // ---------------- TMA producer (warp 4, lane 0): one unit per active chunk ----------------
+    if (tid == kCompute && cnt > 0) {
+      tc::tma_prefetch_desc(&tmA);
+      tc::tma_prefetch_desc(&tmB);
+      int u = 0;
+      for (int p = cnt - 1; p >= 0; --p, ++u) {
+        const int st = u % kU8Units;
+        if (u >= kU8Units && !tc::mbar_wait(&empty[st], ((u / kU8Units) - 1) & 1, abort_s)) break;
+        const long slot = (long)bh * a.max_chunks + act_idx[p];
+        const int row = (int)(slot * kD);
+        tc::mbar_arrive_expect_tx(&full[st], kU8Tx);
+        uint8_t* dst = ring + st * kU8Unit;
+        tc::tma_load_2d(dst, &tmA, 0, row, &full[st]);
+        tc::tma_load_2d(dst + kU8Tile, &tmB, 0, row, &full[st]);
+        tc::bulk_load_1d(sc_s + st, a.df + slot * 4, 16, &full[st]);
+      }
+      if (*abort_s)
+        for (int t = max(0, u - kU8Units); t < u; ++t)
+          tc::mbar_wait(&full[t % kU8Units], (t / kU8Units) & 1, nullptr, 200000000ull);
+    }
+    __syncwarp();
+  } else {
+    // ---------------- compute (warps 0-3), thread = channel / row ----------------
+    float x, y0;
+    decode_prologue(a, bh, n, m, rq, red, wcount, x, y0, false, false, true, false);  // the sweep only
+    const long tok = (long)bh * kD + tid;
+    float y = 0.0f;
+    float g = cnt > 0 ? act_g[cnt - 1] : 0.0f;
+    float unit = write_digits(x, mx, xd);
+    tc::bar_sync(1, kCompute);
+    for (int p = cnt - 1, u = 0; p >= 0; --p, ++u) {
+      const int st = u % kU8Units;
+      const uint8_t* xc = xd + (u & 1) * 3 * kD;
+      const float g_next = p > 0 ? act_g[p - 1] : 0.0f;
+      if (!tc::bar_all(1, kCompute, tc::mbar_wait(&full[st], (u / kU8Units) & 1, abort_s))) break;
+      const uint8_t* rowA = ring + st * kU8Unit + tid * 128;
+      const uint8_t* rowB = rowA + kU8Tile;
+      int a0 = 0, a1 = 0, a2 = 0, b0 = 0, b1 = 0, b2 = 0;
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        const int off = (c ^ (tid & 7)) << 4;
+        const int4 wa = *(const int4*)(rowA + off);
+        const int4 wb = *(const int4*)(rowB + off);
+        const int4 x0 = *(const int4*)(xc + 16 * c);
+        const int4 x1 = *(const int4*)(xc + kD + 16 * c);
+        const int4 x2 = *(const int4*)(xc + 2 * kD + 16 * c);
+        a0 = __dp4a(wa.w, x0.w, __dp4a(wa.z, x0.z, __dp4a(wa.y, x0.y, __dp4a(wa.x, x0.x, a0))));
+        a1 = __dp4a(wa.w, x1.w, __dp4a(wa.z, x1.z, __dp4a(wa.y, x1.y, __dp4a(wa.x, x1.x, a1))));
+        a2 = __dp4a(wa.w, x2.w, __dp4a(wa.z, x2.z, __dp4a(wa.y, x2.y, __dp4a(wa.x, x2.x, a2))));
+        b0 = __dp4a(wb.w, x0.w, __dp4a(wb.z, x0.z, __dp4a(wb.y, x0.y, __dp4a(wb.x, x0.x, b0))));
+        b1 = __dp4a(wb.w, x1.w, __dp4a(wb.z, x1.z, __dp4a(wb.y, x1.y, __dp4a(wb.x, x1.x, b1))));
+        b2 = __dp4a(wb.w, x2.w, __dp4a(wb.z, x2.z, __dp4a(wb.y, x2.y, __dp4a(wb.x, x2.x, b2))));
+      }
+      const float4 sc = sc_s[st];
+      y = fmaf(g * sc.z, join_digits(b0, b1, b2, unit), y);
+      x = fmaf(1.0f - g, x, g * fmaf(sc.x, x, sc.y * join_digits(a0, a1, a2, unit)));
+      g = g_next;
+      // the digits of the new x; the barrier inside also says that this unit has been read
+      unit = write_digits(x, mx + 4 * ((u + 1) & 1), xd + ((u + 1) & 1) * 3 * kD);
+      if (tid == 0) tc::mbar_arrive(&empty[st]);
+    }
+    stf((__nv_bfloat16*)a.o + tok, y + y0);
+  }
+  __syncthreads();
+  if (tid == 0 && *abort_s) report_device_error(kErrMbarTimeout);
+}
+
 }  // namespace
 
 cudaError_t launch_decode_stream_factored(const DecodeArgs& a, cudaStream_t s) {
@@ -640,10 +790,17 @@ cudaError_t launch_decode_stream_factored(const DecodeArgs& a, cudaStream_t s) {
 
 cudaError_t launch_decode_stream(const DecodeArgs& a, cudaStream_t s) {
   const long rows = (long)a.B * a.H * a.max_chunks * kD;
+  const bool int8 = a.format == HLA_CACHE_INT8;
   CUtensorMap tmA, tmB;
-  cudaError_t e = make_tmap_rows128(&tmA, a.A, rows);
-  if (e != cudaSuccess) return e;
-  e = make_tmap_rows128(&tmB, a.Bm, rows);
+  cudaError_t e;
+  if (int8) {  // a row of 128 codes as 64 two-byte elements
+    if (rows >= (1L << 31)) return cudaErrorNotSupported;  // tile coordinates are 32-bit
+    e = make_tmap_2d(&tmA, a.A, kD / 2, rows, kD, kD / 2, kD);
+    if (e == cudaSuccess) e = make_tmap_2d(&tmB, a.Bm, kD / 2, rows, kD, kD / 2, kD);
+  } else {
+    e = make_tmap_rows128(&tmA, a.A, rows);
+    if (e == cudaSuccess) e = make_tmap_rows128(&tmB, a.Bm, rows);
+  }
   if (e != cudaSuccess) return e;
   // key pools (one per chunk; with window representatives the gates read them directly)
   CUtensorMap tmR;
@@ -658,8 +815,10 @@ cudaError_t launch_decode_stream(const DecodeArgs& a, cudaStream_t s) {
   decode_gates_kernel<<<a.B * a.H, kThreads, gsmem, s>>>(tmR, a);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  const size_t smem = 1024 + kUnits * kUnit + 2 * kUnits * 8 + (4 * kD + 16) * 4;
-  e = cudaFuncSetAttribute(decode_stream_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  const size_t smem = int8 ? 1024 + kU8Units * (kU8Unit + 16) + 2 * 3 * kD + 32 + 2 * kU8Units * 8 + (kD + 16) * 4
+                           : 1024 + kUnits * kUnit + 2 * kUnits * 8 + (4 * kD + 16) * 4;
+  auto* kern = int8 ? decode_stream8_kernel : decode_stream_kernel;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   // programmatic dependent launch: the stream CTAs are scheduled while the gate grid
   // drains and wait (griddepcontrol.wait) for it to complete
@@ -673,7 +832,7 @@ cudaError_t launch_decode_stream(const DecodeArgs& a, cudaStream_t s) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, decode_stream_kernel, tmA, tmB, a);
+  e = cudaLaunchKernelEx(&cfg, kern, tmA, tmB, a);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }

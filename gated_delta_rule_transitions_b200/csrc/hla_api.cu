@@ -1180,8 +1180,8 @@ hla_status hla_decode_step(const hla_config* cfg, hla_cache* cache, const void* 
   }
   cudaStream_t s = (cudaStream_t)stream;
   {
-    // the dense bf16 cache with d = 128 gates in one kernel and streams in another
-    const bool two = cache->format == HLA_CACHE_DENSE && cfg->dtype == HLA_BF16 && cfg->dk == 128;
+    // the dense and 8-bit bf16 caches with d = 128 gate in one kernel and stream in another
+    const bool two = cache->format != HLA_CACHE_FACTORED && cfg->dtype == HLA_BF16 && cfg->dk == 128;
     StageScope _sc(HLA_STAGE_DECODE, s, two ? 2 : 1);
     HLA_CUDA(hla::launch_decode_main(a, s), "decode launch");
   }
