@@ -1,0 +1,717 @@
+// The gated delta rule by chunks of 64 tokens on tcgen05 tensor cores (bf16, d = 128, one
+// decay per head), ragged sequences, float32 state in and out.
+//
+// HLA summary page, "Methodology in Plain English" para. 1 (the per-token rule; affine maps
+// compose); chunkwise WY/UT form (the chunkwise WY algorithm named in the Gated DeltaNet-2
+// abstract on the HLA listing page).  Per chunk, with l_t = sum_{s<=t} log alpha_s,
+// gamma_t = e^{l_t}, Gamma_ts = e^{l_t - l_s}:
+//   L = strictly-lower(diag(beta) (Gamma o K K^T)),  T = (I + L)^{-1} diag(beta),
+//   G = tril(Gamma o Q K^T) T                                     (gdn_wy_kernel)
+//   R = V - diag(gamma) K S^T,  U = T R,  O = diag(gamma) Q S^T + G R,
+//   S <- gamma_C S + U^T diag(gamma_C / gamma_t) K                 (gdn_scan_kernel)
+// T and G do not depend on the state: gdn_wy_kernel makes them for every chunk at once.
+// gdn_scan_kernel then walks the chunks of one (sequence, head) and one half of the value
+// dim, three products a chunk, each waiting for the one before.
+//
+// Precision.  The state is float32 and stays so: it is held in registers, and what goes into
+// a product (S, R, U, T) goes in as two bf16 numbers, x = hi + lo, hi = bf16(x),
+// lo = bf16(x - hi), off by at most 2^-18 of x; K, Q and V are bf16 already.  Only the lo lo
+// parts are left out (2^-18).  G alone is rounded to one bf16: it reaches the output and
+// nothing else, and the output is bf16.  Decays are differences of 64-bit running sums.
+#include "common.cuh"
+#include "kernels.cuh"
+#include "tc_common.cuh"
+
+namespace hla {
+
+HLA_DEFINE_ERROR_WORD(gdn_chunk)
+
+cudaError_t make_tmap_2d(CUtensorMap* m, const void* base, long inner, long rows, long row_stride_bytes,
+                         int box_inner, int box_rows);
+
+namespace {
+
+constexpr int kD = 128;
+constexpr int kC = 64;
+constexpr int kTile = kC * 128;               // 8 KiB: 64 rows of 128 bytes, 128-byte swizzle
+constexpr int kWy = 3 * kTile;                // T_hi, G, T_lo of a chunk, as they lie in shared memory
+constexpr int kScal = 2 * kC * 4;             // gamma_t, gamma_C / gamma_t
+constexpr int kSlot = kWy + kScal;            // workspace bytes per (chunk slot, head)
+
+__device__ __forceinline__ int swz(int row, int chunk) { return row * 128 + ((chunk ^ (row & 7)) << 4); }
+
+// Chunk slots.  Sequence s owns the slots cu[s] / 64 + s + c, c < ceil(len / 64): they never
+// meet the next sequence's, so no prefix sum over the lengths is needed.  The owner of a slot
+// is the last sequence whose first slot is not above it.
+__device__ __forceinline__ int slot_owner(const int32_t* cu, int n_seq, int slot) {
+  int lo = 0, hi = n_seq;  // owner in [lo, hi)
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (cu[mid] / kC + mid <= slot)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  return lo;
+}
+
+__device__ __forceinline__ bool good_bounds(int t0, int t1, int T) { return t0 >= 0 && t1 >= t0 && t1 <= T; }
+
+// x as two bf16 numbers, packed for two neighbours.
+__device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
+  hi = tc::pack_bf16x2(a, b);
+  lo = tc::pack_bf16x2(a - tc::bf16lo(hi), b - tc::bf16hi(hi));
+}
+
+// Waits for this thread's tensor-memory loads; the registers are operands, so that no use of
+// them is scheduled before the wait.
+__device__ __forceinline__ void wait_ld(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                 "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                 "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
+}
+
+// ---- T and G of every chunk ------------------------------------------------------------
+
+constexpr int kP = kC + 4;                    // row pitch (floats): 16-byte rows
+constexpr int kMat = kC * kP * 4;             // one 64 x 64 float32 matrix
+constexpr int kWyQK = 0;                      // [kb][Q | K][64 rows][128 B]; then P and L'
+constexpr int kWyL = 4 * kTile;               // L, then G
+constexpr int kWyU = kWyL + kMat;             // (I + L)^{-1}
+constexpr int kWySmall = kWyU + kMat;
+constexpr int kXP = 52;                       // row pitch (floats) of L'
+constexpr int kWyP = kWyQK;                   // P over the Q, K tiles once they are multiplied
+constexpr int kWyX = kWyQK + kMat;
+constexpr int kWySmem = kWySmall + kC * 8 + 5 * kC * 4 + 2 * 8 + 32;
+static_assert(kMat + 48 * kXP * 4 <= 4 * kTile, "P and L' fit over the tiles");
+constexpr uint32_t kIdescWy = tc::idesc_bf16_f32(128, 64, 0, 0);
+constexpr float kProductRange = 40.0f;
+
+__device__ __forceinline__ uint32_t tf32(float x) {
+  uint32_t r;
+  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(x));
+  return r;
+}
+
+__device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+
+// acc += A (16 x K) B (K x 8), float32 in shared memory (row pitches pa, pb), K a multiple of
+// 8; kExact: each factor as two tf32 numbers (2^-22), else as one (2^-12).
+template <bool kExact>
+__device__ __forceinline__ void rows16(float (&acc)[4], const float* A, int pa, const float* B, int pb, int K,
+                                       int lane) {
+  const int g = lane >> 2, q = lane & 3;
+  for (int k0 = 0; k0 < K; k0 += 8) {
+    const float a[4] = {A[g * pa + k0 + q], A[(g + 8) * pa + k0 + q], A[g * pa + k0 + q + 4],
+                        A[(g + 8) * pa + k0 + q + 4]};
+    const float b[2] = {B[(k0 + q) * pb + g], B[(k0 + q + 4) * pb + g]};
+    uint32_t ah[4], bh[2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) ah[i] = tf32(a[i]);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) bh[i] = tf32(b[i]);
+    if (kExact) {
+      uint32_t al[4], bl[2];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) al[i] = tf32(a[i] - __uint_as_float(ah[i]));
+#pragma unroll
+      for (int i = 0; i < 2; ++i) bl[i] = tf32(b[i] - __uint_as_float(bh[i]));
+      mma_tf32(acc, ah, bl);
+      mma_tf32(acc, al, bh);
+    }
+    mma_tf32(acc, ah, bh);
+  }
+}
+
+__device__ __forceinline__ void store16(float* D, int pd, const float (&acc)[4], float s, int lane) {
+  const int g = lane >> 2, q = lane & 3;
+  *(float2*)(D + g * pd + 2 * q) = make_float2(s * acc[0], s * acc[1]);
+  *(float2*)(D + (g + 8) * pd + 2 * q) = make_float2(s * acc[2], s * acc[3]);
+}
+
+// e^x of a 64-bit exponent, to float32's last bits.
+__device__ __forceinline__ float exp64(double x) {
+  const float h = (float)x;
+  const float e = expf(h);
+  return fmaf(e, (float)(x - (double)h), e);
+}
+
+// One CTA (4 warps) per (chunk slot, head), three per SM.
+__global__ void __launch_bounds__(128, 3)
+    gdn_wy_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK, GdnArgs a,
+                  uint8_t* ws) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* sm = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  float* Ls = (float*)(sm + kWyL);
+  float* Us = (float*)(sm + kWyU);
+  float* Ps = (float*)(sm + kWyP);
+  float* Xs = (float*)(sm + kWyX);
+  double* ell = (double*)(sm + kWySmall);
+  float* beta_s = (float*)(ell + kC);
+  float* gam = beta_s + kC;
+  float* igam = gam + kC;
+  uint64_t* bars = (uint64_t*)(igam + kC);      // tma, mma
+  double* wsum = (double*)(bars + 2);
+  uint32_t* lmax = (uint32_t*)(wsum + 1);       // [2]
+  uint32_t* tmem_s = lmax + 2;
+  volatile int* abort_s = (volatile int*)(tmem_s + 1);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int h = blockIdx.x % a.H;
+  const int slot = blockIdx.x / a.H;
+  const int seq = slot_owner(a.cu, a.n_seq, slot);
+  const int s0 = a.cu[seq], s1 = a.cu[seq + 1];
+  const int c = slot - (s0 / kC + seq);
+  if (!good_bounds(s0, s1, a.T) || c < 0 || c >= (s1 - s0 + kC - 1) / kC) return;  // a slot of no chunk
+  const int t0 = s0 + c * kC;
+  const int n = min(kC, s1 - t0);
+  const int hk = h / (a.H / a.Hk);
+
+  if (tid == 0) {
+    tc::mbar_init(&bars[0], 1);
+    tc::mbar_init(&bars[1], 1);
+    *abort_s = 0;
+    tc::mbar_fence_init();
+    tc::fence_async_smem();
+  }
+  if (warp == 0) tc::tmem_alloc(tmem_s, 64);
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tm = *tmem_s;
+  if (tid == 0) {
+    tc::mbar_arrive_expect_tx(&bars[0], 4 * kTile);
+    for (int kb = 0; kb < 2; ++kb) {
+      tc::tma_load_2d(sm + kWyQK + kb * 2 * kTile, &tmQ, hk * kD + 64 * kb, t0, &bars[0]);
+      tc::tma_load_2d(sm + kWyQK + kb * 2 * kTile + kTile, &tmK, hk * kD + 64 * kb, t0, &bars[0]);
+    }
+  }
+  // l_t: log decays summed in 64 bits (a decay of zero as e^-200, which is zero in float32
+  // next to anything else)
+  double la = 0.0;
+  float be = 0.0f;
+  if (tid < kC) {
+    if (tid < n) {
+      const long at = (long)(t0 + tid) * a.H + h;
+      const float x = logf(a.alpha[at]);
+      la = x < -200.0f ? -200.0 : (double)x;
+      be = a.beta[at];
+    }
+    beta_s[tid] = be;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const double y = __shfl_up_sync(0xFFFFFFFFu, la, o);
+      if (lane >= o) la += y;
+    }
+    if (tid == 31) *wsum = la;
+  }
+  __syncthreads();
+  if (tid < kC) {
+    if (warp == 1) la += *wsum;
+    ell[tid] = la;
+    const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fabsf((float)la)));
+    if (lane == 0) lmax[warp] = m;
+  }
+  __syncthreads();
+  if (tid < kC) {
+    gam[tid] = exp64(la);
+    igam[tid] = exp64(-la);
+  }
+  bool ok = tc::bar_all(1, 128, tid == 0 ? tc::mbar_wait(&bars[0], 0, abort_s) : true);
+  if (ok && n < kC) {
+    // rows behind the sequence belong to another one, or to none: zero
+    for (int e = tid; e < (kC - n) * 32; e += 128) {
+      const int r = n + e / 32, x = e % 32;  // 4 tiles of 8 16-byte pieces
+      *(uint4*)(sm + kWyQK + (x >> 3) * kTile + r * 128 + (x & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+    }
+    tc::fence_async_smem();
+    __syncthreads();
+  }
+  // [Q; K] K^T: rows 0-63 Q K^T, rows 64-127 K K^T
+  if (ok && tid == 0) {
+    const uint32_t base = tc::smem_u32(sm + kWyQK);
+#pragma unroll
+    for (int ks = 0; ks < kD / 16; ++ks) {
+      const uint32_t off = (ks >> 2) * 2 * kTile + (ks & 3) * 32;
+      tc::mma_ss(tm, tc::sdesc_sw128(base + off, 16, 1024), tc::sdesc_sw128(base + kTile + off, 16, 1024), kIdescWy,
+                 ks > 0 ? 1u : 0u);
+    }
+    tc::mma_commit(&bars[1]);
+  }
+  if (ok) ok = tc::bar_all(1, 128, tid == 0 ? tc::mbar_wait(&bars[1], 0, abort_s) : true);
+  if (ok) {
+    tc::tc_fence_after();
+    const int t = tid & (kC - 1);
+    const bool isL = tid >= kC;
+    float* row = (isL ? Ls : Ps) + t * kP;
+    const float bt = isL ? beta_s[t] : 1.0f;
+    const int last = isL ? t - 1 : t;  // columns up to and with `last`
+    const bool product = max(lmax[0], lmax[1]) <= __float_as_uint(kProductRange);
+    const float gt = gam[t] * bt;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      uint32_t x[32];
+      tc::tmem_ld32(tm + ((uint32_t)(32 * warp) << 16) + 32 * half, x);
+      wait_ld(x);
+#pragma unroll
+      for (int e4 = 0; e4 < 32; e4 += 4) {
+        float v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int s = 32 * half + e4 + e;
+          float d = 0.0f;
+          // the pair's decay as a product of two exponentials while both stay in range
+          if (s <= last) d = product ? gt * igam[s] : bt * expf((float)(ell[t] - ell[s]));
+          v[e] = s <= last ? d * __uint_as_float(x[e4 + e]) : 0.0f;
+        }
+        *(float4*)(row + 32 * half + e4) = make_float4(v[0], v[1], v[2], v[3]);
+      }
+    }
+    tc::tc_fence_before();
+  }
+  __syncthreads();
+  // U = (I + L)^{-1} by 16 x 16 blocks: forward substitution on the diagonal blocks, then
+  // U_ij = -sum_{k=j}^{i-1} (U_ii L_ik) U_kj, one level i - j after the other
+  if (tid < kC) {
+    const int k = tid >> 4, cc = tid & 15;
+    float x[16];
+#pragma unroll
+    for (int tl = 0; tl < 16; ++tl) {
+      const float* Lrow = Ls + (16 * k + tl) * kP + 16 * k;
+      float v = tl == cc ? 1.0f : 0.0f;
+#pragma unroll
+      for (int sl = 0; sl < tl; ++sl) v = fmaf(-Lrow[sl], x[sl], v);
+      x[tl] = v;
+    }
+#pragma unroll
+    for (int tl = 0; tl < 16; ++tl) Us[(16 * k + tl) * kP + 16 * k + cc] = x[tl];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int r = 0; r < 3; ++r) {  // L'_ik = U_ii L_ik: 6 blocks, 12 halves, 3 a warp
+    const int u = warp + 4 * r, blk = u >> 1, nh = u & 1;
+    const int ib = blk < 1 ? 1 : (blk < 3 ? 2 : 3);
+    const int kb = blk - (ib * (ib - 1)) / 2;
+    float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    rows16<true>(acc, Us + 16 * ib * kP + 16 * ib, kP, Ls + 16 * ib * kP + 16 * kb + 8 * nh, kP, 16, lane);
+    store16(Xs + (16 * ib - 16) * kXP + 16 * kb + 8 * nh, kXP, acc, 1.0f, lane);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int lev = 1; lev <= 3; ++lev) {
+    for (int u = warp; u < 2 * (4 - lev); u += 4) {
+      const int jb = u >> 1, nh = u & 1;
+      float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      rows16<true>(acc, Xs + 16 * (jb + lev - 1) * kXP + 16 * jb, kXP, Us + 16 * jb * kP + 16 * jb + 8 * nh, kP,
+                   16 * lev, lane);
+      store16(Us + 16 * (jb + lev) * kP + 16 * jb + 8 * nh, kP, acc, -1.0f, lane);
+    }
+    __syncthreads();
+  }
+  // G = P U diag(beta) over L (no longer needed); warp = block of 16 rows
+  for (int nt = 0; nt < 2 * (warp + 1); ++nt) {
+    const int k0 = 16 * (nt >> 1);
+    float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    rows16<false>(acc, Ps + 16 * warp * kP + k0, kP, Us + k0 * kP + 8 * nt, kP, 16 * (warp + 1) - k0, lane);
+    store16(Ls + 16 * warp * kP + 8 * nt, kP, acc, 1.0f, lane);
+  }
+  __syncthreads();
+  // out: T_hi, G, T_lo as swizzled tiles, then gamma_t and gamma_C / gamma_t
+  uint8_t* out = ws + ((long)slot * a.H + h) * kSlot;
+  const int t = tid & (kC - 1);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const int c8 = 4 * (tid >> 6) + e;
+    uint32_t th[4] = {0u, 0u, 0u, 0u}, tl[4] = {0u, 0u, 0u, 0u}, gg[4] = {0u, 0u, 0u, 0u};
+    if ((c8 >> 1) <= (t >> 4)) {  // blocks above the diagonal are zero
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int cc = 8 * c8 + 2 * u;
+        const float2 b2 = *(const float2*)(beta_s + cc);
+        const float2 x = *(const float2*)(Us + t * kP + cc), y = *(const float2*)(Ls + t * kP + cc);
+        split2(x.x * b2.x, x.y * b2.y, th[u], tl[u]);
+        gg[u] = tc::pack_bf16x2(y.x * b2.x, y.y * b2.y);
+      }
+    }
+    const int at = swz(t, c8);
+    *(uint4*)(out + at) = make_uint4(th[0], th[1], th[2], th[3]);
+    *(uint4*)(out + kTile + at) = make_uint4(gg[0], gg[1], gg[2], gg[3]);
+    *(uint4*)(out + 2 * kTile + at) = make_uint4(tl[0], tl[1], tl[2], tl[3]);
+  }
+  float* sc = (float*)(out + kWy);
+  if (tid < kC)
+    sc[tid] = gam[tid];
+  else
+    sc[tid] = exp64(ell[kC - 1] - ell[tid - kC]);
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  if (warp == 0) tc::tmem_dealloc(tm, 64);
+  if (tid == 0 && *abort_s) report_device_error(kErrMbarTimeout);
+}
+
+// ---- the walk over a sequence's chunks ---------------------------------------------------
+//
+// One CTA per (sequence, head, 64 value columns): warp 0 loads, warp 1 issues the products,
+// warps 2-5 do the rest.  Two stages of 64.5 KiB.
+//   A  [K; Q] (128 x 128) x S^T (128 x 64, hi and lo)  -> K S^T (rows 0-63), Q S^T (64-127)
+//      rows 0-63: R_t = V_t - gamma_t (K S^T)_t into shared memory (hi, lo); rows 64-127
+//      keep gamma_t (Q S^T)_t in registers
+//   B  [T_hi; G] (128 x 64) x R (64 x 64, hi and lo), and T_lo x R_hi -> U (rows 0-63), G R
+//      rows 0-63: diag(gamma_C / gamma_t) U (hi, lo) over R; rows 64-127: the output
+//   C  K^T (128 x 64) x U (64 x 64, hi and lo)         -> S's update, one row k a thread:
+//      S <- gamma_C S + update in registers, and hi, lo of it for the next A.
+
+constexpr int kV = 64;                        // value columns per CTA
+constexpr int kStK = 0;                       // stage: [kb][K | Q][64 rows][128 B]
+constexpr int kStV = 4 * kTile;
+constexpr int kStWy = kStV + kTile;           // T_hi, G, T_lo
+constexpr int kStScal = kStWy + kWy;
+constexpr int kStage = kStScal + 1024;
+constexpr int kStages = 2;
+constexpr uint32_t kStTx = 5 * kTile + kSlot;
+constexpr int kScS = kStages * kStage;        // S^T hi, lo: 128 rows of 128 B each
+constexpr int kScR = kScS + 4 * kTile;        // R (then U) hi, lo
+constexpr int kScSmall = kScR + 2 * kTile;
+constexpr int kScSmem = kScSmall + 128;
+constexpr int kScThreads = 192;
+constexpr uint32_t kIdescA = tc::idesc_bf16_f32(128, kV, 0, 1);
+constexpr uint32_t kIdescC = tc::idesc_bf16_f32(128, kV, 1, 1);
+
+// 32 float32 values as hi and lo halves of rows of 128 bytes (row r of two swizzled tiles).
+__device__ __forceinline__ void store_split(uint8_t* hi, uint8_t* lo, int r, int half, const float* x) {
+#pragma unroll
+  for (int p = 0; p < 4; ++p) {
+    uint32_t h[4], l[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) split2(x[8 * p + 2 * e], x[8 * p + 2 * e + 1], h[e], l[e]);
+    const int at = swz(r, 4 * half + p);
+    *(uint4*)(hi + at) = make_uint4(h[0], h[1], h[2], h[3]);
+    *(uint4*)(lo + at) = make_uint4(l[0], l[1], l[2], l[3]);
+  }
+}
+
+__global__ void __launch_bounds__(kScThreads, 1)
+    gdn_scan_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                    const __grid_constant__ CUtensorMap tmV, GdnArgs a, const uint8_t* ws) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* sm = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  uint64_t* full = (uint64_t*)(sm + kScSmall);
+  uint64_t* empty = full + kStages;
+  uint64_t* doneA = empty + kStages;
+  uint64_t* doneB = doneA + 1;
+  uint64_t* doneC = doneB + 1;
+  uint64_t* s_ready = doneC + 1;
+  uint64_t* r_ready = s_ready + 1;
+  uint64_t* u_ready = r_ready + 1;
+  uint64_t* fin = u_ready + 1;
+  uint32_t* tmem_s = (uint32_t*)(fin + 1);
+  volatile int* abort_s = (volatile int*)(tmem_s + 1);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int vh = blockIdx.x & 1;
+  const int h = (int)((blockIdx.x >> 1) % a.H);
+  const int seq = (int)((blockIdx.x >> 1) / a.H);
+  const int hk = h / (a.H / a.Hk);
+  // what the device arrays cannot mean is refused: nothing is read or written for it
+  int slot = seq;
+  if (a.slots != nullptr) {
+    slot = a.slots[seq];
+    if (slot < 0) return;  // padding of the batch
+    bool twice = false;    // an earlier sequence has the same state
+    for (int i = tid; i < seq; i += kScThreads) twice |= a.slots[i] == slot;
+    if (__syncthreads_or(twice) || slot >= a.n_slots) {
+      if (tid == 0) report_device_error(kErrBadIndex);
+      return;
+    }
+  }
+  const int s0 = a.cu[seq], s1 = a.cu[seq + 1];
+  const int len = s1 - s0;
+  const int nc = (len + kC - 1) / kC;
+  const int base = s0 / kC + seq;
+  // (a slot's owner is found by bisection: where the bounds are in order it is this sequence)
+  if (!good_bounds(s0, s1, a.T) ||
+      (nc > 0 && (slot_owner(a.cu, a.n_seq, base) != seq || slot_owner(a.cu, a.n_seq, base + nc - 1) != seq))) {
+    if (tid == 0) report_device_error(kErrBadIndex);
+    return;
+  }
+  const long soff = ((long)slot * a.H + h) * kD * kD + (long)vh * kV * kD;  // state rows of this half
+  if (nc == 0) {  // no tokens: the state passes through
+    if (a.state_out != nullptr && a.state_out != a.state_in)
+      for (int e = tid; e < kV * kD / 4; e += kScThreads) {
+        float4 w = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (a.state_in != nullptr) w = ((const float4*)(a.state_in + soff))[e];
+        ((float4*)(a.state_out + soff))[e] = w;
+      }
+    return;
+  }
+
+  if (tid == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      tc::mbar_init(&full[s], 1);
+      tc::mbar_init(&empty[s], 1);
+    }
+    tc::mbar_init(doneA, 1);
+    tc::mbar_init(doneB, 1);
+    tc::mbar_init(doneC, 1);
+    tc::mbar_init(s_ready, 4);
+    tc::mbar_init(r_ready, 2);
+    tc::mbar_init(u_ready, 2);
+    tc::mbar_init(fin, 1);
+    *abort_s = 0;
+    tc::mbar_fence_init();
+    tc::fence_async_smem();
+  }
+  if (warp == 1) tc::tmem_alloc(tmem_s, 256);
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tm = *tmem_s;  // columns 0-63: A, 64-127: B, 128-191: T_lo R_hi, 192-255: C
+
+  if (warp == 0) {
+    // ---------------- loads ----------------
+    if (lane == 0) {
+      tc::tma_prefetch_desc(&tmQ);
+      tc::tma_prefetch_desc(&tmK);
+      tc::tma_prefetch_desc(&tmV);
+      int c = 0;
+      for (; c < nc; ++c) {
+        const int st = c % kStages;
+        if (c >= kStages && !tc::mbar_wait(&empty[st], ((c / kStages) - 1) & 1, abort_s)) break;
+        uint8_t* dst = sm + st * kStage;
+        const int y = s0 + c * kC;
+        tc::mbar_arrive_expect_tx(&full[st], kStTx);
+        for (int kb = 0; kb < 2; ++kb) {
+          tc::tma_load_2d(dst + kStK + kb * 2 * kTile, &tmK, hk * kD + 64 * kb, y, &full[st]);
+          tc::tma_load_2d(dst + kStK + kb * 2 * kTile + kTile, &tmQ, hk * kD + 64 * kb, y, &full[st]);
+        }
+        tc::tma_load_2d(dst + kStV, &tmV, h * kD + vh * kV, y, &full[st]);
+        tc::bulk_load_1d(dst + kStWy, ws + ((long)(base + c) * a.H + h) * kSlot, kSlot, &full[st]);
+      }
+      if (*abort_s)  // never leave the CTA with copies in flight
+        for (int t = max(0, c - kStages); t < c; ++t)
+          tc::mbar_wait(&full[t % kStages], (t / kStages) & 1, nullptr, 200000000ull);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ---------------- products ----------------
+    if (lane == 0) {
+      const uint32_t s_hi = tc::smem_u32(sm + kScS), s_lo = s_hi + 2 * kTile;
+      const uint32_t r_hi = tc::smem_u32(sm + kScR), r_lo = r_hi + kTile;
+      for (int c = 0; c < nc; ++c) {
+        const int st = c % kStages;
+        const uint32_t par = (uint32_t)c & 1;
+        const uint32_t stage = tc::smem_u32(sm + st * kStage);
+        if (!tc::mbar_wait(&full[st], (uint32_t)(c / kStages) & 1, abort_s) || !tc::mbar_wait(s_ready, par, abort_s))
+          break;
+        tc::tc_fence_after();
+#pragma unroll
+        for (int p = 0; p < 2; ++p)
+#pragma unroll
+          for (int ks = 0; ks < kD / 16; ++ks)
+            tc::mma_ss(tm, tc::sdesc_sw128(stage + kStK + (ks >> 2) * 2 * kTile + (ks & 3) * 32, 16, 1024),
+                       tc::sdesc_sw128((p ? s_lo : s_hi) + ks * 2048, kTile, 1024), kIdescA, (p | ks) > 0 ? 1u : 0u);
+        tc::mma_commit(doneA);
+        if (!tc::mbar_wait(r_ready, par, abort_s)) break;
+        tc::tc_fence_after();
+#pragma unroll
+        for (int p = 0; p < 3; ++p)
+#pragma unroll
+          for (int ks = 0; ks < kC / 16; ++ks)  // p: T_hi R_hi, T_hi R_lo, T_lo R_hi (its rows 64-127 are not read)
+            tc::mma_ss(tm + (p == 2 ? 128 : 64),
+                       tc::sdesc_sw128(stage + kStWy + (p == 2 ? 2 * kTile : 0) + ks * 32, 16, 1024),
+                       tc::sdesc_sw128((p == 1 ? r_lo : r_hi) + ks * 2048, kTile, 1024), kIdescA,
+                       (p == 1 || ks > 0) ? 1u : 0u);
+        tc::mma_commit(doneB);
+        if (!tc::mbar_wait(u_ready, par, abort_s)) break;
+        tc::tc_fence_after();
+#pragma unroll
+        for (int p = 0; p < 2; ++p)
+#pragma unroll
+          for (int ks = 0; ks < kC / 16; ++ks)
+            tc::mma_ss(tm + 192, tc::sdesc_sw128(stage + kStK + ks * 2048, 2 * kTile, 1024),
+                       tc::sdesc_sw128((p ? r_lo : r_hi) + ks * 2048, kTile, 1024), kIdescC, (p | ks) > 0 ? 1u : 0u);
+        tc::mma_commit(doneC);
+        tc::mma_commit(&empty[st]);
+      }
+      // every product issued here completes before tensor memory is freed
+      tc::mma_commit(fin);
+      tc::mbar_wait(fin, 0, nullptr, 200000000ull);
+    }
+    __syncwarp();
+  } else {
+    // ---------------- warps 2-5: row r of every product ----------------
+    const int q = warp & 3;            // tensor-memory lanes of this warp
+    const int r = 32 * q + lane;       // A, B: token r & 63; C and S: key channel r
+    const int t = r & (kC - 1);
+    const bool low = r < kC;
+    const uint32_t row = tm + ((uint32_t)(32 * q) << 16);
+    uint8_t* sh = sm + kScS;
+    uint8_t* rh = sm + kScR;
+    float S[kV];
+    if (a.state_in != nullptr) {
+#pragma unroll
+      for (int v = 0; v < kV; ++v) S[v] = a.state_in[soff + (long)v * kD + r];
+    } else {
+#pragma unroll
+      for (int v = 0; v < kV; ++v) S[v] = 0.0f;
+    }
+    bool ok = true;
+    for (int c = 0; c < nc; ++c) {
+      const int st = c % kStages;
+      const uint32_t par = (uint32_t)c & 1;
+      uint8_t* stage = sm + st * kStage;
+      const float* sc = (const float*)(stage + kStScal);
+      const int n = min(kC, len - c * kC);
+      store_split(sh, sh + 2 * kTile, r, 0, S);
+      store_split(sh, sh + 2 * kTile, r, 1, S + 32);
+      ok = tc::mbar_wait(&full[st], (uint32_t)(c / kStages) & 1, abort_s);
+      if (!ok) break;
+      if (n < kC && low && t >= n) {
+        // keys behind the sequence belong to another one, or to none: zero
+#pragma unroll
+        for (int c8 = 0; c8 < 8; ++c8) {
+          *(uint4*)(stage + kStK + t * 128 + 16 * c8) = make_uint4(0u, 0u, 0u, 0u);
+          *(uint4*)(stage + kStK + 2 * kTile + t * 128 + 16 * c8) = make_uint4(0u, 0u, 0u, 0u);
+        }
+      }
+      // (read before this warp's s_ready: the stage may be refilled as soon as C is done)
+      const float gt = sc[t], dt = sc[kC + t], gC = sc[kC - 1];
+      tc::fence_async_smem();
+      tc::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(s_ready);
+      ok = tc::mbar_wait_warp(doneA, par, abort_s);
+      if (!ok) break;
+      tc::tc_fence_after();
+      uint32_t x[2][32];  // K S^T or Q S^T
+      tc::tmem_ld32(row, x[0]);
+      tc::tmem_ld32(row + 32, x[1]);
+      wait_ld(x[0]);
+      wait_ld(x[1]);
+      if (low) {
+        // R_t, zero behind the sequence
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          float f[32];
+#pragma unroll
+          for (int p = 0; p < 4; ++p) {
+            const uint4 w = *(const uint4*)(stage + kStV + swz(t, 4 * half + p));
+            const uint32_t vw[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int v = 8 * p + 2 * e;
+              f[v] = t < n ? fmaf(-gt, __uint_as_float(x[half][v]), tc::bf16lo(vw[e])) : 0.0f;
+              f[v + 1] = t < n ? fmaf(-gt, __uint_as_float(x[half][v + 1]), tc::bf16hi(vw[e])) : 0.0f;
+            }
+          }
+          store_split(rh, rh + kTile, t, half, f);
+        }
+        tc::fence_async_smem();
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(r_ready);
+      }
+      ok = tc::mbar_wait_warp(doneB, par, abort_s);
+      if (!ok) break;
+      tc::tc_fence_after();
+      if (low) {
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint32_t y[32], z[32];
+          tc::tmem_ld32(row + 64 + 32 * half, y);
+          tc::tmem_ld32(row + 128 + 32 * half, z);
+          wait_ld(y);
+          wait_ld(z);
+          float f[32];
+#pragma unroll
+          for (int v = 0; v < 32; ++v) f[v] = dt * (__uint_as_float(y[v]) + __uint_as_float(z[v]));
+          store_split(rh, rh + kTile, t, half, f);
+        }
+        tc::fence_async_smem();
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(u_ready);
+      } else {
+        __nv_bfloat16* orow = (__nv_bfloat16*)a.o + ((long)(s0 + c * kC + t) * a.H + h) * kD + vh * kV;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint32_t y[32];
+          tc::tmem_ld32(row + 64 + 32 * half, y);
+          wait_ld(y);
+          if (t < n) {
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+              uint32_t w[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int v = 8 * p + 2 * e;
+                w[e] = tc::pack_bf16x2(fmaf(gt, __uint_as_float(x[half][v]), __uint_as_float(y[v])),
+                                       fmaf(gt, __uint_as_float(x[half][v + 1]), __uint_as_float(y[v + 1])));
+              }
+              *(uint4*)(orow + 32 * half + 8 * p) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          }
+        }
+      }
+      ok = tc::mbar_wait_warp(doneC, par, abort_s);
+      if (!ok) break;
+      tc::tc_fence_after();
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        uint32_t z[32];
+        tc::tmem_ld32(row + 192 + 32 * half, z);
+        wait_ld(z);
+#pragma unroll
+        for (int v = 0; v < 32; ++v) S[32 * half + v] = fmaf(gC, S[32 * half + v], __uint_as_float(z[v]));
+      }
+    }
+    if (ok && a.state_out != nullptr) {
+#pragma unroll
+      for (int v = 0; v < kV; ++v) a.state_out[soff + (long)v * kD + r] = S[v];
+    }
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  if (warp == 1) tc::tmem_dealloc(tm, 256);
+  if (tid == 0 && *abort_s) report_device_error(kErrMbarTimeout);
+}
+
+}  // namespace
+
+// Chunk slots of T tokens in n sequences (see slot_owner).
+static long gdn_slots(int T, int n_seq) { return (long)T / kC + n_seq; }
+
+size_t gdn_chunk_workspace(int T, int n_seq, int H) { return (size_t)gdn_slots(T, n_seq) * H * kSlot; }
+
+cudaError_t launch_gdn_chunk(const GdnArgs& a, void* ws, cudaStream_t s) {
+  const long wy = gdn_slots(a.T, a.n_seq) * a.H, scan = (long)a.n_seq * a.H * 2;
+  if (wy >= (1L << 31) || scan >= (1L << 31)) return cudaErrorNotSupported;
+  CUtensorMap tq, tk, tv;
+  cudaError_t e = make_tmap_2d(&tq, a.q, (long)a.Hk * kD, a.T, (long)a.Hk * kD * 2, 64, 64);
+  if (e == cudaSuccess) e = make_tmap_2d(&tk, a.k, (long)a.Hk * kD, a.T, (long)a.Hk * kD * 2, 64, 64);
+  if (e == cudaSuccess) e = make_tmap_2d(&tv, a.v, (long)a.H * kD, a.T, (long)a.H * kD * 2, 64, 64);
+  if (e != cudaSuccess) return e;
+  const int wsm = 1024 + kWySmem, ssm = 1024 + kScSmem;
+  e = cudaFuncSetAttribute(gdn_wy_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, wsm);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(gdn_scan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, ssm);
+  if (e != cudaSuccess) return e;
+  gdn_wy_kernel<<<(unsigned)wy, 128, wsm, s>>>(tq, tk, a, (uint8_t*)ws);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  gdn_scan_kernel<<<(unsigned)scan, kScThreads, ssm, s>>>(tq, tk, tv, a, (const uint8_t*)ws);
+  return cudaGetLastError();
+}
+
+}  // namespace hla

@@ -752,14 +752,20 @@ static hla_status check_gdn(const gdn_config* c) {
   return HLA_OK;
 }
 
+// Chunks of 64 tokens on the tensor cores, or token by token: by the mean length, which is
+// what the host knows of the lengths.
+static bool gdn_by_chunks(const gdn_config* c, int32_t T) {
+  return c->dtype == HLA_BF16 && c->dk == 128 && c->decay_mode == HLA_DECAY_SCALAR && T >= 32 * (int64_t)c->n_seq;
+}
+
 size_t gdn_workspace_bytes(const gdn_config* cfg, int32_t T) {
   if (check_gdn(cfg) != HLA_OK || T <= 0) return 0;
-  return 256;
+  return gdn_by_chunks(cfg, T) ? align256(hla::gdn_chunk_workspace(T, cfg->n_seq, cfg->H)) : 256;
 }
 
 static hla_status gdn_run(const gdn_config* cfg, const void* q, const void* k, const void* v, const float* alpha,
                           const float* beta, const int32_t* cu, int32_t T, const int32_t* slots,
-                          const float* state_in, float* state_out, void* o, cudaStream_t s) {
+                          const float* state_in, float* state_out, void* o, void* ws, cudaStream_t s) {
   HLA_TRY(need_ptr(q, "q"));
   HLA_TRY(need_ptr(k, "k"));
   HLA_TRY(need_ptr(v, "v"));
@@ -790,7 +796,10 @@ static hla_status gdn_run(const gdn_config* cfg, const void* q, const void* k, c
   a.state_in = state_in;
   a.state_out = state_out;
   a.o = o;
-  HLA_CUDA(hla::launch_gdn_recurrent(a, s), "gated delta rule launch");
+  if (ws != nullptr && gdn_by_chunks(cfg, T))
+    HLA_CUDA(hla::launch_gdn_chunk(a, ws, s), "gated delta rule (chunks) launch");
+  else
+    HLA_CUDA(hla::launch_gdn_recurrent(a, s), "gated delta rule launch");
   return HLA_OK;
 }
 
@@ -808,7 +817,8 @@ hla_status gdn_forward(const gdn_config* cfg, const void* q, const void* k, cons
   if (((uintptr_t)workspace & 255u) != 0) return fail(HLA_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
   const size_t need = gdn_workspace_bytes(cfg, T);
   if (workspace_bytes < need) return fail(HLA_ERR_WORKSPACE, "workspace too small: %zu < %zu", workspace_bytes, need);
-  return gdn_run(cfg, q, k, v, alpha, beta, cu_seqlens, T, slots, state_in, state_out, o, (cudaStream_t)stream);
+  return gdn_run(cfg, q, k, v, alpha, beta, cu_seqlens, T, slots, state_in, state_out, o, workspace,
+                 (cudaStream_t)stream);
 }
 
 hla_status gdn_step(const gdn_config* cfg, const void* q, const void* k, const void* v, const float* alpha,
@@ -816,7 +826,8 @@ hla_status gdn_step(const gdn_config* cfg, const void* q, const void* k, const v
   g_msg[0] = 0;
   HLA_TRY(check_gdn(cfg));
   HLA_TRY(need_ptr(state, "state"));
-  return gdn_run(cfg, q, k, v, alpha, beta, nullptr, cfg->n_seq, slots, state, state, o, (cudaStream_t)stream);
+  return gdn_run(cfg, q, k, v, alpha, beta, nullptr, cfg->n_seq, slots, state, state, o, nullptr,
+                 (cudaStream_t)stream);
 }
 
 hla_status hla_prefill(const hla_config* cfg, const void* q, const void* k, const void* v, const float* alpha,
@@ -1323,6 +1334,8 @@ hla_status hla_device_status(int32_t clear, uint32_t* code_out) {
   HLA_CUDA(hla::read_error_word_chan_prep(&w, clear != 0), "hla_device_status read");
   word |= w;
   HLA_CUDA(hla::read_error_word_gdn_recurrent(&w, clear != 0), "hla_device_status read");
+  word |= w;
+  HLA_CUDA(hla::read_error_word_gdn_chunk(&w, clear != 0), "hla_device_status read");
   word |= w;
   if (code_out) *code_out = word;
   if (word & (hla::kErrMbarTimeout | hla::kErrTmemAlloc))

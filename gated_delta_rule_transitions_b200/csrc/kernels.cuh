@@ -288,6 +288,9 @@ cudaError_t launch_gate_mass(const float* gates, int B, int H, int N, int ncols,
 cudaError_t launch_evict(const EvictArgs& a, cudaStream_t s);
 cudaError_t launch_cache8(const Cache8Args& a, bool close, cudaStream_t s);
 cudaError_t launch_gdn_recurrent(const GdnArgs& a, cudaStream_t s);
+size_t gdn_chunk_workspace(int T, int n_seq, int H);
+cudaError_t launch_gdn_chunk(const GdnArgs& a, void* ws, cudaStream_t s);
+cudaError_t read_error_word_gdn_chunk(unsigned int* out, bool clear);
 cudaError_t read_error_word_gdn_recurrent(unsigned int* out, bool clear);
 cudaError_t launch_wait_check(uint64_t limit_ns, bool complete, cudaStream_t s);
 
