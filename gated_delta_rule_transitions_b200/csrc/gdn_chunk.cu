@@ -14,10 +14,11 @@
 // dim, three products a chunk, each waiting for the one before.
 //
 // Precision.  The state is float32 and stays so: it is held in registers, and what goes into
-// a product (S, R, U, T) goes in as two bf16 numbers, x = hi + lo, hi = bf16(x),
-// lo = bf16(x - hi), off by at most 2^-18 of x; K, Q and V are bf16 already.  Only the lo lo
-// parts are left out (2^-18).  G alone is rounded to one bf16: it reaches the output and
-// nothing else, and the output is bf16.  Decays are differences of 64-bit running sums.
+// a product (S, R, U, T) goes in as three bf16 numbers, x = x1 + x2 + x3, each the rounding
+// of what the ones before it left: 24 bits, off by at most 2^-27 of x (two would be off by
+// 2^-18, 2.8e-6 in the mean, more than float32 sums are).  K, Q and V are bf16 already.  Left
+// out are the products of parts that are 2^-27 and less.  G, which reaches the bf16 output
+// and nothing else, goes in as two.  Decays are differences of 64-bit running sums.
 #include "common.cuh"
 #include "kernels.cuh"
 #include "tc_common.cuh"
@@ -34,7 +35,7 @@ namespace {
 constexpr int kD = 128;
 constexpr int kC = 64;
 constexpr int kTile = kC * 128;               // 8 KiB: 64 rows of 128 bytes, 128-byte swizzle
-constexpr int kWy = 3 * kTile;                // T_hi, G, T_lo of a chunk, as they lie in shared memory
+constexpr int kWy = 5 * kTile;                // T1, G1, T2, G2, T3 of a chunk, as they lie in shared memory
 constexpr int kScal = 2 * kC * 4;             // gamma_t, gamma_C / gamma_t
 constexpr int kSlot = kWy + kScal;            // workspace bytes per (chunk slot, head)
 
@@ -57,10 +58,13 @@ __device__ __forceinline__ int slot_owner(const int32_t* cu, int n_seq, int slot
 
 __device__ __forceinline__ bool good_bounds(int t0, int t1, int T) { return t0 >= 0 && t1 >= t0 && t1 <= T; }
 
-// x as two bf16 numbers, packed for two neighbours.
-__device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
-  hi = tc::pack_bf16x2(a, b);
-  lo = tc::pack_bf16x2(a - tc::bf16lo(hi), b - tc::bf16hi(hi));
+// x as three bf16 numbers, packed for two neighbours.
+__device__ __forceinline__ void split3(float a, float b, uint32_t& p1, uint32_t& p2, uint32_t& p3) {
+  p1 = tc::pack_bf16x2(a, b);
+  a -= tc::bf16lo(p1);
+  b -= tc::bf16hi(p1);
+  p2 = tc::pack_bf16x2(a, b);
+  p3 = tc::pack_bf16x2(a - tc::bf16lo(p2), b - tc::bf16hi(p2));
 }
 
 // Waits for this thread's tensor-memory loads; the registers are operands, so that no use of
@@ -106,8 +110,7 @@ __device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], 
 }
 
 // acc += A (16 x K) B (K x 8), float32 in shared memory (row pitches pa, pb), K a multiple of
-// 8; kExact: each factor as two tf32 numbers (2^-22), else as one (2^-12).
-template <bool kExact>
+// 8; each factor as two tf32 numbers (2^-22).
 __device__ __forceinline__ void rows16(float (&acc)[4], const float* A, int pa, const float* B, int pb, int K,
                                        int lane) {
   const int g = lane >> 2, q = lane & 3;
@@ -115,20 +118,19 @@ __device__ __forceinline__ void rows16(float (&acc)[4], const float* A, int pa, 
     const float a[4] = {A[g * pa + k0 + q], A[(g + 8) * pa + k0 + q], A[g * pa + k0 + q + 4],
                         A[(g + 8) * pa + k0 + q + 4]};
     const float b[2] = {B[(k0 + q) * pb + g], B[(k0 + q + 4) * pb + g]};
-    uint32_t ah[4], bh[2];
+    uint32_t ah[4], bh[2], al[4], bl[2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) ah[i] = tf32(a[i]);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) bh[i] = tf32(b[i]);
-    if (kExact) {
-      uint32_t al[4], bl[2];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) al[i] = tf32(a[i] - __uint_as_float(ah[i]));
-#pragma unroll
-      for (int i = 0; i < 2; ++i) bl[i] = tf32(b[i] - __uint_as_float(bh[i]));
-      mma_tf32(acc, ah, bl);
-      mma_tf32(acc, al, bh);
+    for (int i = 0; i < 4; ++i) {
+      ah[i] = tf32(a[i]);
+      al[i] = tf32(a[i] - __uint_as_float(ah[i]));
     }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      bh[i] = tf32(b[i]);
+      bl[i] = tf32(b[i] - __uint_as_float(bh[i]));
+    }
+    mma_tf32(acc, ah, bl);
+    mma_tf32(acc, al, bh);
     mma_tf32(acc, ah, bh);
   }
 }
@@ -303,7 +305,7 @@ __global__ void __launch_bounds__(128, 3)
     const int ib = blk < 1 ? 1 : (blk < 3 ? 2 : 3);
     const int kb = blk - (ib * (ib - 1)) / 2;
     float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    rows16<true>(acc, Us + 16 * ib * kP + 16 * ib, kP, Ls + 16 * ib * kP + 16 * kb + 8 * nh, kP, 16, lane);
+    rows16(acc, Us + 16 * ib * kP + 16 * ib, kP, Ls + 16 * ib * kP + 16 * kb + 8 * nh, kP, 16, lane);
     store16(Xs + (16 * ib - 16) * kXP + 16 * kb + 8 * nh, kXP, acc, 1.0f, lane);
   }
   __syncthreads();
@@ -312,7 +314,7 @@ __global__ void __launch_bounds__(128, 3)
     for (int u = warp; u < 2 * (4 - lev); u += 4) {
       const int jb = u >> 1, nh = u & 1;
       float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-      rows16<true>(acc, Xs + 16 * (jb + lev - 1) * kXP + 16 * jb, kXP, Us + 16 * jb * kP + 16 * jb + 8 * nh, kP,
+      rows16(acc, Xs + 16 * (jb + lev - 1) * kXP + 16 * jb, kXP, Us + 16 * jb * kP + 16 * jb + 8 * nh, kP,
                    16 * lev, lane);
       store16(Us + 16 * (jb + lev) * kP + 16 * jb + 8 * nh, kP, acc, -1.0f, lane);
     }
@@ -322,31 +324,31 @@ __global__ void __launch_bounds__(128, 3)
   for (int nt = 0; nt < 2 * (warp + 1); ++nt) {
     const int k0 = 16 * (nt >> 1);
     float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    rows16<false>(acc, Ps + 16 * warp * kP + k0, kP, Us + k0 * kP + 8 * nt, kP, 16 * (warp + 1) - k0, lane);
+    rows16(acc, Ps + 16 * warp * kP + k0, kP, Us + k0 * kP + 8 * nt, kP, 16 * (warp + 1) - k0, lane);
     store16(Ls + 16 * warp * kP + 8 * nt, kP, acc, 1.0f, lane);
   }
   __syncthreads();
-  // out: T_hi, G, T_lo as swizzled tiles, then gamma_t and gamma_C / gamma_t
+  // out: the parts of T and G as swizzled tiles, then gamma_t and gamma_C / gamma_t
   uint8_t* out = ws + ((long)slot * a.H + h) * kSlot;
   const int t = tid & (kC - 1);
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     const int c8 = 4 * (tid >> 6) + e;
-    uint32_t th[4] = {0u, 0u, 0u, 0u}, tl[4] = {0u, 0u, 0u, 0u}, gg[4] = {0u, 0u, 0u, 0u};
-    if ((c8 >> 1) <= (t >> 4)) {  // blocks above the diagonal are zero
+    uint32_t w[5][4] = {};  // T1, G1, T2, G2, T3; blocks above the diagonal are zero
+    if ((c8 >> 1) <= (t >> 4)) {
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         const int cc = 8 * c8 + 2 * u;
         const float2 b2 = *(const float2*)(beta_s + cc);
         const float2 x = *(const float2*)(Us + t * kP + cc), y = *(const float2*)(Ls + t * kP + cc);
-        split2(x.x * b2.x, x.y * b2.y, th[u], tl[u]);
-        gg[u] = tc::pack_bf16x2(y.x * b2.x, y.y * b2.y);
+        uint32_t rest;
+        split3(x.x * b2.x, x.y * b2.y, w[0][u], w[2][u], w[4][u]);
+        split3(y.x * b2.x, y.y * b2.y, w[1][u], w[3][u], rest);
       }
     }
     const int at = swz(t, c8);
-    *(uint4*)(out + at) = make_uint4(th[0], th[1], th[2], th[3]);
-    *(uint4*)(out + kTile + at) = make_uint4(gg[0], gg[1], gg[2], gg[3]);
-    *(uint4*)(out + 2 * kTile + at) = make_uint4(tl[0], tl[1], tl[2], tl[3]);
+#pragma unroll
+    for (int p = 0; p < 5; ++p) *(uint4*)(out + p * kTile + at) = make_uint4(w[p][0], w[p][1], w[p][2], w[p][3]);
   }
   float* sc = (float*)(out + kWy);
   if (tid < kC)
@@ -363,41 +365,65 @@ __global__ void __launch_bounds__(128, 3)
 // ---- the walk over a sequence's chunks ---------------------------------------------------
 //
 // One CTA per (sequence, head, 64 value columns): warp 0 loads, warp 1 issues the products,
-// warps 2-5 do the rest.  Two stages of 64.5 KiB.
-//   A  [K; Q] (128 x 128) x S^T (128 x 64, hi and lo)  -> K S^T (rows 0-63), Q S^T (64-127)
-//      rows 0-63: R_t = V_t - gamma_t (K S^T)_t into shared memory (hi, lo); rows 64-127
+// warps 2-9 do the rest (two warps per 32 rows, 32 columns each).  The parts of the right
+// factor lie side by side, so that one instruction reads the left one once for all of them.
+//   A  [K; Q] (128 x 128) x [S1 | S2 | S3] (128 x 192)     -> K S^T (rows 0-63), Q S^T (64-127)
+//      rows 0-63: R_t = V_t - gamma_t (K S^T)_t into shared memory (three parts); rows 64-127
 //      keep gamma_t (Q S^T)_t in registers
-//   B  [T_hi; G] (128 x 64) x R (64 x 64, hi and lo), and T_lo x R_hi -> U (rows 0-63), G R
-//      rows 0-63: diag(gamma_C / gamma_t) U (hi, lo) over R; rows 64-127: the output
-//   C  K^T (128 x 64) x U (64 x 64, hi and lo)         -> S's update, one row k a thread:
-//      S <- gamma_C S + update in registers, and hi, lo of it for the next A.
+//   B  [T1; G1] (128 x 64) x [R1 | R2 | R3] (64 x 192), [T2; G2] x [R1 | R2], [T3; 0] x R1
+//      rows 0-63: diag(gamma_C / gamma_t) U (three parts) over R; rows 64-127: the output
+//   C  K^T (128 x 64) x [U1 | U2 | U3] (64 x 192)          -> S's update, one row k a thread:
+//      S <- gamma_C S + update in registers, and its parts for the next A.
 
 constexpr int kV = 64;                        // value columns per CTA
 constexpr int kStK = 0;                       // stage: [kb][K | Q][64 rows][128 B]
 constexpr int kStV = 4 * kTile;
-constexpr int kStWy = kStV + kTile;           // T_hi, G, T_lo
-constexpr int kStScal = kStWy + kWy;
+constexpr int kStScal = kStV + kTile;
 constexpr int kStage = kStScal + 1024;
 constexpr int kStages = 2;
-constexpr uint32_t kStTx = 5 * kTile + kSlot;
-constexpr int kScS = kStages * kStage;        // S^T hi, lo: 128 rows of 128 B each
-constexpr int kScR = kScS + 4 * kTile;        // R (then U) hi, lo
-constexpr int kScSmall = kScR + 2 * kTile;
-constexpr int kScSmem = kScSmall + 128;
-constexpr int kScThreads = 192;
-constexpr uint32_t kIdescA = tc::idesc_bf16_f32(128, kV, 0, 1);
-constexpr uint32_t kIdescC = tc::idesc_bf16_f32(128, kV, 1, 1);
+constexpr uint32_t kStTx = 5 * kTile + kScal;
+constexpr int kScWy = kStages * kStage;       // T1, G1, T2, G2, T3, zeros
+constexpr int kScS = kScWy + 6 * kTile;       // S^T in three parts: 128 rows of 128 B each
+constexpr int kScR = kScS + 6 * kTile;        // R (then U) in three parts
+constexpr int kScSmall = kScR + 3 * kTile;
+constexpr int kScSmem = kScSmall + 160;
+constexpr int kScThreads = 320;
+constexpr uint32_t kIdescA = tc::idesc_bf16_f32(128, 3 * kV, 0, 1);
+constexpr uint32_t kIdescB2 = tc::idesc_bf16_f32(128, 2 * kV, 0, 1);
+constexpr uint32_t kIdescB3 = tc::idesc_bf16_f32(128, kV, 0, 1);
+constexpr uint32_t kIdescC = tc::idesc_bf16_f32(128, 3 * kV, 1, 1);
+// tensor memory: A and C, then the two accumulators of B
+constexpr uint32_t kTmA = 0, kTmB = 192, kTmB2 = 384;
 
-// 32 float32 values as hi and lo halves of rows of 128 bytes (row r of two swizzled tiles).
-__device__ __forceinline__ void store_split(uint8_t* hi, uint8_t* lo, int r, int half, const float* x) {
+// 32 float32 values as three parts, columns 32 half .. + 31 of rows of 128 bytes (row r of
+// three swizzled tiles, `pitch` bytes apart).
+__device__ __forceinline__ void store_split(uint8_t* dst, int pitch, int r, int half, const float (&x)[32]) {
 #pragma unroll
   for (int p = 0; p < 4; ++p) {
-    uint32_t h[4], l[4];
+    uint32_t w1[4], w2[4], w3[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) split2(x[8 * p + 2 * e], x[8 * p + 2 * e + 1], h[e], l[e]);
+    for (int e = 0; e < 4; ++e) split3(x[8 * p + 2 * e], x[8 * p + 2 * e + 1], w1[e], w2[e], w3[e]);
     const int at = swz(r, 4 * half + p);
-    *(uint4*)(hi + at) = make_uint4(h[0], h[1], h[2], h[3]);
-    *(uint4*)(lo + at) = make_uint4(l[0], l[1], l[2], l[3]);
+    *(uint4*)(dst + at) = make_uint4(w1[0], w1[1], w1[2], w1[3]);
+    *(uint4*)(dst + pitch + at) = make_uint4(w2[0], w2[1], w2[2], w2[3]);
+    *(uint4*)(dst + 2 * pitch + at) = make_uint4(w3[0], w3[1], w3[2], w3[3]);
+  }
+}
+
+// Sum of kN accumulators, 64 columns apart, on 32 columns.
+template <int kN>
+__device__ __forceinline__ void sum_parts(uint32_t addr, float (&x)[32]) {
+  uint32_t y[kN][32];
+#pragma unroll
+  for (int p = 0; p < kN; ++p) tc::tmem_ld32(addr + 64 * p, y[p]);
+#pragma unroll
+  for (int p = 0; p < kN; ++p) wait_ld(y[p]);
+#pragma unroll
+  for (int v = 0; v < 32; ++v) {
+    float s = __uint_as_float(y[kN - 1][v]);  // the smallest first
+#pragma unroll
+    for (int p = kN - 2; p >= 0; --p) s += __uint_as_float(y[p][v]);
+    x[v] = s;
   }
 }
 
@@ -408,8 +434,9 @@ __global__ void __launch_bounds__(kScThreads, 1)
   uint8_t* sm = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   uint64_t* full = (uint64_t*)(sm + kScSmall);
   uint64_t* empty = full + kStages;
-  uint64_t* doneA = empty + kStages;
-  uint64_t* doneB = doneA + 1;
+  uint64_t* wfull = empty + kStages;
+  uint64_t* doneA = wfull + 1;
+  uint64_t* doneB = doneA + 1;   // also: T and G are free
   uint64_t* doneC = doneB + 1;
   uint64_t* s_ready = doneC + 1;
   uint64_t* r_ready = s_ready + 1;
@@ -461,22 +488,25 @@ __global__ void __launch_bounds__(kScThreads, 1)
       tc::mbar_init(&full[s], 1);
       tc::mbar_init(&empty[s], 1);
     }
+    tc::mbar_init(wfull, 1);
     tc::mbar_init(doneA, 1);
     tc::mbar_init(doneB, 1);
     tc::mbar_init(doneC, 1);
-    tc::mbar_init(s_ready, 4);
-    tc::mbar_init(r_ready, 2);
-    tc::mbar_init(u_ready, 2);
+    tc::mbar_init(s_ready, 8);
+    tc::mbar_init(r_ready, 4);
+    tc::mbar_init(u_ready, 8);
     tc::mbar_init(fin, 1);
     *abort_s = 0;
     tc::mbar_fence_init();
-    tc::fence_async_smem();
   }
-  if (warp == 1) tc::tmem_alloc(tmem_s, 256);
+  for (int e = tid; e < kTile / 16; e += kScThreads)
+    *(uint4*)(sm + kScWy + 5 * kTile + 16 * e) = make_uint4(0u, 0u, 0u, 0u);
+  tc::fence_async_smem();
+  if (warp == 1) tc::tmem_alloc(tmem_s, 512);
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
-  const uint32_t tm = *tmem_s;  // columns 0-63: A, 64-127: B, 128-191: T_lo R_hi, 192-255: C
+  const uint32_t tm = *tmem_s;
 
   if (warp == 0) {
     // ---------------- loads ----------------
@@ -484,10 +514,10 @@ __global__ void __launch_bounds__(kScThreads, 1)
       tc::tma_prefetch_desc(&tmQ);
       tc::tma_prefetch_desc(&tmK);
       tc::tma_prefetch_desc(&tmV);
-      int c = 0;
-      for (; c < nc; ++c) {
+      const uint8_t* wy = ws + ((long)base * a.H + h) * kSlot;
+      auto load_stage = [&](int c) {
         const int st = c % kStages;
-        if (c >= kStages && !tc::mbar_wait(&empty[st], ((c / kStages) - 1) & 1, abort_s)) break;
+        if (c >= kStages && !tc::mbar_wait(&empty[st], ((c / kStages) - 1) & 1, abort_s)) return false;
         uint8_t* dst = sm + st * kStage;
         const int y = s0 + c * kC;
         tc::mbar_arrive_expect_tx(&full[st], kStTx);
@@ -496,51 +526,67 @@ __global__ void __launch_bounds__(kScThreads, 1)
           tc::tma_load_2d(dst + kStK + kb * 2 * kTile + kTile, &tmQ, hk * kD + 64 * kb, y, &full[st]);
         }
         tc::tma_load_2d(dst + kStV, &tmV, h * kD + vh * kV, y, &full[st]);
-        tc::bulk_load_1d(dst + kStWy, ws + ((long)(base + c) * a.H + h) * kSlot, kSlot, &full[st]);
+        tc::bulk_load_1d(dst + kStScal, wy + (long)c * a.H * kSlot + kWy, kScal, &full[st]);
+        return true;
+      };
+      int c = 0, stages = 0;  // loads issued
+      if (load_stage(0)) ++stages;
+      for (; c < nc; ++c) {
+        if (c > 0 && !tc::mbar_wait(doneB, (c - 1) & 1, abort_s)) break;
+        tc::mbar_arrive_expect_tx(wfull, kWy);
+        tc::bulk_load_1d(sm + kScWy, wy + (long)c * a.H * kSlot, kWy, wfull);
+        if (c + 1 < nc) {
+          if (!load_stage(c + 1)) {
+            ++c;
+            break;
+          }
+          ++stages;
+        }
       }
-      if (*abort_s)  // never leave the CTA with copies in flight
-        for (int t = max(0, c - kStages); t < c; ++t)
+      if (*abort_s) {  // never leave the CTA with copies in flight
+        for (int t = max(0, stages - kStages); t < stages; ++t)
           tc::mbar_wait(&full[t % kStages], (t / kStages) & 1, nullptr, 200000000ull);
+        if (c > 0) tc::mbar_wait(wfull, (c - 1) & 1, nullptr, 200000000ull);
+      }
     }
     __syncwarp();
   } else if (warp == 1) {
     // ---------------- products ----------------
     if (lane == 0) {
-      const uint32_t s_hi = tc::smem_u32(sm + kScS), s_lo = s_hi + 2 * kTile;
-      const uint32_t r_hi = tc::smem_u32(sm + kScR), r_lo = r_hi + kTile;
+      const uint32_t sb = tc::smem_u32(sm + kScS), rb = tc::smem_u32(sm + kScR), wb = tc::smem_u32(sm + kScWy);
       for (int c = 0; c < nc; ++c) {
         const int st = c % kStages;
         const uint32_t par = (uint32_t)c & 1;
-        const uint32_t stage = tc::smem_u32(sm + st * kStage);
+        const uint32_t kb = tc::smem_u32(sm + st * kStage + kStK);
         if (!tc::mbar_wait(&full[st], (uint32_t)(c / kStages) & 1, abort_s) || !tc::mbar_wait(s_ready, par, abort_s))
           break;
         tc::tc_fence_after();
 #pragma unroll
-        for (int p = 0; p < 2; ++p)
-#pragma unroll
-          for (int ks = 0; ks < kD / 16; ++ks)
-            tc::mma_ss(tm, tc::sdesc_sw128(stage + kStK + (ks >> 2) * 2 * kTile + (ks & 3) * 32, 16, 1024),
-                       tc::sdesc_sw128((p ? s_lo : s_hi) + ks * 2048, kTile, 1024), kIdescA, (p | ks) > 0 ? 1u : 0u);
+        for (int ks = 0; ks < kD / 16; ++ks)
+          tc::mma_ss(tm + kTmA, tc::sdesc_sw128(kb + (ks >> 2) * 2 * kTile + (ks & 3) * 32, 16, 1024),
+                     tc::sdesc_sw128(sb + ks * 2048, 2 * kTile, 1024), kIdescA, ks > 0 ? 1u : 0u);
         tc::mma_commit(doneA);
-        if (!tc::mbar_wait(r_ready, par, abort_s)) break;
+        if (!tc::mbar_wait(wfull, par, abort_s) || !tc::mbar_wait(r_ready, par, abort_s)) break;
         tc::tc_fence_after();
 #pragma unroll
-        for (int p = 0; p < 3; ++p)
+        for (int ks = 0; ks < kC / 16; ++ks)
+          tc::mma_ss(tm + kTmB, tc::sdesc_sw128(wb + ks * 32, 16, 1024), tc::sdesc_sw128(rb + ks * 2048, kTile, 1024),
+                     kIdescA, ks > 0 ? 1u : 0u);
 #pragma unroll
-          for (int ks = 0; ks < kC / 16; ++ks)  // p: T_hi R_hi, T_hi R_lo, T_lo R_hi (its rows 64-127 are not read)
-            tc::mma_ss(tm + (p == 2 ? 128 : 64),
-                       tc::sdesc_sw128(stage + kStWy + (p == 2 ? 2 * kTile : 0) + ks * 32, 16, 1024),
-                       tc::sdesc_sw128((p == 1 ? r_lo : r_hi) + ks * 2048, kTile, 1024), kIdescA,
-                       (p == 1 || ks > 0) ? 1u : 0u);
+        for (int ks = 0; ks < kC / 16; ++ks)
+          tc::mma_ss(tm + kTmB2, tc::sdesc_sw128(wb + 2 * kTile + ks * 32, 16, 1024),
+                     tc::sdesc_sw128(rb + ks * 2048, kTile, 1024), kIdescB2, ks > 0 ? 1u : 0u);
+#pragma unroll
+        for (int ks = 0; ks < kC / 16; ++ks)
+          tc::mma_ss(tm + kTmB2, tc::sdesc_sw128(wb + 4 * kTile + ks * 32, 16, 1024),
+                     tc::sdesc_sw128(rb + ks * 2048, kTile, 1024), kIdescB3, 1u);
         tc::mma_commit(doneB);
         if (!tc::mbar_wait(u_ready, par, abort_s)) break;
         tc::tc_fence_after();
 #pragma unroll
-        for (int p = 0; p < 2; ++p)
-#pragma unroll
-          for (int ks = 0; ks < kC / 16; ++ks)
-            tc::mma_ss(tm + 192, tc::sdesc_sw128(stage + kStK + ks * 2048, 2 * kTile, 1024),
-                       tc::sdesc_sw128((p ? r_lo : r_hi) + ks * 2048, kTile, 1024), kIdescC, (p | ks) > 0 ? 1u : 0u);
+        for (int ks = 0; ks < kC / 16; ++ks)
+          tc::mma_ss(tm + kTmA, tc::sdesc_sw128(kb + ks * 2048, 2 * kTile, 1024),
+                     tc::sdesc_sw128(rb + ks * 2048, kTile, 1024), kIdescC, ks > 0 ? 1u : 0u);
         tc::mma_commit(doneC);
         tc::mma_commit(&empty[st]);
       }
@@ -550,22 +596,17 @@ __global__ void __launch_bounds__(kScThreads, 1)
     }
     __syncwarp();
   } else {
-    // ---------------- warps 2-5: row r of every product ----------------
+    // ---------------- warps 2-9: row r, column half ch of every product ----------------
     const int q = warp & 3;            // tensor-memory lanes of this warp
+    const int ch = (warp - 2) >> 2;
     const int r = 32 * q + lane;       // A, B: token r & 63; C and S: key channel r
     const int t = r & (kC - 1);
     const bool low = r < kC;
-    const uint32_t row = tm + ((uint32_t)(32 * q) << 16);
-    uint8_t* sh = sm + kScS;
-    uint8_t* rh = sm + kScR;
-    float S[kV];
-    if (a.state_in != nullptr) {
+    const uint32_t row = tm + ((uint32_t)(32 * q) << 16) + 32 * ch;
+    const long srow = soff + (long)(32 * ch) * kD + r;
+    float S[32];
 #pragma unroll
-      for (int v = 0; v < kV; ++v) S[v] = a.state_in[soff + (long)v * kD + r];
-    } else {
-#pragma unroll
-      for (int v = 0; v < kV; ++v) S[v] = 0.0f;
-    }
+    for (int v = 0; v < 32; ++v) S[v] = a.state_in != nullptr ? a.state_in[srow + (long)v * kD] : 0.0f;
     bool ok = true;
     for (int c = 0; c < nc; ++c) {
       const int st = c % kStages;
@@ -573,17 +614,14 @@ __global__ void __launch_bounds__(kScThreads, 1)
       uint8_t* stage = sm + st * kStage;
       const float* sc = (const float*)(stage + kStScal);
       const int n = min(kC, len - c * kC);
-      store_split(sh, sh + 2 * kTile, r, 0, S);
-      store_split(sh, sh + 2 * kTile, r, 1, S + 32);
-      ok = tc::mbar_wait(&full[st], (uint32_t)(c / kStages) & 1, abort_s);
+      store_split(sm + kScS, 2 * kTile, r, ch, S);
+      ok = tc::mbar_wait_warp(&full[st], (uint32_t)(c / kStages) & 1, abort_s);
       if (!ok) break;
       if (n < kC && low && t >= n) {
-        // keys behind the sequence belong to another one, or to none: zero
+        // keys behind the sequence belong to another one, or to none: zero (key half ch)
 #pragma unroll
-        for (int c8 = 0; c8 < 8; ++c8) {
-          *(uint4*)(stage + kStK + t * 128 + 16 * c8) = make_uint4(0u, 0u, 0u, 0u);
-          *(uint4*)(stage + kStK + 2 * kTile + t * 128 + 16 * c8) = make_uint4(0u, 0u, 0u, 0u);
-        }
+        for (int c8 = 0; c8 < 8; ++c8)
+          *(uint4*)(stage + kStK + ch * 2 * kTile + t * 128 + 16 * c8) = make_uint4(0u, 0u, 0u, 0u);
       }
       // (read before this warp's s_ready: the stage may be refilled as soon as C is done)
       const float gt = sc[t], dt = sc[kC + t], gC = sc[kC - 1];
@@ -594,97 +632,81 @@ __global__ void __launch_bounds__(kScThreads, 1)
       ok = tc::mbar_wait_warp(doneA, par, abort_s);
       if (!ok) break;
       tc::tc_fence_after();
-      uint32_t x[2][32];  // K S^T or Q S^T
-      tc::tmem_ld32(row, x[0]);
-      tc::tmem_ld32(row + 32, x[1]);
-      wait_ld(x[0]);
-      wait_ld(x[1]);
+      float x[32];  // K S^T or Q S^T
+      sum_parts<3>(row + kTmA, x);
       if (low) {
         // R_t, zero behind the sequence
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          float f[32];
+        for (int p = 0; p < 4; ++p) {
+          const uint4 w = *(const uint4*)(stage + kStV + swz(t, 4 * ch + p));
+          const uint32_t vw[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-          for (int p = 0; p < 4; ++p) {
-            const uint4 w = *(const uint4*)(stage + kStV + swz(t, 4 * half + p));
-            const uint32_t vw[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int v = 8 * p + 2 * e;
-              f[v] = t < n ? fmaf(-gt, __uint_as_float(x[half][v]), tc::bf16lo(vw[e])) : 0.0f;
-              f[v + 1] = t < n ? fmaf(-gt, __uint_as_float(x[half][v + 1]), tc::bf16hi(vw[e])) : 0.0f;
-            }
+          for (int e = 0; e < 4; ++e) {
+            const int v = 8 * p + 2 * e;
+            x[v] = t < n ? fmaf(-gt, x[v], tc::bf16lo(vw[e])) : 0.0f;
+            x[v + 1] = t < n ? fmaf(-gt, x[v + 1], tc::bf16hi(vw[e])) : 0.0f;
           }
-          store_split(rh, rh + kTile, t, half, f);
         }
+        store_split(sm + kScR, kTile, t, ch, x);
         tc::fence_async_smem();
         tc::tc_fence_before();
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(r_ready);
+      } else {
+        // C may take A's columns now
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(u_ready);
       }
       ok = tc::mbar_wait_warp(doneB, par, abort_s);
       if (!ok) break;
       tc::tc_fence_after();
       if (low) {
+        float y[32];
+        sum_parts<3>(row + kTmB, x);
+        sum_parts<2>(row + kTmB2, y);
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          uint32_t y[32], z[32];
-          tc::tmem_ld32(row + 64 + 32 * half, y);
-          tc::tmem_ld32(row + 128 + 32 * half, z);
-          wait_ld(y);
-          wait_ld(z);
-          float f[32];
-#pragma unroll
-          for (int v = 0; v < 32; ++v) f[v] = dt * (__uint_as_float(y[v]) + __uint_as_float(z[v]));
-          store_split(rh, rh + kTile, t, half, f);
-        }
+        for (int v = 0; v < 32; ++v) x[v] = dt * (x[v] + y[v]);
+        store_split(sm + kScR, kTile, t, ch, x);
         tc::fence_async_smem();
         tc::tc_fence_before();
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(u_ready);
       } else {
-        __nv_bfloat16* orow = (__nv_bfloat16*)a.o + ((long)(s0 + c * kC + t) * a.H + h) * kD + vh * kV;
+        float y[32], z[32];
+        sum_parts<2>(row + kTmB, y);
+        sum_parts<1>(row + kTmB2, z);
+        if (t < n) {
+          __nv_bfloat16* orow =
+              (__nv_bfloat16*)a.o + ((long)(s0 + c * kC + t) * a.H + h) * kD + vh * kV + 32 * ch;
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          uint32_t y[32];
-          tc::tmem_ld32(row + 64 + 32 * half, y);
-          wait_ld(y);
-          if (t < n) {
+          for (int p = 0; p < 4; ++p) {
+            uint32_t w[4];
 #pragma unroll
-            for (int p = 0; p < 4; ++p) {
-              uint32_t w[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const int v = 8 * p + 2 * e;
-                w[e] = tc::pack_bf16x2(fmaf(gt, __uint_as_float(x[half][v]), __uint_as_float(y[v])),
-                                       fmaf(gt, __uint_as_float(x[half][v + 1]), __uint_as_float(y[v + 1])));
-              }
-              *(uint4*)(orow + 32 * half + 8 * p) = make_uint4(w[0], w[1], w[2], w[3]);
+            for (int e = 0; e < 4; ++e) {
+              const int v = 8 * p + 2 * e;
+              w[e] = tc::pack_bf16x2(fmaf(gt, x[v], y[v] + z[v]), fmaf(gt, x[v + 1], y[v + 1] + z[v + 1]));
             }
+            *(uint4*)(orow + 8 * p) = make_uint4(w[0], w[1], w[2], w[3]);
           }
         }
       }
       ok = tc::mbar_wait_warp(doneC, par, abort_s);
       if (!ok) break;
       tc::tc_fence_after();
+      sum_parts<3>(row + kTmA, x);
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        uint32_t z[32];
-        tc::tmem_ld32(row + 192 + 32 * half, z);
-        wait_ld(z);
-#pragma unroll
-        for (int v = 0; v < 32; ++v) S[32 * half + v] = fmaf(gC, S[32 * half + v], __uint_as_float(z[v]));
-      }
+      for (int v = 0; v < 32; ++v) S[v] = fmaf(gC, S[v], x[v]);
     }
     if (ok && a.state_out != nullptr) {
 #pragma unroll
-      for (int v = 0; v < kV; ++v) a.state_out[soff + (long)v * kD + r] = S[v];
+      for (int v = 0; v < 32; ++v) a.state_out[srow + (long)v * kD] = S[v];
     }
   }
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
-  if (warp == 1) tc::tmem_dealloc(tm, 256);
+  if (warp == 1) tc::tmem_dealloc(tm, 512);
   if (tid == 0 && *abort_s) report_device_error(kErrMbarTimeout);
 }
 
