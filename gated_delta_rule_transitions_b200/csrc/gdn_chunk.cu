@@ -35,9 +35,14 @@ namespace {
 constexpr int kD = 128;
 constexpr int kC = 64;
 constexpr int kTile = kC * 128;               // 8 KiB: 64 rows of 128 bytes, 128-byte swizzle
-constexpr int kWy = 5 * kTile;                // T1, G1, T2, G2, T3 of a chunk, as they lie in shared memory
+constexpr int kWy = 5 * kTile;                // [T1; G1], [T2; G2], T3 of a chunk, as they lie in shared memory
 constexpr int kScal = 2 * kC * 4;             // gamma_t, gamma_C / gamma_t
 constexpr int kSlot = kWy + kScal;            // workspace bytes per (chunk slot, head)
+
+// Rows of a stacked left factor [X; Y] (64 rows each): 16 of X, 16 of Y, and so on, so that each
+// quarter of tensor memory's lanes (one warp's reach) gets 16 rows of either product and no
+// warp is without work in any step.  Row of X's row t (Y's is 16 further on):
+__device__ __forceinline__ int stacked(int t) { return 32 * (t >> 4) + (t & 15); }
 
 __device__ __forceinline__ int swz(int row, int chunk) { return row * 128 + ((chunk ^ (row & 7)) << 4); }
 
@@ -109,29 +114,40 @@ __device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
 }
 
-// acc += A (16 x K) B (K x 8), float32 in shared memory (row pitches pa, pb), K a multiple of
-// 8; each factor as two tf32 numbers (2^-22).
-__device__ __forceinline__ void rows16(float (&acc)[4], const float* A, int pa, const float* B, int pb, int K,
-                                       int lane) {
+// Float32 fragments as two tf32 numbers each (2^-22).
+__device__ __forceinline__ void frag_a(const float* A, int pa, int lane, uint32_t (&h)[4], uint32_t (&l)[4]) {
   const int g = lane >> 2, q = lane & 3;
-  for (int k0 = 0; k0 < K; k0 += 8) {
-    const float a[4] = {A[g * pa + k0 + q], A[(g + 8) * pa + k0 + q], A[g * pa + k0 + q + 4],
-                        A[(g + 8) * pa + k0 + q + 4]};
-    const float b[2] = {B[(k0 + q) * pb + g], B[(k0 + q + 4) * pb + g]};
-    uint32_t ah[4], bh[2], al[4], bl[2];
+  const float a[4] = {A[g * pa + q], A[(g + 8) * pa + q], A[g * pa + q + 4], A[(g + 8) * pa + q + 4]};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      ah[i] = tf32(a[i]);
-      al[i] = tf32(a[i] - __uint_as_float(ah[i]));
-    }
+  for (int i = 0; i < 4; ++i) {
+    h[i] = tf32(a[i]);
+    l[i] = tf32(a[i] - __uint_as_float(h[i]));
+  }
+}
+
+// acc[j] += A (16 x 16) B (16 x 8 kN)'s column tile j, float32 in shared memory (row pitches
+// pa, pb).
+template <int kN>
+__device__ __forceinline__ void block16(float (&acc)[kN][4], const float* A, int pa, const float* B, int pb,
+                                        int lane) {
+  const int g = lane >> 2, q = lane & 3;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      bh[i] = tf32(b[i]);
-      bl[i] = tf32(b[i] - __uint_as_float(bh[i]));
+  for (int k0 = 0; k0 < 16; k0 += 8) {
+    uint32_t ah[4], al[4];
+    frag_a(A + k0, pa, lane, ah, al);
+#pragma unroll
+    for (int j = 0; j < kN; ++j) {
+      const float b[2] = {B[(k0 + q) * pb + 8 * j + g], B[(k0 + q + 4) * pb + 8 * j + g]};
+      uint32_t bh[2], bl[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        bh[i] = tf32(b[i]);
+        bl[i] = tf32(b[i] - __uint_as_float(bh[i]));
+      }
+      mma_tf32(acc[j], ah, bl);
+      mma_tf32(acc[j], al, bh);
+      mma_tf32(acc[j], ah, bh);
     }
-    mma_tf32(acc, ah, bl);
-    mma_tf32(acc, al, bh);
-    mma_tf32(acc, ah, bh);
   }
 }
 
@@ -289,10 +305,16 @@ __global__ void __launch_bounds__(128, 3)
     float x[16];
 #pragma unroll
     for (int tl = 0; tl < 16; ++tl) {
-      const float* Lrow = Ls + (16 * k + tl) * kP + 16 * k;
+      const float4* Lrow = (const float4*)(Ls + (16 * k + tl) * kP + 16 * k);
       float v = tl == cc ? 1.0f : 0.0f;
 #pragma unroll
-      for (int sl = 0; sl < tl; ++sl) v = fmaf(-Lrow[sl], x[sl], v);
+      for (int s4 = 0; s4 < tl; s4 += 4) {
+        const float4 w = Lrow[s4 >> 2];
+        v = fmaf(-w.x, x[s4], v);
+        if (s4 + 1 < tl) v = fmaf(-w.y, x[s4 + 1], v);
+        if (s4 + 2 < tl) v = fmaf(-w.z, x[s4 + 2], v);
+        if (s4 + 3 < tl) v = fmaf(-w.w, x[s4 + 3], v);
+      }
       x[tl] = v;
     }
 #pragma unroll
@@ -304,28 +326,44 @@ __global__ void __launch_bounds__(128, 3)
     const int u = warp + 4 * r, blk = u >> 1, nh = u & 1;
     const int ib = blk < 1 ? 1 : (blk < 3 ? 2 : 3);
     const int kb = blk - (ib * (ib - 1)) / 2;
-    float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    rows16(acc, Us + 16 * ib * kP + 16 * ib, kP, Ls + 16 * ib * kP + 16 * kb + 8 * nh, kP, 16, lane);
-    store16(Xs + (16 * ib - 16) * kXP + 16 * kb + 8 * nh, kXP, acc, 1.0f, lane);
+    float acc[1][4] = {};
+    block16<1>(acc, Us + 16 * ib * kP + 16 * ib, kP, Ls + 16 * ib * kP + 16 * kb + 8 * nh, kP, lane);
+    store16(Xs + (16 * ib - 16) * kXP + 16 * kb + 8 * nh, kXP, acc[0], 1.0f, lane);
   }
   __syncthreads();
 #pragma unroll
   for (int lev = 1; lev <= 3; ++lev) {
     for (int u = warp; u < 2 * (4 - lev); u += 4) {
       const int jb = u >> 1, nh = u & 1;
-      float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-      rows16(acc, Xs + 16 * (jb + lev - 1) * kXP + 16 * jb, kXP, Us + 16 * jb * kP + 16 * jb + 8 * nh, kP,
-                   16 * lev, lane);
-      store16(Us + 16 * (jb + lev) * kP + 16 * jb + 8 * nh, kP, acc, -1.0f, lane);
+      float acc[1][4] = {};
+#pragma unroll
+      for (int k = 0; k < lev; ++k)
+        block16<1>(acc, Xs + 16 * (jb + lev - 1) * kXP + 16 * (jb + k), kXP, Us + 16 * (jb + k) * kP + 16 * jb + 8 * nh,
+                   kP, lane);
+      store16(Us + 16 * (jb + lev) * kP + 16 * jb + 8 * nh, kP, acc[0], -1.0f, lane);
     }
     __syncthreads();
   }
-  // G = P U diag(beta) over L (no longer needed); warp = block of 16 rows
-  for (int nt = 0; nt < 2 * (warp + 1); ++nt) {
-    const int k0 = 16 * (nt >> 1);
-    float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    rows16(acc, Ps + 16 * warp * kP + k0, kP, Us + k0 * kP + 8 * nt, kP, 16 * (warp + 1) - k0, lane);
-    store16(Ls + 16 * warp * kP + 8 * nt, kP, acc, 1.0f, lane);
+  // G = P U over L (no longer needed), blocks (i, j), j <= i, of i - j + 1 products: 5 a warp
+  auto g_block = [&](int i, int j) {
+    float acc[2][4] = {};
+    for (int k = j; k <= i; ++k)
+      block16<2>(acc, Ps + 16 * i * kP + 16 * k, kP, Us + 16 * k * kP + 16 * j, kP, lane);
+    store16(Ls + 16 * i * kP + 16 * j, kP, acc[0], 1.0f, lane);
+    store16(Ls + 16 * i * kP + 16 * j + 8, kP, acc[1], 1.0f, lane);
+  };
+  if (warp == 0) {
+    g_block(3, 0);
+    g_block(0, 0);
+  } else if (warp == 1) {
+    g_block(3, 1);
+    g_block(3, 2);
+  } else if (warp == 2) {
+    g_block(2, 0);
+    g_block(2, 1);
+  } else {
+    g_block(1, 0);
+    for (int i = 1; i < 4; ++i) g_block(i, i);
   }
   __syncthreads();
   // out: the parts of T and G as swizzled tiles, then gamma_t and gamma_C / gamma_t
@@ -334,7 +372,7 @@ __global__ void __launch_bounds__(128, 3)
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     const int c8 = 4 * (tid >> 6) + e;
-    uint32_t w[5][4] = {};  // T1, G1, T2, G2, T3; blocks above the diagonal are zero
+    uint32_t w[5][4] = {};  // T1, G1, T2, G2, T3 (blocks above the diagonal are zero)
     if ((c8 >> 1) <= (t >> 4)) {
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
@@ -346,9 +384,11 @@ __global__ void __launch_bounds__(128, 3)
         split3(y.x * b2.x, y.y * b2.y, w[1][u], w[3][u], rest);
       }
     }
-    const int at = swz(t, c8);
 #pragma unroll
-    for (int p = 0; p < 5; ++p) *(uint4*)(out + p * kTile + at) = make_uint4(w[p][0], w[p][1], w[p][2], w[p][3]);
+    for (int p = 0; p < 5; ++p) {
+      const int row = p < 4 ? stacked(t) + 16 * (p & 1) : t;
+      *(uint4*)(out + 2 * (p >> 1) * kTile + swz(row, c8)) = make_uint4(w[p][0], w[p][1], w[p][2], w[p][3]);
+    }
   }
   float* sc = (float*)(out + kWy);
   if (tid < kC)
@@ -364,75 +404,152 @@ __global__ void __launch_bounds__(128, 3)
 
 // ---- the walk over a sequence's chunks ---------------------------------------------------
 //
-// One CTA per (sequence, head, 64 value columns): warp 0 loads, warp 1 issues the products,
-// warps 2-9 do the rest (two warps per 32 rows, 32 columns each).  The parts of the right
-// factor lie side by side, so that one instruction reads the left one once for all of them.
-//   A  [K; Q] (128 x 128) x [S1 | S2 | S3] (128 x 192)     -> K S^T (rows 0-63), Q S^T (64-127)
-//      rows 0-63: R_t = V_t - gamma_t (K S^T)_t into shared memory (three parts); rows 64-127
-//      keep gamma_t (Q S^T)_t in registers
-//   B  [T1; G1] (128 x 64) x [R1 | R2 | R3] (64 x 192), [T2; G2] x [R1 | R2], [T3; 0] x R1
-//      rows 0-63: diag(gamma_C / gamma_t) U (three parts) over R; rows 64-127: the output
-//   C  K^T (128 x 64) x [U1 | U2 | U3] (64 x 192)          -> S's update, one row k a thread:
+// One CTA per (sequence, head, kV value columns): warp 0 loads, warp 1 issues the products,
+// warps 2-9 do the rest.  The parts of the right factor lie side by side, so that one
+// instruction reads the left one once for all of them.
+//   A  [K; Q] (128 x 128) x [S1 | S2 | S3]     -> K S^T and Q S^T (rows as in stacked())
+//      R_t = V_t - gamma_t (K S^T)_t into shared memory (three parts); gamma_t (Q S^T)_t stays
+//      in registers
+//   B  [T1; G1] (128 x 64) x [R1 | R2 | R3], [T2; G2] x [R1 | R2], [T3; 0] x R1
+//      diag(gamma_C / gamma_t) U (three parts) over R; then, beside C, the output
+//   C  K^T (128 x 64) x [U1 | U2 | U3]          -> S's update, one row k a thread:
 //      S <- gamma_C S + update in registers, and its parts for the next A.
+// What bounds it is the chain: three products, each with its way through tensor memory and
+// registers to the next one's operand, and nothing to overlap them with but the output.
 
-constexpr int kV = 64;                        // value columns per CTA
-constexpr int kStK = 0;                       // stage: [kb][K | Q][64 rows][128 B]
-constexpr int kStV = 4 * kTile;
+constexpr int kStKQ = 0;                      // stage: [kb][K, Q stacked: 128 rows][128 B]
+constexpr int kStV = 4 * kTile;               // 64 value columns
 constexpr int kStScal = kStV + kTile;
 constexpr int kStage = kStScal + 1024;
 constexpr int kStages = 2;
 constexpr uint32_t kStTx = 5 * kTile + kScal;
-constexpr int kScWy = kStages * kStage;       // T1, G1, T2, G2, T3, zeros
-constexpr int kScS = kScWy + 6 * kTile;       // S^T in three parts: 128 rows of 128 B each
-constexpr int kScR = kScS + 6 * kTile;        // R (then U) in three parts
-constexpr int kScSmall = kScR + 3 * kTile;
-constexpr int kScSmem = kScSmall + 160;
 constexpr int kScThreads = 320;
-constexpr uint32_t kIdescA = tc::idesc_bf16_f32(128, 3 * kV, 0, 1);
-constexpr uint32_t kIdescB2 = tc::idesc_bf16_f32(128, 2 * kV, 0, 1);
-constexpr uint32_t kIdescB3 = tc::idesc_bf16_f32(128, kV, 0, 1);
-constexpr uint32_t kIdescC = tc::idesc_bf16_f32(128, 3 * kV, 1, 1);
-// tensor memory: A and C, then the two accumulators of B
-constexpr uint32_t kTmA = 0, kTmB = 192, kTmB2 = 384;
 
-// 32 float32 values as three parts, columns 32 half .. + 31 of rows of 128 bytes (row r of
-// three swizzled tiles, `pitch` bytes apart).
-__device__ __forceinline__ void store_split(uint8_t* dst, int pitch, int r, int half, const float (&x)[32]) {
-#pragma unroll
-  for (int p = 0; p < 4; ++p) {
-    uint32_t w1[4], w2[4], w3[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) split3(x[8 * p + 2 * e], x[8 * p + 2 * e + 1], w1[e], w2[e], w3[e]);
-    const int at = swz(r, 4 * half + p);
-    *(uint4*)(dst + at) = make_uint4(w1[0], w1[1], w1[2], w1[3]);
-    *(uint4*)(dst + pitch + at) = make_uint4(w2[0], w2[1], w2[2], w2[3]);
-    *(uint4*)(dst + 2 * pitch + at) = make_uint4(w3[0], w3[1], w3[2], w3[3]);
-  }
+// A right factor of kV columns in three parts: 64-column atoms (128-byte rows) of `rows` rows.
+// kV = 64: an atom per part; kV = 32: parts 1 and 2 share the first.
+template <int kV>
+struct Geo {
+  static constexpr int kAtoms = kV == 64 ? 3 : 2;
+  static constexpr int kHalf = kV / 2;        // columns per warp
+  static constexpr int kPieces = kHalf / 8;   // 16-byte pieces of a row per warp and part
+  static constexpr int kWyAt = kStages * kStage;         // [T1; G1], [T2; G2], [T3; 0]
+  static constexpr int kSAt = kWyAt + 6 * kTile;         // S^T: 128 rows
+  static constexpr int kRAt = kSAt + kAtoms * 2 * kTile; // R, then U: 64 rows
+  static constexpr int kSmallAt = kRAt + kAtoms * kTile;
+  static constexpr int kSmem = kSmallAt + 160;
+  static constexpr uint32_t kIdescA = tc::idesc_bf16_f32(128, 3 * kV, 0, 1);
+  static constexpr uint32_t kIdescB2 = tc::idesc_bf16_f32(128, 2 * kV, 0, 1);
+  static constexpr uint32_t kIdescB3 = tc::idesc_bf16_f32(128, kV, 0, 1);
+  static constexpr uint32_t kIdescC = tc::idesc_bf16_f32(128, 3 * kV, 1, 1);
+  // tensor memory columns: A and C, then the two accumulators of B
+  static constexpr uint32_t kTmA = 0, kTmB = 3 * kV, kTmB2 = 6 * kV, kTmCols = 8 * kV;
+  // byte offset of part p's atom, and the 16-byte piece its columns start at
+  static __device__ __forceinline__ int atom(int p, int rows) { return (kV == 64 ? p : p >> 1) * rows * 128; }
+  static __device__ __forceinline__ int piece(int p) { return kV == 64 ? 0 : 4 * (p & 1); }
+};
+
+// x in three bf16 parts by cutting: exactly x (8 bits each), two neighbours packed.
+__device__ __forceinline__ void cut3(float a, float b, uint32_t& p1, uint32_t& p2, uint32_t& p3) {
+  const float2 x = make_float2(a, b);
+  const uint32_t ua = __float_as_uint(a), ub = __float_as_uint(b);
+  p1 = __byte_perm(ua, ub, 0x7632);
+  const float2 r = __fadd2_rn(x, make_float2(-__uint_as_float(ua & 0xFFFF0000u), -__uint_as_float(ub & 0xFFFF0000u)));
+  const uint32_t va = __float_as_uint(r.x), vb = __float_as_uint(r.y);
+  p2 = __byte_perm(va, vb, 0x7632);
+  const float2 z = __fadd2_rn(r, make_float2(-__uint_as_float(va & 0xFFFF0000u), -__uint_as_float(vb & 0xFFFF0000u)));
+  p3 = __byte_perm(__float_as_uint(z.x), __float_as_uint(z.y), 0x7632);
 }
 
-// Sum of kN accumulators, 64 columns apart, on 32 columns.
+__device__ __forceinline__ void stmatrix4(uint32_t addr, const uint32_t (&r)[4]) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3])
+               : "memory");
+}
+__device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+
+// Tensor memory, 16 lanes x 16 columns in the layout of a warp-level product's result: for
+// the 8-column tile j (registers 4 j ..) rows lane / 4 and lane / 4 + 8, columns 2 (lane % 4), + 1.
+__device__ __forceinline__ void ld_frag(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
+__device__ __forceinline__ void ld_row(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+// Orders the uses of loaded registers after the wait above them.
 template <int kN>
-__device__ __forceinline__ void sum_parts(uint32_t addr, float (&x)[32]) {
-  uint32_t y[kN][32];
+__device__ __forceinline__ void after_wait(uint32_t (&r)[kN]) {
 #pragma unroll
-  for (int p = 0; p < kN; ++p) tc::tmem_ld32(addr + 64 * p, y[p]);
+  for (int i = 0; i < kN; ++i) asm volatile("" : "+r"(r[i]));
+}
+
+// Sum of kN accumulators, `pitch` columns apart, on 16 lanes x 16 kT columns (ld_frag's layout).
+template <int kN, int kT>
+__device__ __forceinline__ void sum_frag(uint32_t addr, int pitch, float (&x)[8 * kT]) {
+  uint32_t y[kN][kT][8];
 #pragma unroll
-  for (int p = 0; p < kN; ++p) wait_ld(y[p]);
+  for (int p = 0; p < kN; ++p)
 #pragma unroll
-  for (int v = 0; v < 32; ++v) {
-    float s = __uint_as_float(y[kN - 1][v]);  // the smallest first
+    for (int i = 0; i < kT; ++i) ld_frag(addr + pitch * p + 16 * i, y[p][i]);
+  tc::tmem_wait_ld();
 #pragma unroll
-    for (int p = kN - 2; p >= 0; --p) s += __uint_as_float(y[p][v]);
-    x[v] = s;
+  for (int p = 0; p < kN; ++p)
+#pragma unroll
+    for (int i = 0; i < kT; ++i) after_wait(y[p][i]);
+#pragma unroll
+  for (int i = 0; i < kT; ++i)
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) {
+      // the smallest first
+      float2 s = make_float2(__uint_as_float(y[kN - 1][i][e]), __uint_as_float(y[kN - 1][i][e + 1]));
+#pragma unroll
+      for (int p = kN - 2; p >= 0; --p)
+        s = __fadd2_rn(s, make_float2(__uint_as_float(y[p][i][e]), __uint_as_float(y[p][i][e + 1])));
+      x[8 * i + e] = s.x;
+      x[8 * i + e + 1] = s.y;
+    }
+}
+
+// 16 rows x kHalf columns (sum_frag's layout) into the three parts of R / U: rows 16 q .. of the
+// 64-row atoms, columns half ch.
+template <int kV>
+__device__ __forceinline__ void store_frag(uint32_t dst, int q, int ch, int lane, const float (&x)[Geo<kV>::kHalf / 2]) {
+  using G = Geo<kV>;
+  const int row = 16 * q + (lane & 15);  // this lane's address: matrices (rows 0-7, 8-15) x (pieces 2 i, 2 i + 1)
+#pragma unroll
+  for (int i = 0; i < G::kHalf / 16; ++i) {
+    uint32_t w[3][4];
+#pragma unroll
+    for (int m = 0; m < 4; ++m)  // matrix m: rows 8 (m & 1), piece 2 i + (m >> 1)
+      cut3(x[8 * i + 4 * (m >> 1) + 2 * (m & 1)], x[8 * i + 4 * (m >> 1) + 2 * (m & 1) + 1], w[0][m], w[1][m], w[2][m]);
+#pragma unroll
+    for (int p = 0; p < 3; ++p)
+      stmatrix4(dst + G::atom(p, kC) + swz(row, G::piece(p) + G::kPieces * ch + 2 * i + (lane >> 4)), w[p]);
   }
 }
 
+template <int kV>
 __global__ void __launch_bounds__(kScThreads, 1)
     gdn_scan_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV, GdnArgs a, const uint8_t* ws) {
+  using G = Geo<kV>;
+  constexpr int kSplit = kD / kV;
+  constexpr int kHalf = G::kHalf;
+  constexpr int kT = kHalf / 16;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* sm = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-  uint64_t* full = (uint64_t*)(sm + kScSmall);
+  uint64_t* full = (uint64_t*)(sm + G::kSmallAt);
   uint64_t* empty = full + kStages;
   uint64_t* wfull = empty + kStages;
   uint64_t* doneA = wfull + 1;
@@ -446,9 +563,9 @@ __global__ void __launch_bounds__(kScThreads, 1)
   volatile int* abort_s = (volatile int*)(tmem_s + 1);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int vh = blockIdx.x & 1;
-  const int h = (int)((blockIdx.x >> 1) % a.H);
-  const int seq = (int)((blockIdx.x >> 1) / a.H);
+  const int v0 = (int)(blockIdx.x % kSplit) * kV;
+  const int h = (int)((blockIdx.x / kSplit) % a.H);
+  const int seq = (int)((blockIdx.x / kSplit) / a.H);
   const int hk = h / (a.H / a.Hk);
   // what the device arrays cannot mean is refused: nothing is read or written for it
   int slot = seq;
@@ -472,7 +589,7 @@ __global__ void __launch_bounds__(kScThreads, 1)
     if (tid == 0) report_device_error(kErrBadIndex);
     return;
   }
-  const long soff = ((long)slot * a.H + h) * kD * kD + (long)vh * kV * kD;  // state rows of this half
+  const long soff = ((long)slot * a.H + h) * kD * kD + (long)v0 * kD;  // this CTA's state rows
   if (nc == 0) {  // no tokens: the state passes through
     if (a.state_out != nullptr && a.state_out != a.state_in)
       for (int e = tid; e < kV * kD / 4; e += kScThreads) {
@@ -493,16 +610,17 @@ __global__ void __launch_bounds__(kScThreads, 1)
     tc::mbar_init(doneB, 1);
     tc::mbar_init(doneC, 1);
     tc::mbar_init(s_ready, 8);
-    tc::mbar_init(r_ready, 4);
+    tc::mbar_init(r_ready, 8);
     tc::mbar_init(u_ready, 8);
     tc::mbar_init(fin, 1);
     *abort_s = 0;
     tc::mbar_fence_init();
   }
-  for (int e = tid; e < kTile / 16; e += kScThreads)
-    *(uint4*)(sm + kScWy + 5 * kTile + 16 * e) = make_uint4(0u, 0u, 0u, 0u);
+  // [T3; 0]: the loads write the rows of T3 alone
+  for (int e = tid; e < 2 * kTile / 16; e += kScThreads)
+    *(uint4*)(sm + G::kWyAt + 4 * kTile + 16 * e) = make_uint4(0u, 0u, 0u, 0u);
   tc::fence_async_smem();
-  if (warp == 1) tc::tmem_alloc(tmem_s, 512);
+  if (warp == 1) tc::tmem_alloc(tmem_s, G::kTmCols);
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
@@ -521,11 +639,15 @@ __global__ void __launch_bounds__(kScThreads, 1)
         uint8_t* dst = sm + st * kStage;
         const int y = s0 + c * kC;
         tc::mbar_arrive_expect_tx(&full[st], kStTx);
-        for (int kb = 0; kb < 2; ++kb) {
-          tc::tma_load_2d(dst + kStK + kb * 2 * kTile, &tmK, hk * kD + 64 * kb, y, &full[st]);
-          tc::tma_load_2d(dst + kStK + kb * 2 * kTile + kTile, &tmQ, hk * kD + 64 * kb, y, &full[st]);
-        }
-        tc::tma_load_2d(dst + kStV, &tmV, h * kD + vh * kV, y, &full[st]);
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            uint8_t* at = dst + kStKQ + kb * 2 * kTile + g * 4096;
+            tc::tma_load_2d(at, &tmK, hk * kD + 64 * kb, y + 16 * g, &full[st]);
+            tc::tma_load_2d(at + 2048, &tmQ, hk * kD + 64 * kb, y + 16 * g, &full[st]);
+          }
+        tc::tma_load_2d(dst + kStV, &tmV, h * kD + (v0 & 64), y, &full[st]);
         tc::bulk_load_1d(dst + kStScal, wy + (long)c * a.H * kSlot + kWy, kScal, &full[st]);
         return true;
       };
@@ -533,8 +655,13 @@ __global__ void __launch_bounds__(kScThreads, 1)
       if (load_stage(0)) ++stages;
       for (; c < nc; ++c) {
         if (c > 0 && !tc::mbar_wait(doneB, (c - 1) & 1, abort_s)) break;
+        const uint8_t* src = wy + (long)c * a.H * kSlot;
+        uint8_t* dst = sm + G::kWyAt;
         tc::mbar_arrive_expect_tx(wfull, kWy);
-        tc::bulk_load_1d(sm + kScWy, wy + (long)c * a.H * kSlot, kWy, wfull);
+        tc::bulk_load_1d(dst, src, 4 * kTile, wfull);
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+          tc::bulk_load_1d(dst + 4 * kTile + g * 4096, src + 4 * kTile + g * 2048, 2048, wfull);
         if (c + 1 < nc) {
           if (!load_stage(c + 1)) {
             ++c;
@@ -553,40 +680,42 @@ __global__ void __launch_bounds__(kScThreads, 1)
   } else if (warp == 1) {
     // ---------------- products ----------------
     if (lane == 0) {
-      const uint32_t sb = tc::smem_u32(sm + kScS), rb = tc::smem_u32(sm + kScR), wb = tc::smem_u32(sm + kScWy);
+      // descriptors of the operands' starts; a step adds its bytes / 16 to the address field
+      const uint64_t kq0 = tc::sdesc_sw128(tc::smem_u32(sm + kStKQ), 16, 1024);
+      const uint64_t kt0 = tc::sdesc_sw128(tc::smem_u32(sm + kStKQ), 2 * kTile, 1024);
+      const uint64_t w0 = tc::sdesc_sw128(tc::smem_u32(sm + G::kWyAt), 16, 1024);
+      const uint64_t s_d = tc::sdesc_sw128(tc::smem_u32(sm + G::kSAt), 2 * kTile, 1024);
+      const uint64_t r_d = tc::sdesc_sw128(tc::smem_u32(sm + G::kRAt), kTile, 1024);
       for (int c = 0; c < nc; ++c) {
         const int st = c % kStages;
         const uint32_t par = (uint32_t)c & 1;
-        const uint32_t kb = tc::smem_u32(sm + st * kStage + kStK);
+        const uint64_t kq = kq0 + (uint64_t)(st * (kStage >> 4)), kt = kt0 + (uint64_t)(st * (kStage >> 4));
         if (!tc::mbar_wait(&full[st], (uint32_t)(c / kStages) & 1, abort_s) || !tc::mbar_wait(s_ready, par, abort_s))
           break;
         tc::tc_fence_after();
 #pragma unroll
         for (int ks = 0; ks < kD / 16; ++ks)
-          tc::mma_ss(tm + kTmA, tc::sdesc_sw128(kb + (ks >> 2) * 2 * kTile + (ks & 3) * 32, 16, 1024),
-                     tc::sdesc_sw128(sb + ks * 2048, 2 * kTile, 1024), kIdescA, ks > 0 ? 1u : 0u);
+          tc::mma_ss(tm + G::kTmA, kq + (((ks >> 2) * 2 * kTile + (ks & 3) * 32) >> 4), s_d + ((ks * 2048) >> 4),
+                     G::kIdescA, ks > 0 ? 1u : 0u);
         tc::mma_commit(doneA);
         if (!tc::mbar_wait(wfull, par, abort_s) || !tc::mbar_wait(r_ready, par, abort_s)) break;
         tc::tc_fence_after();
 #pragma unroll
         for (int ks = 0; ks < kC / 16; ++ks)
-          tc::mma_ss(tm + kTmB, tc::sdesc_sw128(wb + ks * 32, 16, 1024), tc::sdesc_sw128(rb + ks * 2048, kTile, 1024),
-                     kIdescA, ks > 0 ? 1u : 0u);
+          tc::mma_ss(tm + G::kTmB, w0 + ((ks * 32) >> 4), r_d + ((ks * 2048) >> 4), G::kIdescA, ks > 0 ? 1u : 0u);
 #pragma unroll
         for (int ks = 0; ks < kC / 16; ++ks)
-          tc::mma_ss(tm + kTmB2, tc::sdesc_sw128(wb + 2 * kTile + ks * 32, 16, 1024),
-                     tc::sdesc_sw128(rb + ks * 2048, kTile, 1024), kIdescB2, ks > 0 ? 1u : 0u);
+          tc::mma_ss(tm + G::kTmB2, w0 + ((2 * kTile + ks * 32) >> 4), r_d + ((ks * 2048) >> 4), G::kIdescB2,
+                     ks > 0 ? 1u : 0u);
 #pragma unroll
         for (int ks = 0; ks < kC / 16; ++ks)
-          tc::mma_ss(tm + kTmB2, tc::sdesc_sw128(wb + 4 * kTile + ks * 32, 16, 1024),
-                     tc::sdesc_sw128(rb + ks * 2048, kTile, 1024), kIdescB3, 1u);
+          tc::mma_ss(tm + G::kTmB2, w0 + ((4 * kTile + ks * 32) >> 4), r_d + ((ks * 2048) >> 4), G::kIdescB3, 1u);
         tc::mma_commit(doneB);
         if (!tc::mbar_wait(u_ready, par, abort_s)) break;
         tc::tc_fence_after();
 #pragma unroll
         for (int ks = 0; ks < kC / 16; ++ks)
-          tc::mma_ss(tm + kTmA, tc::sdesc_sw128(kb + ks * 2048, 2 * kTile, 1024),
-                     tc::sdesc_sw128(rb + ks * 2048, kTile, 1024), kIdescC, ks > 0 ? 1u : 0u);
+          tc::mma_ss(tm + G::kTmA, kt + ((ks * 4096) >> 4), r_d + ((ks * 2048) >> 4), G::kIdescC, ks > 0 ? 1u : 0u);
         tc::mma_commit(doneC);
         tc::mma_commit(&empty[st]);
       }
@@ -596,118 +725,154 @@ __global__ void __launch_bounds__(kScThreads, 1)
     }
     __syncwarp();
   } else {
-    // ---------------- warps 2-9: row r, column half ch of every product ----------------
-    const int q = warp & 3;            // tensor-memory lanes of this warp
+    // ---------------- warps 2-9: lane quarter q, column half ch of every product ----------------
+    const int q = warp & 3;
     const int ch = (warp - 2) >> 2;
-    const int r = 32 * q + lane;       // A, B: token r & 63; C and S: key channel r
-    const int t = r & (kC - 1);
-    const bool low = r < kC;
-    const uint32_t row = tm + ((uint32_t)(32 * q) << 16) + 32 * ch;
-    const long srow = soff + (long)(32 * ch) * kD + r;
-    float S[32];
+    const int r = 32 * q + lane;             // C and S: key channel r
+    const int ta = 16 * q + (lane >> 2);     // A, B: tokens ta and ta + 8
+    const uint32_t lanes = tm + ((uint32_t)(32 * q) << 16) + kHalf * ch;
+    const uint32_t lanes2 = lanes + (16u << 16);  // the rows of Q and G
+    const long srow = soff + (long)(kHalf * ch) * kD + r;
+    const uint32_t rdst = tc::smem_u32(sm + G::kRAt);
+    // V's pieces of this warp's columns in the stage's 64
+    const int vpiece = ((v0 & 63) >> 3) + G::kPieces * ch;
+    float S[kHalf];
 #pragma unroll
-    for (int v = 0; v < 32; ++v) S[v] = a.state_in != nullptr ? a.state_in[srow + (long)v * kD] : 0.0f;
+    for (int v = 0; v < kHalf; ++v) S[v] = a.state_in != nullptr ? a.state_in[srow + (long)v * kD] : 0.0f;
     bool ok = true;
-    for (int c = 0; c < nc; ++c) {
+    for (int c = 0; ok && c < nc; ++c) {
       const int st = c % kStages;
       const uint32_t par = (uint32_t)c & 1;
       uint8_t* stage = sm + st * kStage;
       const float* sc = (const float*)(stage + kStScal);
       const int n = min(kC, len - c * kC);
-      store_split(sm + kScS, 2 * kTile, r, ch, S);
-      ok = tc::mbar_wait_warp(&full[st], (uint32_t)(c / kStages) & 1, abort_s);
+      // S's parts: row r, columns half ch
+#pragma unroll
+      for (int i = 0; i < G::kPieces; ++i) {
+        uint32_t w[3][4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) cut3(S[8 * i + 2 * e], S[8 * i + 2 * e + 1], w[0][e], w[1][e], w[2][e]);
+#pragma unroll
+        for (int p = 0; p < 3; ++p)
+          *(uint4*)(sm + G::kSAt + G::atom(p, kD) + swz(r, G::piece(p) + G::kPieces * ch + i)) =
+              make_uint4(w[p][0], w[p][1], w[p][2], w[p][3]);
+      }
+      ok = tc::mbar_wait(&full[st], (uint32_t)(c / kStages) & 1, abort_s);
       if (!ok) break;
-      if (n < kC && low && t >= n) {
+      if (n < kC && r < kC && r >= n) {
         // keys behind the sequence belong to another one, or to none: zero (key half ch)
 #pragma unroll
         for (int c8 = 0; c8 < 8; ++c8)
-          *(uint4*)(stage + kStK + ch * 2 * kTile + t * 128 + 16 * c8) = make_uint4(0u, 0u, 0u, 0u);
+          *(uint4*)(stage + kStKQ + ch * 2 * kTile + stacked(r) * 128 + 16 * c8) = make_uint4(0u, 0u, 0u, 0u);
       }
-      // (read before this warp's s_ready: the stage may be refilled as soon as C is done)
-      const float gt = sc[t], dt = sc[kC + t], gC = sc[kC - 1];
       tc::fence_async_smem();
       tc::tc_fence_before();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(s_ready);
-      ok = tc::mbar_wait_warp(doneA, par, abort_s);
+      // what the steps to come need of this chunk (read before this warp's r_ready: the stage
+      // may be refilled as soon as C is done)
+      const float ga = sc[ta], gb = sc[ta + 8], da = sc[kC + ta], db = sc[kC + ta + 8], gC = sc[kC - 1];
+      uint32_t vw[kT][4];  // V: matrix m of tile pair i as in store_frag
+#pragma unroll
+      for (int i = 0; i < kT; ++i)
+        ldmatrix4(tc::smem_u32(stage + kStV) + swz(16 * q + (lane & 15), vpiece + 2 * i + (lane >> 4)), vw[i]);
+      ok = tc::mbar_wait(doneA, par, abort_s);
       if (!ok) break;
       tc::tc_fence_after();
-      float x[32];  // K S^T or Q S^T
-      sum_parts<3>(row + kTmA, x);
-      if (low) {
-        // R_t, zero behind the sequence
+      float x[kHalf / 2];
+      sum_frag<3, kT>(lanes + G::kTmA, kV, x);
+      {
+        const bool la = ta < n, lb = ta + 8 < n;  // R is zero behind the sequence
 #pragma unroll
-        for (int p = 0; p < 4; ++p) {
-          const uint4 w = *(const uint4*)(stage + kStV + swz(t, 4 * ch + p));
-          const uint32_t vw[4] = {w.x, w.y, w.z, w.w};
+        for (int i = 0; i < kT; ++i)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int v = 8 * p + 2 * e;
-            x[v] = t < n ? fmaf(-gt, x[v], tc::bf16lo(vw[e])) : 0.0f;
-            x[v + 1] = t < n ? fmaf(-gt, x[v + 1], tc::bf16hi(vw[e])) : 0.0f;
+          for (int m = 0; m < 4; ++m) {
+            const int e = 8 * i + 4 * (m >> 1) + 2 * (m & 1);
+            const float g = (m & 1) ? gb : ga;
+            const bool live = (m & 1) ? lb : la;
+            x[e] = live ? fmaf(-g, x[e], tc::bf16lo(vw[i][m])) : 0.0f;
+            x[e + 1] = live ? fmaf(-g, x[e + 1], tc::bf16hi(vw[i][m])) : 0.0f;
           }
-        }
-        store_split(sm + kScR, kTile, t, ch, x);
-        tc::fence_async_smem();
-        tc::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(r_ready);
-      } else {
-        // C may take A's columns now
-        tc::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(u_ready);
       }
-      ok = tc::mbar_wait_warp(doneB, par, abort_s);
+      store_frag<kV>(rdst, q, ch, lane, x);
+      tc::fence_async_smem();
+      tc::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(r_ready);
+      float y[kHalf / 2];
+      sum_frag<2, kT>(lanes2 + G::kTmA, kV, y);  // Q S^T, off by 2^-15: it goes to a bf16 output
+      ok = tc::mbar_wait(doneB, par, abort_s);
       if (!ok) break;
       tc::tc_fence_after();
-      if (low) {
-        float y[32];
-        sum_parts<3>(row + kTmB, x);
-        sum_parts<2>(row + kTmB2, y);
+      {
+        float z[kHalf / 2];
+        sum_frag<3, kT>(lanes + G::kTmB, kV, x);
+        sum_frag<2, kT>(lanes + G::kTmB2, kV, z);
 #pragma unroll
-        for (int v = 0; v < 32; ++v) x[v] = dt * (x[v] + y[v]);
-        store_split(sm + kScR, kTile, t, ch, x);
-        tc::fence_async_smem();
-        tc::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(u_ready);
-      } else {
-        float y[32], z[32];
-        sum_parts<2>(row + kTmB, y);
-        sum_parts<1>(row + kTmB2, z);
-        if (t < n) {
-          __nv_bfloat16* orow =
-              (__nv_bfloat16*)a.o + ((long)(s0 + c * kC + t) * a.H + h) * kD + vh * kV + 32 * ch;
+        for (int e = 0; e < kHalf / 2; ++e) x[e] = ((e & 2) ? db : da) * (x[e] + z[e]);
+      }
+      store_frag<kV>(rdst, q, ch, lane, x);
+      tc::fence_async_smem();
+      tc::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(u_ready);
+      {
+        // the output of tokens ta and ta + 8, beside C
+        float z[kHalf / 2];
+        sum_frag<2, kT>(lanes2 + G::kTmB, kV, x);
+        sum_frag<1, kT>(lanes2 + G::kTmB2, kV, z);
+        __nv_bfloat16* orow =
+            (__nv_bfloat16*)a.o + ((long)(s0 + c * kC + ta) * a.H + h) * kD + v0 + kHalf * ch + 2 * (lane & 3);
 #pragma unroll
-          for (int p = 0; p < 4; ++p) {
-            uint32_t w[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int v = 8 * p + 2 * e;
-              w[e] = tc::pack_bf16x2(fmaf(gt, x[v], y[v] + z[v]), fmaf(gt, x[v + 1], y[v + 1] + z[v + 1]));
-            }
-            *(uint4*)(orow + 8 * p) = make_uint4(w[0], w[1], w[2], w[3]);
-          }
+        for (int e = 0; e < kHalf / 2; e += 2) {
+          const bool second = (e & 2) != 0;
+          const float g = second ? gb : ga;
+          if (ta + (second ? 8 : 0) < n)
+            *(uint32_t*)(orow + (second ? 8L * a.H * kD : 0) + 8 * (e >> 2)) =
+                tc::pack_bf16x2(fmaf(g, y[e], x[e] + z[e]), fmaf(g, y[e + 1], x[e + 1] + z[e + 1]));
         }
       }
-      ok = tc::mbar_wait_warp(doneC, par, abort_s);
+      ok = tc::mbar_wait(doneC, par, abort_s);
       if (!ok) break;
       tc::tc_fence_after();
-      sum_parts<3>(row + kTmA, x);
+      {
+        uint32_t z[3][kT][16];
 #pragma unroll
-      for (int v = 0; v < 32; ++v) S[v] = fmaf(gC, S[v], x[v]);
+        for (int p = 0; p < 3; ++p)
+#pragma unroll
+          for (int i = 0; i < kT; ++i) ld_row(lanes + G::kTmA + kV * p + 16 * i, z[p][i]);
+        tc::tmem_wait_ld();
+#pragma unroll
+        for (int p = 0; p < 3; ++p)
+#pragma unroll
+          for (int i = 0; i < kT; ++i) after_wait(z[p][i]);
+#pragma unroll
+        for (int v = 0; v < kHalf; ++v)
+          S[v] = fmaf(gC, S[v],
+                      (__uint_as_float(z[2][v >> 4][v & 15]) + __uint_as_float(z[1][v >> 4][v & 15])) +
+                          __uint_as_float(z[0][v >> 4][v & 15]));
+      }
     }
     if (ok && a.state_out != nullptr) {
 #pragma unroll
-      for (int v = 0; v < 32; ++v) a.state_out[srow + (long)v * kD] = S[v];
+      for (int v = 0; v < kHalf; ++v) a.state_out[srow + (long)v * kD] = S[v];
     }
   }
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
-  if (warp == 1) tc::tmem_dealloc(tm, 512);
+  if (warp == 1) tc::tmem_dealloc(tm, G::kTmCols);
   if (tid == 0 && *abort_s) report_device_error(kErrMbarTimeout);
+}
+
+template <int kV>
+cudaError_t launch_scan(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const GdnArgs& a,
+                        const uint8_t* ws, cudaStream_t s) {
+  const int smem = 1024 + Geo<kV>::kSmem;
+  cudaError_t e = cudaFuncSetAttribute(gdn_scan_kernel<kV>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  gdn_scan_kernel<kV><<<(unsigned)((long)a.n_seq * a.H * (kD / kV)), kScThreads, smem, s>>>(tq, tk, tv, a, ws);
+  return cudaGetLastError();
 }
 
 }  // namespace
@@ -718,22 +883,25 @@ static long gdn_slots(int T, int n_seq) { return (long)T / kC + n_seq; }
 size_t gdn_chunk_workspace(int T, int n_seq, int H) { return (size_t)gdn_slots(T, n_seq) * H * kSlot; }
 
 cudaError_t launch_gdn_chunk(const GdnArgs& a, void* ws, cudaStream_t s) {
-  const long wy = gdn_slots(a.T, a.n_seq) * a.H, scan = (long)a.n_seq * a.H * 2;
-  if (wy >= (1L << 31) || scan >= (1L << 31)) return cudaErrorNotSupported;
-  CUtensorMap tq, tk, tv;
-  cudaError_t e = make_tmap_2d(&tq, a.q, (long)a.Hk * kD, a.T, (long)a.Hk * kD * 2, 64, 64);
-  if (e == cudaSuccess) e = make_tmap_2d(&tk, a.k, (long)a.Hk * kD, a.T, (long)a.Hk * kD * 2, 64, 64);
-  if (e == cudaSuccess) e = make_tmap_2d(&tv, a.v, (long)a.H * kD, a.T, (long)a.H * kD * 2, 64, 64);
+  const long wy = gdn_slots(a.T, a.n_seq) * a.H, pairs = (long)a.n_seq * a.H;
+  if (wy >= (1L << 31) || pairs * 4 >= (1L << 31)) return cudaErrorNotSupported;
+  const long rowk = (long)a.Hk * kD, rowv = (long)a.H * kD;
+  CUtensorMap tq, tk, tq16, tk16, tv;
+  cudaError_t e = make_tmap_2d(&tq, a.q, rowk, a.T, rowk * 2, 64, 64);
+  if (e == cudaSuccess) e = make_tmap_2d(&tk, a.k, rowk, a.T, rowk * 2, 64, 64);
+  if (e == cudaSuccess) e = make_tmap_2d(&tq16, a.q, rowk, a.T, rowk * 2, 64, 16);
+  if (e == cudaSuccess) e = make_tmap_2d(&tk16, a.k, rowk, a.T, rowk * 2, 64, 16);
+  if (e == cudaSuccess) e = make_tmap_2d(&tv, a.v, rowv, a.T, rowv * 2, 64, 64);
   if (e != cudaSuccess) return e;
-  const int wsm = 1024 + kWySmem, ssm = 1024 + kScSmem;
+  const int wsm = 1024 + kWySmem;
   e = cudaFuncSetAttribute(gdn_wy_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, wsm);
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(gdn_scan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, ssm);
   if (e != cudaSuccess) return e;
   gdn_wy_kernel<<<(unsigned)wy, 128, wsm, s>>>(tq, tk, a, (uint8_t*)ws);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  gdn_scan_kernel<<<(unsigned)scan, kScThreads, ssm, s>>>(tq, tk, tv, a, (const uint8_t*)ws);
-  return cudaGetLastError();
+  // four CTAs per (sequence, head) while they all run at once, else two
+  return pairs * 4 <= num_sms() ? launch_scan<32>(tq16, tk16, tv, a, (const uint8_t*)ws, s)
+                                : launch_scan<64>(tq16, tk16, tv, a, (const uint8_t*)ws, s);
 }
 
 }  // namespace hla
