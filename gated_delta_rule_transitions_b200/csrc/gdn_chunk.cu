@@ -88,23 +88,15 @@ __device__ __forceinline__ void wait_ld(uint32_t (&r)[32]) {
 
 constexpr int kP = kC + 4;                    // row pitch (floats): 16-byte rows
 constexpr int kMat = kC * kP * 4;             // one 64 x 64 float32 matrix
-constexpr int kWyQK = 0;                      // [kb][Q | K][64 rows][128 B]; then P and L'
-constexpr int kWyL = 4 * kTile;               // L, then G
-constexpr int kWyU = kWyL + kMat;             // (I + L)^{-1}
+constexpr int kWyQK = 0;                      // [kb][Q | K][64 rows][128 B]; once they are multiplied:
+constexpr int kWyP = 0;                       //   P, then
+constexpr int kWyL = kMat;                    //   L, then L' (off the diagonal blocks), then G
+constexpr int kWyU = 2 * kMat;                // (I + L)^{-1}
 constexpr int kWySmall = kWyU + kMat;
-constexpr int kXP = 52;                       // row pitch (floats) of L'
-constexpr int kWyP = kWyQK;                   // P over the Q, K tiles once they are multiplied
-constexpr int kWyX = kWyQK + kMat;
-constexpr int kWySmem = kWySmall + kC * 8 + 5 * kC * 4 + 2 * 8 + 32;
-static_assert(kMat + 48 * kXP * 4 <= 4 * kTile, "P and L' fit over the tiles");
+constexpr int kWySmem = kWySmall + kC * 8 + 3 * kC * 4 + 2 * 8 + 32;
+static_assert(2 * kMat >= 4 * kTile, "the tiles fit under P and L");
 constexpr uint32_t kIdescWy = tc::idesc_bf16_f32(128, 64, 0, 0);
 constexpr float kProductRange = 40.0f;
-
-__device__ __forceinline__ uint32_t tf32(float x) {
-  uint32_t r;
-  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(x));
-  return r;
-}
 
 __device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
   asm volatile(
@@ -114,15 +106,10 @@ __device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
 }
 
-// Float32 fragments as two tf32 numbers each (2^-22).
-__device__ __forceinline__ void frag_a(const float* A, int pa, int lane, uint32_t (&h)[4], uint32_t (&l)[4]) {
-  const int g = lane >> 2, q = lane & 3;
-  const float a[4] = {A[g * pa + q], A[(g + 8) * pa + q], A[g * pa + q + 4], A[(g + 8) * pa + q + 4]};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    h[i] = tf32(a[i]);
-    l[i] = tf32(a[i] - __uint_as_float(h[i]));
-  }
+// x as two tf32 numbers, cut (the instruction does not read the last 13 bits): off by 2^-21.
+__device__ __forceinline__ void cut_tf32(float x, uint32_t& h, uint32_t& l) {
+  h = __float_as_uint(x) & 0xFFFFE000u;
+  l = __float_as_uint(x - __uint_as_float(h));
 }
 
 // acc[j] += A (16 x 16) B (16 x 8 kN)'s column tile j, float32 in shared memory (row pitches
@@ -134,16 +121,15 @@ __device__ __forceinline__ void block16(float (&acc)[kN][4], const float* A, int
 #pragma unroll
   for (int k0 = 0; k0 < 16; k0 += 8) {
     uint32_t ah[4], al[4];
-    frag_a(A + k0, pa, lane, ah, al);
+    cut_tf32(A[g * pa + k0 + q], ah[0], al[0]);
+    cut_tf32(A[(g + 8) * pa + k0 + q], ah[1], al[1]);
+    cut_tf32(A[g * pa + k0 + q + 4], ah[2], al[2]);
+    cut_tf32(A[(g + 8) * pa + k0 + q + 4], ah[3], al[3]);
 #pragma unroll
     for (int j = 0; j < kN; ++j) {
-      const float b[2] = {B[(k0 + q) * pb + 8 * j + g], B[(k0 + q + 4) * pb + 8 * j + g]};
       uint32_t bh[2], bl[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        bh[i] = tf32(b[i]);
-        bl[i] = tf32(b[i] - __uint_as_float(bh[i]));
-      }
+      cut_tf32(B[(k0 + q) * pb + 8 * j + g], bh[0], bl[0]);
+      cut_tf32(B[(k0 + q + 4) * pb + 8 * j + g], bh[1], bl[1]);
       mma_tf32(acc[j], ah, bl);
       mma_tf32(acc[j], al, bh);
       mma_tf32(acc[j], ah, bh);
@@ -164,8 +150,8 @@ __device__ __forceinline__ float exp64(double x) {
   return fmaf(e, (float)(x - (double)h), e);
 }
 
-// One CTA (4 warps) per (chunk slot, head), three per SM.
-__global__ void __launch_bounds__(128, 3)
+// One CTA (4 warps) per (chunk slot, head), four per SM.
+__global__ void __launch_bounds__(128, 4)
     gdn_wy_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK, GdnArgs a,
                   uint8_t* ws) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -173,7 +159,6 @@ __global__ void __launch_bounds__(128, 3)
   float* Ls = (float*)(sm + kWyL);
   float* Us = (float*)(sm + kWyU);
   float* Ps = (float*)(sm + kWyP);
-  float* Xs = (float*)(sm + kWyX);
   double* ell = (double*)(sm + kWySmall);
   float* beta_s = (float*)(ell + kC);
   float* gam = beta_s + kC;
@@ -281,18 +266,25 @@ __global__ void __launch_bounds__(128, 3)
       uint32_t x[32];
       tc::tmem_ld32(tm + ((uint32_t)(32 * warp) << 16) + 32 * half, x);
       wait_ld(x);
+      if (product) {  // the pair's decay as a product of two exponentials while both stay in range
 #pragma unroll
-      for (int e4 = 0; e4 < 32; e4 += 4) {
-        float v[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int s = 32 * half + e4 + e;
-          float d = 0.0f;
-          // the pair's decay as a product of two exponentials while both stay in range
-          if (s <= last) d = product ? gt * igam[s] : bt * expf((float)(ell[t] - ell[s]));
-          v[e] = s <= last ? d * __uint_as_float(x[e4 + e]) : 0.0f;
+        for (int e = 0; e < 32; e += 4) {
+          const int s = 32 * half + e;
+          const float4 i4 = *(const float4*)(igam + s);
+          float4 v;
+          v.x = s <= last ? gt * i4.x * __uint_as_float(x[e]) : 0.0f;
+          v.y = s + 1 <= last ? gt * i4.y * __uint_as_float(x[e + 1]) : 0.0f;
+          v.z = s + 2 <= last ? gt * i4.z * __uint_as_float(x[e + 2]) : 0.0f;
+          v.w = s + 3 <= last ? gt * i4.w * __uint_as_float(x[e + 3]) : 0.0f;
+          *(float4*)(row + s) = v;
         }
-        *(float4*)(row + 32 * half + e4) = make_float4(v[0], v[1], v[2], v[3]);
+      } else {
+        const double lt = ell[t];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          const int s = 32 * half + e;
+          row[s] = s <= last ? bt * expf((float)(lt - ell[s])) * __uint_as_float(x[e]) : 0.0f;
+        }
       }
     }
     tc::tc_fence_before();
@@ -322,13 +314,15 @@ __global__ void __launch_bounds__(128, 3)
   }
   __syncthreads();
 #pragma unroll
-  for (int r = 0; r < 3; ++r) {  // L'_ik = U_ii L_ik: 6 blocks, 12 halves, 3 a warp
+  for (int r = 0; r < 3; ++r) {  // L'_ik = U_ii L_ik in L's place: 6 blocks, 12 halves, 3 a warp
     const int u = warp + 4 * r, blk = u >> 1, nh = u & 1;
     const int ib = blk < 1 ? 1 : (blk < 3 ? 2 : 3);
     const int kb = blk - (ib * (ib - 1)) / 2;
     float acc[1][4] = {};
-    block16<1>(acc, Us + 16 * ib * kP + 16 * ib, kP, Ls + 16 * ib * kP + 16 * kb + 8 * nh, kP, lane);
-    store16(Xs + (16 * ib - 16) * kXP + 16 * kb + 8 * nh, kXP, acc[0], 1.0f, lane);
+    float* at = Ls + 16 * ib * kP + 16 * kb + 8 * nh;
+    block16<1>(acc, Us + 16 * ib * kP + 16 * ib, kP, at, kP, lane);
+    __syncwarp();
+    store16(at, kP, acc[0], 1.0f, lane);
   }
   __syncthreads();
 #pragma unroll
@@ -338,13 +332,13 @@ __global__ void __launch_bounds__(128, 3)
       float acc[1][4] = {};
 #pragma unroll
       for (int k = 0; k < lev; ++k)
-        block16<1>(acc, Xs + 16 * (jb + lev - 1) * kXP + 16 * (jb + k), kXP, Us + 16 * (jb + k) * kP + 16 * jb + 8 * nh,
-                   kP, lane);
+        block16<1>(acc, Ls + 16 * (jb + lev) * kP + 16 * (jb + k), kP, Us + 16 * (jb + k) * kP + 16 * jb + 8 * nh, kP,
+                   lane);
       store16(Us + 16 * (jb + lev) * kP + 16 * jb + 8 * nh, kP, acc[0], -1.0f, lane);
     }
     __syncthreads();
   }
-  // G = P U over L (no longer needed), blocks (i, j), j <= i, of i - j + 1 products: 5 a warp
+  // G = P U over L' (no longer needed), blocks (i, j), j <= i, of i - j + 1 products: 5 a warp
   auto g_block = [&](int i, int j) {
     float acc[2][4] = {};
     for (int k = j; k <= i; ++k)
