@@ -673,50 +673,65 @@ __global__ void __launch_bounds__(kScThreads, 1)
     __syncwarp();
   } else if (warp == 1) {
     // ---------------- products ----------------
-    if (lane == 0) {
-      // descriptors of the operands' starts; a step adds its bytes / 16 to the address field
-      const uint64_t kq0 = tc::sdesc_sw128(tc::smem_u32(sm + kStKQ), 16, 1024);
-      const uint64_t kt0 = tc::sdesc_sw128(tc::smem_u32(sm + kStKQ), 2 * kTile, 1024);
-      const uint64_t w0 = tc::sdesc_sw128(tc::smem_u32(sm + G::kWyAt), 16, 1024);
-      const uint64_t s_d = tc::sdesc_sw128(tc::smem_u32(sm + G::kSAt), 2 * kTile, 1024);
-      const uint64_t r_d = tc::sdesc_sw128(tc::smem_u32(sm + G::kRAt), kTile, 1024);
-      for (int c = 0; c < nc; ++c) {
-        const int st = c % kStages;
-        const uint32_t par = (uint32_t)c & 1;
-        const uint64_t kq = kq0 + (uint64_t)(st * (kStage >> 4)), kt = kt0 + (uint64_t)(st * (kStage >> 4));
-        if (!tc::mbar_wait(&full[st], (uint32_t)(c / kStages) & 1, abort_s) || !tc::mbar_wait(s_ready, par, abort_s))
-          break;
-        tc::tc_fence_after();
+    // The whole warp walks the loop and one elected lane issues, so that descriptors and
+    // addresses are the same in every lane and live in uniform registers (issued from a
+    // branch of one lane, an instruction took 69 cycles).
+    const bool lead = tc::elect_one();
+    const uint32_t tmu = __shfl_sync(0xFFFFFFFFu, tm, 0);
+    // descriptors of the operands' starts; a step adds its bytes / 16 to the address field
+    const uint64_t kq0 = tc::sdesc_sw128(tc::smem_u32(sm + kStKQ), 16, 1024);
+    const uint64_t kt0 = tc::sdesc_sw128(tc::smem_u32(sm + kStKQ), 2 * kTile, 1024);
+    const uint64_t w0 = tc::sdesc_sw128(tc::smem_u32(sm + G::kWyAt), 16, 1024);
+    const uint64_t s_d = tc::sdesc_sw128(tc::smem_u32(sm + G::kSAt), 2 * kTile, 1024);
+    const uint64_t r_d = tc::sdesc_sw128(tc::smem_u32(sm + G::kRAt), kTile, 1024);
+    for (int c = 0; c < nc; ++c) {
+      const int st = c % kStages;
+      const uint32_t par = (uint32_t)c & 1;
+      const uint64_t kq = kq0 + (uint64_t)(st * (kStage >> 4)), kt = kt0 + (uint64_t)(st * (kStage >> 4));
+      bool go = tc::mbar_wait(&full[st], (uint32_t)(c / kStages) & 1, abort_s) && tc::mbar_wait(s_ready, par, abort_s);
+      if (!__all_sync(0xFFFFFFFFu, go)) break;
+      tc::tc_fence_after();
+      if (lead) {
 #pragma unroll
         for (int ks = 0; ks < kD / 16; ++ks)
-          tc::mma_ss(tm + G::kTmA, kq + (((ks >> 2) * 2 * kTile + (ks & 3) * 32) >> 4), s_d + ((ks * 2048) >> 4),
+          tc::mma_ss(tmu + G::kTmA, kq + (((ks >> 2) * 2 * kTile + (ks & 3) * 32) >> 4), s_d + ((ks * 2048) >> 4),
                      G::kIdescA, ks > 0 ? 1u : 0u);
         tc::mma_commit(doneA);
-        if (!tc::mbar_wait(wfull, par, abort_s) || !tc::mbar_wait(r_ready, par, abort_s)) break;
-        tc::tc_fence_after();
+      }
+      __syncwarp();
+      go = tc::mbar_wait(wfull, par, abort_s) && tc::mbar_wait(r_ready, par, abort_s);
+      if (!__all_sync(0xFFFFFFFFu, go)) break;
+      tc::tc_fence_after();
+      if (lead) {
 #pragma unroll
         for (int ks = 0; ks < kC / 16; ++ks)
-          tc::mma_ss(tm + G::kTmB, w0 + ((ks * 32) >> 4), r_d + ((ks * 2048) >> 4), G::kIdescA, ks > 0 ? 1u : 0u);
+          tc::mma_ss(tmu + G::kTmB, w0 + ((ks * 32) >> 4), r_d + ((ks * 2048) >> 4), G::kIdescA, ks > 0 ? 1u : 0u);
 #pragma unroll
         for (int ks = 0; ks < kC / 16; ++ks)
-          tc::mma_ss(tm + G::kTmB2, w0 + ((2 * kTile + ks * 32) >> 4), r_d + ((ks * 2048) >> 4), G::kIdescB2,
+          tc::mma_ss(tmu + G::kTmB2, w0 + ((2 * kTile + ks * 32) >> 4), r_d + ((ks * 2048) >> 4), G::kIdescB2,
                      ks > 0 ? 1u : 0u);
 #pragma unroll
         for (int ks = 0; ks < kC / 16; ++ks)
-          tc::mma_ss(tm + G::kTmB2, w0 + ((4 * kTile + ks * 32) >> 4), r_d + ((ks * 2048) >> 4), G::kIdescB3, 1u);
+          tc::mma_ss(tmu + G::kTmB2, w0 + ((4 * kTile + ks * 32) >> 4), r_d + ((ks * 2048) >> 4), G::kIdescB3, 1u);
         tc::mma_commit(doneB);
-        if (!tc::mbar_wait(u_ready, par, abort_s)) break;
-        tc::tc_fence_after();
+      }
+      __syncwarp();
+      go = tc::mbar_wait(u_ready, par, abort_s);
+      if (!__all_sync(0xFFFFFFFFu, go)) break;
+      tc::tc_fence_after();
+      if (lead) {
 #pragma unroll
         for (int ks = 0; ks < kC / 16; ++ks)
-          tc::mma_ss(tm + G::kTmA, kt + ((ks * 4096) >> 4), r_d + ((ks * 2048) >> 4), G::kIdescC, ks > 0 ? 1u : 0u);
+          tc::mma_ss(tmu + G::kTmA, kt + ((ks * 4096) >> 4), r_d + ((ks * 2048) >> 4), G::kIdescC, ks > 0 ? 1u : 0u);
         tc::mma_commit(doneC);
         tc::mma_commit(&empty[st]);
       }
-      // every product issued here completes before tensor memory is freed
-      tc::mma_commit(fin);
-      tc::mbar_wait(fin, 0, nullptr, 200000000ull);
+      __syncwarp();
     }
+    // every product issued here completes before tensor memory is freed
+    if (lead) tc::mma_commit(fin);
+    __syncwarp();
+    tc::mbar_wait(fin, 0, nullptr, 200000000ull);
     __syncwarp();
   } else {
     // ---------------- warps 2-9: lane quarter q, column half ch of every product ----------------
