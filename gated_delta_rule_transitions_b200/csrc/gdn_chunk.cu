@@ -399,7 +399,7 @@ __global__ void __launch_bounds__(128, 4)
 // ---- the walk over a sequence's chunks ---------------------------------------------------
 //
 // One CTA per (sequence, head, kV value columns): warp 0 loads, warp 1 issues the products,
-// warps 2-9 do the rest.  The parts of the right factor lie side by side, so that one
+// the others do the rest.  The parts of the right factor lie side by side, so that one
 // instruction reads the left one once for all of them.
 //   A  [K; Q] (128 x 128) x [S1 | S2 | S3]     -> K S^T and Q S^T (rows as in stacked())
 //      R_t = V_t - gamma_t (K S^T)_t into shared memory (three parts); gamma_t (Q S^T)_t stays
@@ -417,14 +417,15 @@ constexpr int kStScal = kStV + kTile;
 constexpr int kStage = kStScal + 1024;
 constexpr int kStages = 2;
 constexpr uint32_t kStTx = 5 * kTile + kScal;
-constexpr int kScThreads = 320;
 
-// A right factor of kV columns in three parts: 64-column atoms (128-byte rows) of `rows` rows.
-// kV = 64: an atom per part; kV = 32: parts 1 and 2 share the first.
+// A right factor of kV columns in three parts side by side: 64-column atoms (128-byte rows).
+// kV = 64: an atom per part; 32: parts 1 and 2 share the first; 16: one for all.
 template <int kV>
 struct Geo {
-  static constexpr int kAtoms = kV == 64 ? 3 : 2;
-  static constexpr int kHalf = kV / 2;        // columns per warp
+  static constexpr int kAtoms = kV == 64 ? 3 : kV == 32 ? 2 : 1;
+  static constexpr int kHalf = kV == 64 ? 32 : 16;  // columns per warp
+  static constexpr int kSets = kV / kHalf;          // warps per 32 rows
+  static constexpr int kThreads = 64 + 128 * kSets;
   static constexpr int kPieces = kHalf / 8;   // 16-byte pieces of a row per warp and part
   static constexpr int kWyAt = kStages * kStage;         // [T1; G1], [T2; G2], [T3; 0]
   static constexpr int kSAt = kWyAt + 6 * kTile;         // S^T: 128 rows
@@ -438,8 +439,8 @@ struct Geo {
   // tensor memory columns: A and C, then the two accumulators of B
   static constexpr uint32_t kTmA = 0, kTmB = 3 * kV, kTmB2 = 6 * kV, kTmCols = 8 * kV;
   // byte offset of part p's atom, and the 16-byte piece its columns start at
-  static __device__ __forceinline__ int atom(int p, int rows) { return (kV == 64 ? p : p >> 1) * rows * 128; }
-  static __device__ __forceinline__ int piece(int p) { return kV == 64 ? 0 : 4 * (p & 1); }
+  static __device__ __forceinline__ int atom(int p, int rows) { return (p * kV >> 6) * rows * 128; }
+  static __device__ __forceinline__ int piece(int p) { return (p * kV & 63) >> 3; }
 };
 
 // x in three bf16 parts by cutting: exactly x (8 bits each), two neighbours packed.
@@ -534,11 +535,12 @@ __device__ __forceinline__ void store_frag(uint32_t dst, int q, int ch, int lane
 }
 
 template <int kV>
-__global__ void __launch_bounds__(kScThreads, 1)
+__global__ void __launch_bounds__(Geo<kV>::kThreads, 1)
     gdn_scan_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV, GdnArgs a, const uint8_t* ws) {
   using G = Geo<kV>;
   constexpr int kSplit = kD / kV;
+  constexpr int kScThreads = G::kThreads;
   constexpr int kHalf = G::kHalf;
   constexpr int kT = kHalf / 16;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -603,9 +605,9 @@ __global__ void __launch_bounds__(kScThreads, 1)
     tc::mbar_init(doneA, 1);
     tc::mbar_init(doneB, 1);
     tc::mbar_init(doneC, 1);
-    tc::mbar_init(s_ready, 8);
-    tc::mbar_init(r_ready, 8);
-    tc::mbar_init(u_ready, 8);
+    tc::mbar_init(s_ready, 4 * G::kSets);
+    tc::mbar_init(r_ready, 4 * G::kSets);
+    tc::mbar_init(u_ready, 4 * G::kSets);
     tc::mbar_init(fin, 1);
     *abort_s = 0;
     tc::mbar_fence_init();
@@ -734,7 +736,7 @@ __global__ void __launch_bounds__(kScThreads, 1)
     tc::mbar_wait(fin, 0, nullptr, 200000000ull);
     __syncwarp();
   } else {
-    // ---------------- warps 2-9: lane quarter q, column half ch of every product ----------------
+    // ---------------- the others: lane quarter q, column set ch of every product ----------------
     const int q = warp & 3;
     const int ch = (warp - 2) >> 2;
     const int r = 32 * q + lane;             // C and S: key channel r
@@ -748,14 +750,34 @@ __global__ void __launch_bounds__(kScThreads, 1)
     float S[kHalf];
 #pragma unroll
     for (int v = 0; v < kHalf; ++v) S[v] = a.state_in != nullptr ? a.state_in[srow + (long)v * kD] : 0.0f;
-    bool ok = true;
-    for (int c = 0; ok && c < nc; ++c) {
-      const int st = c % kStages;
-      const uint32_t par = (uint32_t)c & 1;
-      uint8_t* stage = sm + st * kStage;
-      const float* sc = (const float*)(stage + kStScal);
+    // What the steps of a chunk need of it, fetched while the chunk before is at its last
+    // product (all of it read before this warp's r_ready: the stage may be refilled once C is
+    // done): decays of tokens ta and ta + 8, gamma_C, and V (matrix m of tile pair i as in
+    // store_frag).  Keys behind the sequence belong to another one, or to none: zero.
+    float ga, gb, da, db, gC;
+    uint32_t vw[kT][4];
+    auto fetch = [&](int c) {
+      uint8_t* stage = sm + (c % kStages) * kStage;
+      if (!tc::mbar_wait(&full[c % kStages], (uint32_t)(c / kStages) & 1, abort_s)) return false;
       const int n = min(kC, len - c * kC);
-      // S's parts: row r, columns half ch
+      if (n < kC && r < kC && r >= n)
+        for (int kb = ch; kb < 2; kb += G::kSets)
+#pragma unroll
+          for (int c8 = 0; c8 < 8; ++c8)
+            *(uint4*)(stage + kStKQ + kb * 2 * kTile + stacked(r) * 128 + 16 * c8) = make_uint4(0u, 0u, 0u, 0u);
+      const float* sc = (const float*)(stage + kStScal);
+      ga = sc[ta], gb = sc[ta + 8], da = sc[kC + ta], db = sc[kC + ta + 8], gC = sc[kC - 1];
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < kT; ++i)
+        ldmatrix4(tc::smem_u32(stage + kStV) + swz(16 * q + (lane & 15), vpiece + 2 * i + (lane >> 4)), vw[i]);
+      return true;
+    };
+    bool ok = __all_sync(0xFFFFFFFFu, fetch(0));
+    for (int c = 0; ok && c < nc; ++c) {
+      const uint32_t par = (uint32_t)c & 1;
+      const int n = min(kC, len - c * kC);
+      // S's parts: row r, columns of set ch
 #pragma unroll
       for (int i = 0; i < G::kPieces; ++i) {
         uint32_t w[3][4];
@@ -766,25 +788,10 @@ __global__ void __launch_bounds__(kScThreads, 1)
           *(uint4*)(sm + G::kSAt + G::atom(p, kD) + swz(r, G::piece(p) + G::kPieces * ch + i)) =
               make_uint4(w[p][0], w[p][1], w[p][2], w[p][3]);
       }
-      ok = tc::mbar_wait(&full[st], (uint32_t)(c / kStages) & 1, abort_s);
-      if (!ok) break;
-      if (n < kC && r < kC && r >= n) {
-        // keys behind the sequence belong to another one, or to none: zero (key half ch)
-#pragma unroll
-        for (int c8 = 0; c8 < 8; ++c8)
-          *(uint4*)(stage + kStKQ + ch * 2 * kTile + stacked(r) * 128 + 16 * c8) = make_uint4(0u, 0u, 0u, 0u);
-      }
       tc::fence_async_smem();
       tc::tc_fence_before();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(s_ready);
-      // what the steps to come need of this chunk (read before this warp's r_ready: the stage
-      // may be refilled as soon as C is done)
-      const float ga = sc[ta], gb = sc[ta + 8], da = sc[kC + ta], db = sc[kC + ta + 8], gC = sc[kC - 1];
-      uint32_t vw[kT][4];  // V: matrix m of tile pair i as in store_frag
-#pragma unroll
-      for (int i = 0; i < kT; ++i)
-        ldmatrix4(tc::smem_u32(stage + kStV) + swz(16 * q + (lane & 15), vpiece + 2 * i + (lane >> 4)), vw[i]);
       ok = tc::mbar_wait(doneA, par, abort_s);
       if (!ok) break;
       tc::tc_fence_after();
@@ -841,6 +848,9 @@ __global__ void __launch_bounds__(kScThreads, 1)
                 tc::pack_bf16x2(fmaf(g, y[e], x[e] + z[e]), fmaf(g, y[e + 1], x[e + 1] + z[e + 1]));
         }
       }
+      const float gC_now = gC;
+      if (c + 1 < nc) ok = __all_sync(0xFFFFFFFFu, fetch(c + 1));
+      if (!ok) break;
       ok = tc::mbar_wait(doneC, par, abort_s);
       if (!ok) break;
       tc::tc_fence_after();
@@ -857,7 +867,7 @@ __global__ void __launch_bounds__(kScThreads, 1)
           for (int i = 0; i < kT; ++i) after_wait(z[p][i]);
 #pragma unroll
         for (int v = 0; v < kHalf; ++v)
-          S[v] = fmaf(gC, S[v],
+          S[v] = fmaf(gC_now, S[v],
                       (__uint_as_float(z[2][v >> 4][v & 15]) + __uint_as_float(z[1][v >> 4][v & 15])) +
                           __uint_as_float(z[0][v >> 4][v & 15]));
       }
@@ -880,7 +890,7 @@ cudaError_t launch_scan(const CUtensorMap& tq, const CUtensorMap& tk, const CUte
   const int smem = 1024 + Geo<kV>::kSmem;
   cudaError_t e = cudaFuncSetAttribute(gdn_scan_kernel<kV>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  gdn_scan_kernel<kV><<<(unsigned)((long)a.n_seq * a.H * (kD / kV)), kScThreads, smem, s>>>(tq, tk, tv, a, ws);
+  gdn_scan_kernel<kV><<<(unsigned)((long)a.n_seq * a.H * (kD / kV)), Geo<kV>::kThreads, smem, s>>>(tq, tk, tv, a, ws);
   return cudaGetLastError();
 }
 
@@ -893,7 +903,7 @@ size_t gdn_chunk_workspace(int T, int n_seq, int H) { return (size_t)gdn_slots(T
 
 cudaError_t launch_gdn_chunk(const GdnArgs& a, void* ws, cudaStream_t s) {
   const long wy = gdn_slots(a.T, a.n_seq) * a.H, pairs = (long)a.n_seq * a.H;
-  if (wy >= (1L << 31) || pairs * 4 >= (1L << 31)) return cudaErrorNotSupported;
+  if (wy >= (1L << 31) || pairs * 2 >= (1L << 31)) return cudaErrorNotSupported;
   const long rowk = (long)a.Hk * kD, rowv = (long)a.H * kD;
   CUtensorMap tq, tk, tq16, tk16, tv;
   cudaError_t e = make_tmap_2d(&tq, a.q, rowk, a.T, rowk * 2, 64, 64);
@@ -908,9 +918,10 @@ cudaError_t launch_gdn_chunk(const GdnArgs& a, void* ws, cudaStream_t s) {
   gdn_wy_kernel<<<(unsigned)wy, 128, wsm, s>>>(tq, tk, a, (uint8_t*)ws);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  // four CTAs per (sequence, head) while they all run at once, else two
-  return pairs * 4 <= num_sms() ? launch_scan<32>(tq16, tk16, tv, a, (const uint8_t*)ws, s)
-                                : launch_scan<64>(tq16, tk16, tv, a, (const uint8_t*)ws, s);
+  // the value columns go to as many CTAs as all run at once: each chunk's steps get shorter
+  if (pairs * 8 <= num_sms()) return launch_scan<16>(tq16, tk16, tv, a, (const uint8_t*)ws, s);
+  if (pairs * 4 <= num_sms()) return launch_scan<32>(tq16, tk16, tv, a, (const uint8_t*)ws, s);
+  return launch_scan<64>(tq16, tk16, tv, a, (const uint8_t*)ws, s);
 }
 
 }  // namespace hla
