@@ -405,7 +405,7 @@ __global__ void __launch_bounds__(128, 4)
 //      R_t = V_t - gamma_t (K S^T)_t into shared memory (three parts); gamma_t (Q S^T)_t stays
 //      in registers
 //   B  [T1; G1] (128 x 64) x [R1 | R2 | R3], [T2; G2] x [R1 | R2], [T3; 0] x R1
-//      diag(gamma_C / gamma_t) U (three parts) over R; then, beside C, the output
+//      diag(gamma_C / gamma_t) U (three parts) over R; the output is written beside the next A
 //   C  K^T (128 x 64) x [U1 | U2 | U3]          -> S's update, one row k a thread:
 //      S <- gamma_C S + update in registers, and its parts for the next A.
 // What bounds it is the chain: three products, each with its way through tensor memory and
@@ -423,7 +423,7 @@ constexpr uint32_t kStTx = 5 * kTile + kScal;
 template <int kV>
 struct Geo {
   static constexpr int kAtoms = kV == 64 ? 3 : kV == 32 ? 2 : 1;
-  static constexpr int kHalf = kV == 64 ? 32 : 16;  // columns per warp
+  static constexpr int kHalf = 16;                  // columns per warp
   static constexpr int kSets = kV / kHalf;          // warps per 32 rows
   static constexpr int kThreads = 64 + 128 * kSets;
   static constexpr int kPieces = kHalf / 8;   // 16-byte pieces of a row per warp and part
@@ -750,32 +750,29 @@ __global__ void __launch_bounds__(Geo<kV>::kThreads, 1)
     float S[kHalf];
 #pragma unroll
     for (int v = 0; v < kHalf; ++v) S[v] = a.state_in != nullptr ? a.state_in[srow + (long)v * kD] : 0.0f;
-    // What the steps of a chunk need of it, fetched while the chunk before is at its last
-    // product (all of it read before this warp's r_ready: the stage may be refilled once C is
-    // done): decays of tokens ta and ta + 8, gamma_C, and V (matrix m of tile pair i as in
-    // store_frag).  Keys behind the sequence belong to another one, or to none: zero.
-    float ga, gb, da, db, gC;
-    uint32_t vw[kT][4];
-    auto fetch = [&](int c) {
-      uint8_t* stage = sm + (c % kStages) * kStage;
-      if (!tc::mbar_wait(&full[c % kStages], (uint32_t)(c / kStages) & 1, abort_s)) return false;
-      const int n = min(kC, len - c * kC);
-      if (n < kC && r < kC && r >= n)
-        for (int kb = ch; kb < 2; kb += G::kSets)
+    float ga = 0.0f, gb = 0.0f;       // gamma of tokens ta, ta + 8
+    float y[kHalf / 2];                // Q S^T of the chunk, until its output is written
+    // the output of chunk c's tokens ta and ta + 8, with c's ga, gb and y
+    auto output = [&](int c) {
+      float x[kHalf / 2], z[kHalf / 2];
+      sum_frag<2, kT>(lanes2 + G::kTmB, kV, x);
+      sum_frag<1, kT>(lanes2 + G::kTmB2, kV, z);
+      const int n = len - c * kC;
+      __nv_bfloat16* orow =
+          (__nv_bfloat16*)a.o + ((long)(s0 + c * kC + ta) * a.H + h) * kD + v0 + kHalf * ch + 2 * (lane & 3);
 #pragma unroll
-          for (int c8 = 0; c8 < 8; ++c8)
-            *(uint4*)(stage + kStKQ + kb * 2 * kTile + stacked(r) * 128 + 16 * c8) = make_uint4(0u, 0u, 0u, 0u);
-      const float* sc = (const float*)(stage + kStScal);
-      ga = sc[ta], gb = sc[ta + 8], da = sc[kC + ta], db = sc[kC + ta + 8], gC = sc[kC - 1];
-      __syncwarp();
-#pragma unroll
-      for (int i = 0; i < kT; ++i)
-        ldmatrix4(tc::smem_u32(stage + kStV) + swz(16 * q + (lane & 15), vpiece + 2 * i + (lane >> 4)), vw[i]);
-      return true;
+      for (int e = 0; e < kHalf / 2; e += 2) {
+        const bool second = (e & 2) != 0;
+        const float g = second ? gb : ga;
+        if (ta + (second ? 8 : 0) < n)
+          *(uint32_t*)(orow + (second ? 8L * a.H * kD : 0) + 8 * (e >> 2)) =
+              tc::pack_bf16x2(fmaf(g, y[e], x[e] + z[e]), fmaf(g, y[e + 1], x[e + 1] + z[e + 1]));
+      }
     };
-    bool ok = __all_sync(0xFFFFFFFFu, fetch(0));
-    for (int c = 0; ok && c < nc; ++c) {
+    bool ok = true;
+    for (int c = 0; c < nc; ++c) {
       const uint32_t par = (uint32_t)c & 1;
+      uint8_t* stage = sm + (c % kStages) * kStage;
       const int n = min(kC, len - c * kC);
       // S's parts: row r, columns of set ch
 #pragma unroll
@@ -788,11 +785,34 @@ __global__ void __launch_bounds__(Geo<kV>::kThreads, 1)
           *(uint4*)(sm + G::kSAt + G::atom(p, kD) + swz(r, G::piece(p) + G::kPieces * ch + i)) =
               make_uint4(w[p][0], w[p][1], w[p][2], w[p][3]);
       }
+      if (n < kC) {
+        // keys behind the sequence belong to another one, or to none: zero
+        ok = __all_sync(0xFFFFFFFFu, tc::mbar_wait(&full[c % kStages], (uint32_t)(c / kStages) & 1, abort_s));
+        if (!ok) break;
+        if (r < kC && r >= n)
+          for (int kb = ch; kb < 2; kb += G::kSets)
+#pragma unroll
+            for (int c8 = 0; c8 < 8; ++c8)
+              *(uint4*)(stage + kStKQ + kb * 2 * kTile + stacked(r) * 128 + 16 * c8) = make_uint4(0u, 0u, 0u, 0u);
+      }
       tc::fence_async_smem();
       tc::tc_fence_before();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(s_ready);
-      ok = tc::mbar_wait(doneA, par, abort_s);
+      // while A runs: the output of the chunk before (B's accumulators are not written again
+      // before r_ready), and what the next steps need of this chunk (read before r_ready: the
+      // stage may be refilled once C is done)
+      if (c > 0) output(c - 1);
+      ok = __all_sync(0xFFFFFFFFu, tc::mbar_wait(&full[c % kStages], (uint32_t)(c / kStages) & 1, abort_s));
+      if (!ok) break;
+      const float* sc = (const float*)(stage + kStScal);
+      ga = sc[ta], gb = sc[ta + 8];
+      const float da = sc[kC + ta], db = sc[kC + ta + 8], gC = sc[kC - 1];
+      uint32_t vw[kT][4];  // V: matrix m of tile pair i as in store_frag
+#pragma unroll
+      for (int i = 0; i < kT; ++i)
+        ldmatrix4(tc::smem_u32(stage + kStV) + swz(16 * q + (lane & 15), vpiece + 2 * i + (lane >> 4)), vw[i]);
+      ok = __all_sync(0xFFFFFFFFu, tc::mbar_wait(doneA, par, abort_s));
       if (!ok) break;
       tc::tc_fence_after();
       float x[kHalf / 2];
@@ -815,9 +835,8 @@ __global__ void __launch_bounds__(Geo<kV>::kThreads, 1)
       tc::tc_fence_before();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(r_ready);
-      float y[kHalf / 2];
       sum_frag<2, kT>(lanes2 + G::kTmA, kV, y);  // Q S^T, off by 2^-15: it goes to a bf16 output
-      ok = tc::mbar_wait(doneB, par, abort_s);
+      ok = __all_sync(0xFFFFFFFFu, tc::mbar_wait(doneB, par, abort_s));
       if (!ok) break;
       tc::tc_fence_after();
       {
@@ -832,26 +851,7 @@ __global__ void __launch_bounds__(Geo<kV>::kThreads, 1)
       tc::tc_fence_before();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(u_ready);
-      {
-        // the output of tokens ta and ta + 8, beside C
-        float z[kHalf / 2];
-        sum_frag<2, kT>(lanes2 + G::kTmB, kV, x);
-        sum_frag<1, kT>(lanes2 + G::kTmB2, kV, z);
-        __nv_bfloat16* orow =
-            (__nv_bfloat16*)a.o + ((long)(s0 + c * kC + ta) * a.H + h) * kD + v0 + kHalf * ch + 2 * (lane & 3);
-#pragma unroll
-        for (int e = 0; e < kHalf / 2; e += 2) {
-          const bool second = (e & 2) != 0;
-          const float g = second ? gb : ga;
-          if (ta + (second ? 8 : 0) < n)
-            *(uint32_t*)(orow + (second ? 8L * a.H * kD : 0) + 8 * (e >> 2)) =
-                tc::pack_bf16x2(fmaf(g, y[e], x[e] + z[e]), fmaf(g, y[e + 1], x[e + 1] + z[e + 1]));
-        }
-      }
-      const float gC_now = gC;
-      if (c + 1 < nc) ok = __all_sync(0xFFFFFFFFu, fetch(c + 1));
-      if (!ok) break;
-      ok = tc::mbar_wait(doneC, par, abort_s);
+      ok = __all_sync(0xFFFFFFFFu, tc::mbar_wait(doneC, par, abort_s));
       if (!ok) break;
       tc::tc_fence_after();
       {
@@ -867,11 +867,12 @@ __global__ void __launch_bounds__(Geo<kV>::kThreads, 1)
           for (int i = 0; i < kT; ++i) after_wait(z[p][i]);
 #pragma unroll
         for (int v = 0; v < kHalf; ++v)
-          S[v] = fmaf(gC_now, S[v],
+          S[v] = fmaf(gC, S[v],
                       (__uint_as_float(z[2][v >> 4][v & 15]) + __uint_as_float(z[1][v >> 4][v & 15])) +
                           __uint_as_float(z[0][v >> 4][v & 15]));
       }
     }
+    if (ok) output(nc - 1);
     if (ok && a.state_out != nullptr) {
 #pragma unroll
       for (int v = 0; v < kHalf; ++v) a.state_out[srow + (long)v * kD] = S[v];
