@@ -24,36 +24,53 @@ namespace {
 
 // ---- mass from a gate matrix -----------------------------------------------------------
 
-constexpr int kMassCols = 32;   // columns per CTA: one 128-byte segment of a row
-constexpr int kMassWarps = 16;  // rows in flight per CTA
+// One CTA per (sequence, head) and 32 kQ columns: a warp reads kQ 128-byte segments of a row,
+// 16 warps take the rows in turn (each its own in ascending order), and the 16 sums of a column
+// are added in warp order: the same bits every time.
+constexpr int kMassWarps = 16;
 
+template <int kQ>
 __global__ void __launch_bounds__(32 * kMassWarps) gate_mass_kernel(const float* __restrict__ gates, int N, int ncols,
                                                                      int C, int T, float thr, float* __restrict__ mass,
                                                                      long mass_stride) {
-  __shared__ float part[kMassWarps][kMassCols];
+  constexpr int kCols = 32 * kQ;
+  __shared__ float part[kMassWarps][kCols];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const int tiles = (ncols + kMassCols - 1) / kMassCols;
+  const int tiles = (ncols + kCols - 1) / kCols;
   const long bh = blockIdx.x / tiles;
-  const int j0 = (int)(blockIdx.x % tiles) * kMassCols;
-  const int j = j0 + lane;
-  const float* G = gates + bh * (long)N * N;
-  float acc = 0.0f;
+  const int j0 = (int)(blockIdx.x % tiles) * kCols;
+  const float* G = gates + bh * (long)N * N + j0 + lane;
+  float acc[kQ] = {};
   // rows i > j hold a weight on chunk j; row i stands for the tokens of chunk i
+  int i = j0 + 1 + w;
+  for (; i < min(N, j0 + kCols); i += kMassWarps) {  // rows that meet the diagonal
+    const float wt = (float)min(C, T - i * C);
+#pragma unroll
+    for (int q = 0; q < kQ; ++q)
+      if (j0 + 32 * q + lane < i) {
+        const float g = __ldg(G + (long)i * N + 32 * q);
+        if (thr <= 0.0f || g >= thr) acc[q] = fmaf(wt, g, acc[q]);
+      }
+  }
 #pragma unroll 8
-  for (int i = j0 + 1 + w; i < N; i += kMassWarps) {
-    if (j < i) {
-      const float g = __ldg(G + (long)i * N + j);
-      if (thr <= 0.0f || g >= thr) acc = fmaf((float)min(C, T - i * C), g, acc);
+  for (; i < N; i += kMassWarps) {  // below it every column of the tile counts (j0 + kCols <= i < N)
+    const float wt = (float)min(C, T - i * C);
+#pragma unroll
+    for (int q = 0; q < kQ; ++q) {
+      const float g = __ldg(G + (long)i * N + 32 * q);
+      acc[q] = fmaf(wt, thr <= 0.0f || g >= thr ? g : 0.0f, acc[q]);
     }
   }
-  part[w][lane] = acc;
-  __syncthreads();
-  if (w == 0 && j < ncols) {
-    float s = 0.0f;
 #pragma unroll
-    for (int k = 0; k < kMassWarps; ++k) s += part[k][lane];
-    mass[bh * mass_stride + j] = s;
-  }
+  for (int q = 0; q < kQ; ++q) part[w][32 * q + lane] = acc[q];
+  __syncthreads();
+  for (int c = threadIdx.x; c < kCols; c += 32 * kMassWarps)
+    if (j0 + c < ncols) {
+      float s = 0.0f;
+#pragma unroll
+      for (int k = 0; k < kMassWarps; ++k) s += part[k][c];
+      mass[bh * mass_stride + j0 + c] = s;
+    }
 }
 
 // ---- selection ------------------------------------------------------------------------
@@ -111,11 +128,22 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictArgs a) 
         if ((key & mask) == prefix) atomicAdd(&hist[(key >> shift) & 255u], 1);
       }
       __syncthreads();
-      // thread = digit: how many keys have a larger one
-      int above = 0;
-      for (int d = tid + 1; d < 256; ++d) above += hist[d];
-      if (above < want && above + hist[tid] >= want) {
-        pick[0] = tid;
+      // thread = digit 255 - tid: how many keys have a larger one (a prefix over the threads)
+      const int mine = hist[255 - tid];
+      int above = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int up = __shfl_up_sync(0xFFFFFFFFu, above, o);
+        if ((tid & 31) >= o) above += up;
+      }
+      if ((tid & 31) == 31) wsum[tid >> 5] = above;
+      __syncthreads();
+#pragma unroll
+      for (int k = 0; k < kSelThreads / 32 - 1; ++k)
+        if (k < (tid >> 5)) above += wsum[k];
+      above -= mine;
+      if (above < want && above + mine >= want) {
+        pick[0] = 255 - tid;
         pick[1] = above;
       }
       __syncthreads();
@@ -222,10 +250,15 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(EvictArgs a, u
 
 cudaError_t launch_gate_mass(const float* gates, int B, int H, int N, int ncols, int C, int T, float thr, float* mass,
                              long mass_stride, cudaStream_t s) {
-  const long blocks = (long)B * H * ((ncols + kMassCols - 1) / kMassCols);
+  const long BH = (long)B * H;
+  // wide tiles while they fill the GPU, else narrow ones
+  const bool wide = BH * ((ncols + 127) / 128) >= 2L * num_sms();
+  const int cols = wide ? 128 : 32;
+  const long blocks = BH * ((ncols + cols - 1) / cols);
   if (blocks <= 0) return cudaSuccess;
   if (blocks >= (1L << 31)) return cudaErrorNotSupported;
-  gate_mass_kernel<<<(unsigned)blocks, 32 * kMassWarps, 0, s>>>(gates, N, ncols, C, T, thr, mass, mass_stride);
+  auto* k = wide ? gate_mass_kernel<4> : gate_mass_kernel<1>;
+  k<<<(unsigned)blocks, 32 * kMassWarps, 0, s>>>(gates, N, ncols, C, T, thr, mass, mass_stride);
   return cudaGetLastError();
 }
 
