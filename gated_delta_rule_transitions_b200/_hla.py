@@ -170,35 +170,52 @@ def decode_workspace_bytes(cfg: HlaConfig, max_chunks: int) -> int:
 
 
 def _arg(t, name, dtype, numel, device):
-    """Device pointer of a tensor argument of the given dtype and size (None stays None)."""
+    """Device pointer of a tensor argument of the given dtype and size on CUDA device number
+    `device` (None stays None)."""
     if t is None:
         return None
+    # the checks in one expression first: a step's binding is most of its time
+    if (isinstance(t, torch.Tensor) and t.is_cuda and t.get_device() == device and t.dtype is dtype
+            and t.numel() == numel and t.is_contiguous()):
+        return t.data_ptr()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name}: libhla takes CUDA device tensors only (no CPU path)")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the call's other tensors on {device}")
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, the call's other tensors on cuda:{device}")
     if t.dtype != dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
     if t.numel() != numel:
         raise ValueError(f"{name}: expected {numel} elements, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _device(t, name):
+    """CUDA device number of the tensor that says where a call runs."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: libhla takes CUDA device tensors only (no CPU path)")
+    return t.get_device()
 
 
 def _run(device, stream, fn, *args):
-    """Call fn(*args, stream) with `device` current, on its current stream by default."""
+    """Call fn(*args, stream) with CUDA device number `device` current, on its current stream
+    by default."""
     if stream is None:
-        stream = torch.cuda.current_stream(device)
-    elif stream.device != device:
-        raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
-    if device.index == torch.cuda.current_device():
-        _check(fn(*args, stream.cuda_stream))
+        s = torch.cuda.current_stream(device).cuda_stream
+    elif stream.device.index != device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{device}")
+    else:
+        s = stream.cuda_stream
+    if device == torch.cuda.current_device():
+        st = fn(*args, s)
     else:
         with torch.cuda.device(device):
-            _check(fn(*args, stream.cuda_stream))
+            st = fn(*args, s)
+    if st != HLA_OK:
+        _check(st)
 
 
 _DTYPES = {HLA_F32: torch.float32, HLA_BF16: torch.bfloat16}
@@ -256,7 +273,7 @@ class Cache:
         st = self.struct
         st.max_chunks, st.B, st.H, st.C, st.d, st.dtype = max_chunks, B, H, C, d, cfg.dtype
         st.format, st.pool_window, st.decay_mode = cfg.cache_format, cfg.pool_window, cfg.decay_mode
-        device = next(iter(buffers.values())).device
+        device = _device(buffers["rk"], "rk")
         for name, t in buffers.items():
             if t is None and name != "mass":
                 raise TypeError(f"{name}: expected a torch.Tensor")
@@ -271,10 +288,10 @@ class Cache:
         """Accumulate every closed chunk's gate weight from now on; returns the
         [B, H, max_chunks] float32 tensor that holds it (given or made here, zeroed)."""
         s = self.struct
-        device = self.mem.device if self.mem is not None else self.buffers["rk"].device
+        device = (self.mem if self.mem is not None else self.buffers["rk"]).get_device()
         shape = (s.B, s.H, s.max_chunks)
         if mass is None:
-            mass = torch.empty(shape, dtype=torch.float32, device=device)
+            mass = torch.empty(shape, dtype=torch.float32, device=torch.device("cuda", device))
         p = _arg(mass, "mass", torch.float32, s.B * s.H * s.max_chunks, device)
         _run(device, stream, lib().hla_cache_track_mass, ctypes.byref(s), p)
         self.mass = mass
@@ -319,17 +336,19 @@ def hla_gate_mass(cfg, gates, mass_out, stream=None):
     """Weight that every chunk carried over a prompt, from its gate matrix."""
     n = (cfg.T + cfg.C - 1) // cfg.C if cfg.C > 0 else 0
     bh = cfg.B * cfg.H
-    g = _arg(gates, "gates", torch.float32, bh * n * n, gates.device)
-    m = _arg(mass_out, "mass_out", torch.float32, bh * n, gates.device)
-    _run(gates.device, stream, lib().hla_gate_mass, ctypes.byref(cfg), g, m)
+    dev = _device(gates, "gates")
+    g = _arg(gates, "gates", torch.float32, bh * n * n, dev)
+    m = _arg(mass_out, "mass_out", torch.float32, bh * n, dev)
+    _run(dev, stream, lib().hla_gate_mass, ctypes.byref(cfg), g, m)
     return mass_out
 
 
 def hla_cache_evict(cfg, src, dst, keep, recent, kept_out, stream=None):
     """Keep per (sequence, head) the `recent` last chunks of `src` and the heaviest others,
     `keep` in all; `dst` is `src` (in place) or another cache."""
-    p = _arg(kept_out, "kept_out", torch.int32, cfg.B * cfg.H * keep, kept_out.device)
-    _run(kept_out.device, stream, lib().hla_cache_evict, ctypes.byref(cfg), ctypes.byref(src.struct),
+    dev = _device(kept_out, "kept_out")
+    p = _arg(kept_out, "kept_out", torch.int32, cfg.B * cfg.H * keep, dev)
+    _run(dev, stream, lib().hla_cache_evict, ctypes.byref(cfg), ctypes.byref(src.struct),
          ctypes.byref(dst.struct), keep, recent, p)
     return kept_out
 
@@ -344,22 +363,23 @@ def gdn_workspace_bytes(cfg: GdnConfig, T: int) -> int:
     return int(lib().gdn_workspace_bytes(ctypes.byref(cfg), T))
 
 
-def _gdn_args(cfg, T, q, k, v, alpha, beta, o):
-    dt, dev, d = _DTYPES.get(cfg.dtype, q.dtype), q.device, cfg.dk
-    return (_arg(q, "q", dt, T * cfg.Hk * d, dev), _arg(k, "k", dt, T * cfg.Hk * d, dev),
-            _arg(v, "v", dt, T * cfg.H * d, dev),
-            _arg(alpha, "alpha", torch.float32, T * cfg.H * (d if cfg.decay_mode else 1), dev),
-            _arg(beta, "beta", torch.float32, T * cfg.H, dev), _arg(o, "o", dt, T * cfg.H * d, dev))
+def _gdn_args(cfg, T, dev, q, k, v, alpha, beta, o):
+    dt, d, f32 = _DTYPES.get(cfg.dtype), cfg.dk, torch.float32
+    nk, nb = T * cfg.Hk * d, T * cfg.H
+    nv = nb * d
+    return (_arg(q, "q", dt, nk, dev), _arg(k, "k", dt, nk, dev), _arg(v, "v", dt, nv, dev),
+            _arg(alpha, "alpha", f32, nv if cfg.decay_mode else nb, dev), _arg(beta, "beta", f32, nb, dev),
+            _arg(o, "o", dt, nv, dev))
 
 
 def gdn_forward(cfg: GdnConfig, q, k, v, alpha, beta, cu_seqlens, o, state_in=None, state_out=None, slots=None,
                 workspace=None, stream=None):
     """Ragged sequences through the gated delta rule, states in and out (include/hla.h)."""
-    T, dev = v.shape[0], q.device
-    pq, pk, pv, pa, pb, po = _gdn_args(cfg, T, q, k, v, alpha, beta, o)
+    T, dev = v.shape[0], _device(q, "q")
+    pq, pk, pv, pa, pb, po = _gdn_args(cfg, T, dev, q, k, v, alpha, beta, o)
     ns = cfg.n_slots * cfg.H * cfg.dv * cfg.dk
     if workspace is None:
-        workspace = torch.empty(max(gdn_workspace_bytes(cfg, T), 256), dtype=torch.uint8, device=dev)
+        workspace = torch.empty(max(gdn_workspace_bytes(cfg, T), 256), dtype=torch.uint8, device=q.device)
         if stream is not None:
             workspace.record_stream(stream)
     nb = workspace.numel() * workspace.element_size()
@@ -373,8 +393,8 @@ def gdn_forward(cfg: GdnConfig, q, k, v, alpha, beta, cu_seqlens, o, state_in=No
 
 def gdn_step(cfg: GdnConfig, q, k, v, alpha, beta, state, o, slots=None, stream=None):
     """One token per sequence through the gated delta rule, the states updated in place."""
-    dev = q.device
-    pq, pk, pv, pa, pb, po = _gdn_args(cfg, cfg.n_seq, q, k, v, alpha, beta, o)
+    dev = _device(q, "q")
+    pq, pk, pv, pa, pb, po = _gdn_args(cfg, cfg.n_seq, dev, q, k, v, alpha, beta, o)
     _run(dev, stream, lib().gdn_step, ctypes.byref(cfg), pq, pk, pv, pa, pb,
          _arg(slots, "slots", torch.int32, cfg.n_seq, dev),
          _arg(state, "state", torch.float32, cfg.n_slots * cfg.H * cfg.dv * cfg.dk, dev), po)

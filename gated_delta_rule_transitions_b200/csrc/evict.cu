@@ -15,6 +15,8 @@
 //                      the chunk and takes the kept chunks in ascending order; entry i comes
 //                      from a chunk kept[i] >= i, and reads run ahead of writes, so the move
 //                      is safe in place without any barrier.
+#include <cooperative_groups.h>
+
 #include "common.cuh"
 #include "kernels.cuh"
 
@@ -24,26 +26,33 @@ namespace {
 
 // ---- mass from a gate matrix -----------------------------------------------------------
 
-// One CTA per (sequence, head) and 32 kQ columns: a warp reads kQ 128-byte segments of a row,
-// 16 warps take the rows in turn (each its own in ascending order), and the 16 sums of a column
-// are added in warp order: the same bits every time.
-constexpr int kMassWarps = 16;
+// One cluster of four CTAs per (sequence, head) and 32 kQ columns: a warp reads kQ 128-byte
+// segments of a row, the cluster's 32 warps take the rows in turn (each its own in ascending
+// order), and the 32 sums of a column are added in warp order, the other CTAs' through
+// distributed shared memory: the same bits every time.  The row split evens out the triangle
+// (a tile's rows go from all to few) and leaves work for every SM where heads are few.
+constexpr int kMassWarps = 8;
+constexpr int kMassCtas = 4;
 
 template <int kQ>
-__global__ void __launch_bounds__(32 * kMassWarps) gate_mass_kernel(const float* __restrict__ gates, int N, int ncols,
+__global__ void __cluster_dims__(kMassCtas) __launch_bounds__(32 * kMassWarps) gate_mass_kernel(const float* __restrict__ gates, int N, int ncols,
                                                                      int C, int T, float thr, float* __restrict__ mass,
                                                                      long mass_stride) {
   constexpr int kCols = 32 * kQ;
   __shared__ float part[kMassWarps][kCols];
+  namespace cg = cooperative_groups;
+  const cg::cluster_group cluster = cg::this_cluster();
+  const int rank = (int)cluster.block_rank();
+  constexpr int kStep = kMassWarps * kMassCtas;
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int tiles = (ncols + kCols - 1) / kCols;
-  const long bh = blockIdx.x / tiles;
-  const int j0 = (int)(blockIdx.x % tiles) * kCols;
+  const long bh = blockIdx.x / kMassCtas / tiles;
+  const int j0 = (int)(blockIdx.x / kMassCtas % tiles) * kCols;
   const float* G = gates + bh * (long)N * N + j0 + lane;
   float acc[kQ] = {};
   // rows i > j hold a weight on chunk j; row i stands for the tokens of chunk i
-  int i = j0 + 1 + w;
-  for (; i < min(N, j0 + kCols); i += kMassWarps) {  // rows that meet the diagonal
+  int i = j0 + 1 + rank * kMassWarps + w;
+  for (; i < min(N, j0 + kCols); i += kStep) {  // rows that meet the diagonal
     const float wt = (float)min(C, T - i * C);
 #pragma unroll
     for (int q = 0; q < kQ; ++q)
@@ -53,7 +62,7 @@ __global__ void __launch_bounds__(32 * kMassWarps) gate_mass_kernel(const float*
       }
   }
 #pragma unroll 8
-  for (; i < N; i += kMassWarps) {  // below it every column of the tile counts (j0 + kCols <= i < N)
+  for (; i < N; i += kStep) {  // below it every column of the tile counts (j0 + kCols <= i < N)
     const float wt = (float)min(C, T - i * C);
 #pragma unroll
     for (int q = 0; q < kQ; ++q) {
@@ -63,14 +72,19 @@ __global__ void __launch_bounds__(32 * kMassWarps) gate_mass_kernel(const float*
   }
 #pragma unroll
   for (int q = 0; q < kQ; ++q) part[w][32 * q + lane] = acc[q];
-  __syncthreads();
-  for (int c = threadIdx.x; c < kCols; c += 32 * kMassWarps)
-    if (j0 + c < ncols) {
-      float s = 0.0f;
+  cluster.sync();
+  if (rank == 0)
+    for (int c = threadIdx.x; c < kCols; c += 32 * kMassWarps)
+      if (j0 + c < ncols) {
+        float s = 0.0f;
+        for (int r = 0; r < kMassCtas; ++r) {
+          const float* p = cluster.map_shared_rank(&part[0][0], r);
 #pragma unroll
-      for (int k = 0; k < kMassWarps; ++k) s += part[k][c];
-      mass[bh * mass_stride + j0 + c] = s;
-    }
+          for (int k = 0; k < kMassWarps; ++k) s += p[k * kCols + c];
+        }
+        mass[bh * mass_stride + j0 + c] = s;
+      }
+  cluster.sync();  // the other CTAs' shared memory stays until it has been read
 }
 
 // ---- selection ------------------------------------------------------------------------
@@ -196,10 +210,11 @@ __device__ __forceinline__ void move_column(const uint4* src, uint4* dst, long p
   }
 }
 
-// grid (B H (column blocks + 1), splits of the kept list).  The last column block of a
-// (sequence, head) finishes it: the weights move with their chunks, the open chunk and
-// the counters go along to another cache, and the count changes.  Nothing here but that
-// last step reads the counts (the list ends at its first -1), so it may change them.
+// grid (B H (column blocks + 1), splits of the kept list).  A thread has one 16-byte column of
+// the per-chunk arrays or, into another cache, of the open chunk's.  The last block of a
+// (sequence, head) finishes it: the weights move with their chunks and the counters change.
+// Nothing here but that last step reads the counts (the list ends at its first -1), so it
+// may change them.
 __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(EvictArgs a, unsigned blocks) {
   const long bh = blockIdx.x / (blocks + 1);
   const unsigned blk = blockIdx.x % (blocks + 1);
@@ -208,13 +223,21 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(EvictArgs a, u
   if (blk < blocks) {
     const int per = (a.keep + gridDim.y - 1) / gridDim.y;
     const int i0 = min(a.keep, (int)blockIdx.y * per), i1 = min(a.keep, i0 + per);
-    // this thread's 16-byte column among all arrays' columns
     long col = (long)blk * kMoveThreads + tid;
     for (int x = 0; x < a.n_arrays; ++x) {
       const long cols = a.chunk_bytes[x] / 16;
       if (col < cols) {
         move_column((const uint4*)a.src[x] + bh * a.src_chunks * cols + col,
                     (uint4*)a.dst[x] + bh * a.dst_chunks * cols + col, cols, kept, i0, i1, a.in_place);
+        return;
+      }
+      col -= cols;
+    }
+    if (a.in_place || blockIdx.y != 0) return;
+    for (int x = 0; x < a.n_open; ++x) {
+      const long cols = a.open_bytes[x] / 16;
+      if (col < cols) {
+        ((uint4*)a.open_dst[x])[bh * cols + col] = ((const uint4*)a.open_src[x])[bh * cols + col];
         return;
       }
       col -= cols;
@@ -234,16 +257,10 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(EvictArgs a, u
       if (j >= 0) dst[i] = m;
     }
   }
-  if (!a.in_place) {
-    for (int x = 0; x < a.n_open; ++x) {
-      const long cols = a.open_bytes[x] / 16;
-      const uint4* s4 = (const uint4*)a.open_src[x] + bh * cols;
-      uint4* d4 = (uint4*)a.open_dst[x] + bh * cols;
-      for (long c = tid; c < cols; c += kMoveThreads) d4[c] = s4[c];
-    }
-    if (h == 0 && tid == 0) a.m_dst[b] = a.m_src[b];
+  if (h == 0 && tid == 0) {
+    if (!a.in_place) a.m_dst[b] = a.m_src[b];
+    a.n_dst[b] = min(max(0, min(a.n_src[b], a.src_chunks)), a.keep);
   }
-  if (h == 0 && tid == 0) a.n_dst[b] = min(max(0, min(a.n_src[b], a.src_chunks)), a.keep);
 }
 
 }  // namespace
@@ -252,13 +269,13 @@ cudaError_t launch_gate_mass(const float* gates, int B, int H, int N, int ncols,
                              long mass_stride, cudaStream_t s) {
   const long BH = (long)B * H;
   // wide tiles while they fill the GPU, else narrow ones
-  const bool wide = BH * ((ncols + 127) / 128) >= 2L * num_sms();
+  const bool wide = BH * ((ncols + 127) / 128) * kMassCtas >= 2L * num_sms();
   const int cols = wide ? 128 : 32;
   const long blocks = BH * ((ncols + cols - 1) / cols);
   if (blocks <= 0) return cudaSuccess;
-  if (blocks >= (1L << 31)) return cudaErrorNotSupported;
+  if (blocks * kMassCtas >= (1L << 31)) return cudaErrorNotSupported;
   auto* k = wide ? gate_mass_kernel<4> : gate_mass_kernel<1>;
-  k<<<(unsigned)blocks, 32 * kMassWarps, 0, s>>>(gates, N, ncols, C, T, thr, mass, mass_stride);
+  k<<<(unsigned)(blocks * kMassCtas), 32 * kMassWarps, 0, s>>>(gates, N, ncols, C, T, thr, mass, mass_stride);
   return cudaGetLastError();
 }
 
@@ -266,6 +283,8 @@ cudaError_t launch_evict(const EvictArgs& a, cudaStream_t s) {
   const long BH = (long)a.B * a.H;
   long cols = 0;
   for (int x = 0; x < a.n_arrays; ++x) cols += a.chunk_bytes[x] / 16;
+  if (!a.in_place)
+    for (int x = 0; x < a.n_open; ++x) cols += a.open_bytes[x] / 16;
   const long blocks = (cols + kMoveThreads - 1) / kMoveThreads;
   if (BH * (blocks + 1) >= (1L << 31)) return cudaErrorNotSupported;
   evict_select_kernel<<<(unsigned)BH, kSelThreads, 0, s>>>(a);

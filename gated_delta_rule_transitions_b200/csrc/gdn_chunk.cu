@@ -169,6 +169,8 @@ __global__ void __launch_bounds__(128, 4)
   uint32_t* tmem_s = lmax + 2;
   volatile int* abort_s = (volatile int*)(tmem_s + 1);
 
+  // gdn_scan_kernel's blocks may take their places while this grid drains
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int h = blockIdx.x % a.H;
   const int slot = blockIdx.x / a.H;
@@ -629,6 +631,9 @@ __global__ void __launch_bounds__(Geo<kV>::kThreads, 1)
       tc::tma_prefetch_desc(&tmK);
       tc::tma_prefetch_desc(&tmV);
       const uint8_t* wy = ws + ((long)base * a.H + h) * kSlot;
+      // launched as gdn_wy_kernel's programmatic dependent: the workspace is its output (the
+      // call's inputs were there before that grid started)
+      asm volatile("griddepcontrol.wait;" ::: "memory");
       auto load_stage = [&](int c) {
         const int st = c % kStages;
         if (c >= kStages && !tc::mbar_wait(&empty[st], ((c / kStages) - 1) & 1, abort_s)) return false;
@@ -891,8 +896,17 @@ cudaError_t launch_scan(const CUtensorMap& tq, const CUtensorMap& tk, const CUte
   const int smem = 1024 + Geo<kV>::kSmem;
   cudaError_t e = cudaFuncSetAttribute(gdn_scan_kernel<kV>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  gdn_scan_kernel<kV><<<(unsigned)((long)a.n_seq * a.H * (kD / kV)), Geo<kV>::kThreads, smem, s>>>(tq, tk, tv, a, ws);
-  return cudaGetLastError();
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((long)a.n_seq * a.H * (kD / kV)));
+  cfg.blockDim = dim3(Geo<kV>::kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, gdn_scan_kernel<kV>, tq, tk, tv, a, ws);
 }
 
 }  // namespace

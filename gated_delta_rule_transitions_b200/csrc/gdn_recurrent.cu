@@ -74,6 +74,10 @@ __global__ void __launch_bounds__(kThreads) gdn_recurrent_kernel(GdnArgs a) {
   constexpr int kSeg = seg_len<Tio, kChan>();
   __shared__ __align__(16) Stage<D, R, Tio, kChan> st[2];
   __shared__ float os[kSeg][kRows];
+  // launched as a programmatic dependent: the next step's blocks may take their places while
+  // this grid drains; all that is read comes after the wait for the grid before
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = threadIdx.x;
   const int split = blockIdx.x % kSplit;
   const long sh = blockIdx.x / kSplit;
@@ -233,11 +237,17 @@ template <int D, int R, typename Tio>
 cudaError_t launch_r(const GdnArgs& a, cudaStream_t s) {
   const long blocks = (long)a.n_seq * a.H * (D / (16 * R));
   if (blocks >= (1L << 31)) return cudaErrorNotSupported;
-  if (a.alpha_vec)
-    gdn_recurrent_kernel<D, R, Tio, true><<<(unsigned)blocks, kThreads, 0, s>>>(a);
-  else
-    gdn_recurrent_kernel<D, R, Tio, false><<<(unsigned)blocks, kThreads, 0, s>>>(a);
-  return cudaGetLastError();
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)blocks);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return a.alpha_vec ? cudaLaunchKernelEx(&cfg, gdn_recurrent_kernel<D, R, Tio, true>, a)
+                     : cudaLaunchKernelEx(&cfg, gdn_recurrent_kernel<D, R, Tio, false>, a);
 }
 
 template <int D, typename Tio>
