@@ -26,13 +26,13 @@ namespace {
 
 // ---- mass from a gate matrix -----------------------------------------------------------
 
-// One cluster of four CTAs per (sequence, head) and 32 kQ columns: a warp reads kQ 128-byte
-// segments of a row, the cluster's 32 warps take the rows in turn (each its own in ascending
-// order), and the 32 sums of a column are added in warp order, the other CTAs' through
+// One cluster of eight CTAs per (sequence, head) and 32 kQ columns: a warp reads kQ 128-byte
+// segments of a row, the cluster's 64 warps take the rows in turn (each its own in ascending
+// order), and the 64 sums of a column are added in warp order, the other CTAs' through
 // distributed shared memory: the same bits every time.  The row split evens out the triangle
 // (a tile's rows go from all to few) and leaves work for every SM where heads are few.
 constexpr int kMassWarps = 8;
-constexpr int kMassCtas = 4;
+constexpr int kMassCtas = 8;
 
 template <int kQ>
 __global__ void __cluster_dims__(kMassCtas) __launch_bounds__(32 * kMassWarps) gate_mass_kernel(const float* __restrict__ gates, int N, int ncols,
@@ -61,7 +61,7 @@ __global__ void __cluster_dims__(kMassCtas) __launch_bounds__(32 * kMassWarps) g
         if (thr <= 0.0f || g >= thr) acc[q] = fmaf(wt, g, acc[q]);
       }
   }
-#pragma unroll 8
+#pragma unroll(kQ == 8 ? 4 : 8)
   for (; i < N; i += kStep) {  // below it every column of the tile counts (j0 + kCols <= i < N)
     const float wt = (float)min(C, T - i * C);
 #pragma unroll
@@ -269,12 +269,12 @@ cudaError_t launch_gate_mass(const float* gates, int B, int H, int N, int ncols,
                              long mass_stride, cudaStream_t s) {
   const long BH = (long)B * H;
   // wide tiles while they fill the GPU, else narrow ones
-  const bool wide = BH * ((ncols + 127) / 128) * kMassCtas >= 2L * num_sms();
-  const int cols = wide ? 128 : 32;
+  auto fills = [&](int cols) { return BH * ((ncols + cols - 1) / cols) * kMassCtas >= 4L * num_sms(); };
+  const int cols = fills(256) ? 256 : fills(128) ? 128 : 32;
   const long blocks = BH * ((ncols + cols - 1) / cols);
   if (blocks <= 0) return cudaSuccess;
   if (blocks * kMassCtas >= (1L << 31)) return cudaErrorNotSupported;
-  auto* k = wide ? gate_mass_kernel<4> : gate_mass_kernel<1>;
+  auto* k = cols == 256 ? gate_mass_kernel<8> : cols == 128 ? gate_mass_kernel<4> : gate_mass_kernel<1>;
   k<<<(unsigned)(blocks * kMassCtas), 32 * kMassWarps, 0, s>>>(gates, N, ncols, C, T, thr, mass, mass_stride);
   return cudaGetLastError();
 }
