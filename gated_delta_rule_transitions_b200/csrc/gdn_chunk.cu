@@ -89,12 +89,11 @@ __device__ __forceinline__ void wait_ld(uint32_t (&r)[32]) {
 constexpr int kP = kC + 4;                    // row pitch (floats): 16-byte rows
 constexpr int kMat = kC * kP * 4;             // one 64 x 64 float32 matrix
 constexpr int kWyQK = 0;                      // [kb][Q | K][64 rows][128 B]; once they are multiplied:
-constexpr int kWyP = 0;                       //   P, then
-constexpr int kWyL = kMat;                    //   L, then L' (off the diagonal blocks), then G
-constexpr int kWyU = 2 * kMat;                // (I + L)^{-1}
-constexpr int kWySmall = kWyU + kMat;
+constexpr int kWyL = 0;                       //   L, then L' (off the diagonal blocks), then P, then G
+constexpr int kWyU = kMat;                    //   (I + L)^{-1}
+constexpr int kWySmall = 2 * kMat;
 constexpr int kWySmem = kWySmall + kC * 8 + 3 * kC * 4 + 2 * 8 + 32;
-static_assert(2 * kMat >= 4 * kTile, "the tiles fit under P and L");
+static_assert(2 * kMat >= 4 * kTile, "the tiles fit under L and U");
 constexpr uint32_t kIdescWy = tc::idesc_bf16_f32(128, 64, 0, 0);
 constexpr float kProductRange = 40.0f;
 
@@ -150,15 +149,15 @@ __device__ __forceinline__ float exp64(double x) {
   return fmaf(e, (float)(x - (double)h), e);
 }
 
-// One CTA (4 warps) per (chunk slot, head), four per SM.
-__global__ void __launch_bounds__(128, 4)
+// One CTA (4 warps) per (chunk slot, head), five per SM.  Q K^T stays in tensor memory until L'
+// has been used, so that one buffer serves L and P.
+__global__ void __launch_bounds__(128, 5)
     gdn_wy_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK, GdnArgs a,
                   uint8_t* ws) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* sm = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   float* Ls = (float*)(sm + kWyL);
   float* Us = (float*)(sm + kWyU);
-  float* Ps = (float*)(sm + kWyP);
   double* ell = (double*)(sm + kWySmall);
   float* beta_s = (float*)(ell + kC);
   float* gam = beta_s + kC;
@@ -254,11 +253,10 @@ __global__ void __launch_bounds__(128, 4)
     tc::mma_commit(&bars[1]);
   }
   if (ok) ok = tc::bar_all(1, 128, tid == 0 ? tc::mbar_wait(&bars[1], 0, abort_s) : true);
-  if (ok) {
-    tc::tc_fence_after();
+  // rows 0-63 (warps 0, 1): P = tril(Gamma o Q K^T); rows 64-127 (warps 2, 3): L; each when asked
+  auto masked = [&](bool isL) {
     const int t = tid & (kC - 1);
-    const bool isL = tid >= kC;
-    float* row = (isL ? Ls : Ps) + t * kP;
+    float* row = Ls + t * kP;
     const float bt = isL ? beta_s[t] : 1.0f;
     const int last = isL ? t - 1 : t;  // columns up to and with `last`
     const bool product = max(lmax[0], lmax[1]) <= __float_as_uint(kProductRange);
@@ -289,8 +287,9 @@ __global__ void __launch_bounds__(128, 4)
         }
       }
     }
-    tc::tc_fence_before();
-  }
+  };
+  if (ok) tc::tc_fence_after();
+  if (ok && warp >= 2) masked(true);
   __syncthreads();
   // U = (I + L)^{-1} by 16 x 16 blocks: forward substitution on the diagonal blocks, then
   // U_ij = -sum_{k=j}^{i-1} (U_ii L_ik) U_kj, one level i - j after the other
@@ -340,27 +339,36 @@ __global__ void __launch_bounds__(128, 4)
     }
     __syncthreads();
   }
-  // G = P U over L' (no longer needed), blocks (i, j), j <= i, of i - j + 1 products: 5 a warp
-  auto g_block = [&](int i, int j) {
-    float acc[2][4] = {};
-    for (int k = j; k <= i; ++k)
-      block16<2>(acc, Ps + 16 * i * kP + 16 * k, kP, Us + 16 * k * kP + 16 * j, kP, lane);
-    store16(Ls + 16 * i * kP + 16 * j, kP, acc[0], 1.0f, lane);
-    store16(Ls + 16 * i * kP + 16 * j + 8, kP, acc[1], 1.0f, lane);
+  // P over L' (no longer needed)
+  if (ok && warp < 2) masked(false);
+  tc::tc_fence_before();
+  __syncthreads();
+  // G = P U, blocks (i, j), j <= i, of i - j + 1 products: 5 a warp.  G_ij overwrites P_ij, which
+  // a product of another warp may still want: all of them before any is stored
+  float ga[4][2][4] = {};  // this warp's blocks: (3,0) (0,0) | (3,1) (3,2) | (2,0) (2,1) | (1,0) (1,1) (2,2) (3,3)
+  auto g_at = [&](int u, int& i, int& j) {
+    const int code = warp == 0 ? (u == 0 ? 0x30 : 0x00) : warp == 1 ? (u == 0 ? 0x31 : 0x32)
+                   : warp == 2 ? (u == 0 ? 0x20 : 0x21) : (u == 0 ? 0x10 : 0x11 * u);
+    i = code >> 4;
+    j = code & 15;
   };
-  if (warp == 0) {
-    g_block(3, 0);
-    g_block(0, 0);
-  } else if (warp == 1) {
-    g_block(3, 1);
-    g_block(3, 2);
-  } else if (warp == 2) {
-    g_block(2, 0);
-    g_block(2, 1);
-  } else {
-    g_block(1, 0);
-    for (int i = 1; i < 4; ++i) g_block(i, i);
-  }
+  const int blocks = warp == 3 ? 4 : 2;
+#pragma unroll
+  for (int u = 0; u < 4; ++u)
+    if (u < blocks) {
+      int i, j;
+      g_at(u, i, j);
+      for (int k = j; k <= i; ++k) block16<2>(ga[u], Ls + 16 * i * kP + 16 * k, kP, Us + 16 * k * kP + 16 * j, kP, lane);
+    }
+  __syncthreads();
+#pragma unroll
+  for (int u = 0; u < 4; ++u)
+    if (u < blocks) {
+      int i, j;
+      g_at(u, i, j);
+      store16(Ls + 16 * i * kP + 16 * j, kP, ga[u][0], 1.0f, lane);
+      store16(Ls + 16 * i * kP + 16 * j + 8, kP, ga[u][1], 1.0f, lane);
+    }
   __syncthreads();
   // out: the parts of T and G as swizzled tiles, then gamma_t and gamma_C / gamma_t
   uint8_t* out = ws + ((long)slot * a.H + h) * kSlot;
