@@ -14,11 +14,11 @@
 // dim, three products a chunk, each waiting for the one before.
 //
 // Precision.  The state is float32 and stays so: it is held in registers, and what goes into
-// a product (S, R, U, T) goes in as three bf16 numbers, x = x1 + x2 + x3, each the rounding
-// of what the ones before it left: 24 bits, off by at most 2^-27 of x (two would be off by
-// 2^-18, 2.8e-6 in the mean, more than float32 sums are).  K, Q and V are bf16 already.  Left
-// out are the products of parts that are 2^-27 and less.  G, which reaches the bf16 output
-// and nothing else, goes in as two.  Decays are differences of 64-bit running sums.
+// a product (S, R, U, T) goes in as three bf16 numbers, x = x1 + x2 + x3, each the eight bits
+// after the one before: exactly x (two would leave 2^-16 of it out, more than float32 sums
+// do).  K, Q and V are bf16 already.  Left out are the products of parts that are 2^-22 and
+// less.  G, which reaches the bf16 output and nothing else, goes in as two.  Decays are
+// differences of 64-bit running sums.
 #include "common.cuh"
 #include "kernels.cuh"
 #include "tc_common.cuh"
@@ -63,13 +63,19 @@ __device__ __forceinline__ int slot_owner(const int32_t* cu, int n_seq, int slot
 
 __device__ __forceinline__ bool good_bounds(int t0, int t1, int T) { return t0 >= 0 && t1 >= t0 && t1 <= T; }
 
-// x as three bf16 numbers, packed for two neighbours.
-__device__ __forceinline__ void split3(float a, float b, uint32_t& p1, uint32_t& p2, uint32_t& p3) {
-  p1 = tc::pack_bf16x2(a, b);
-  a -= tc::bf16lo(p1);
-  b -= tc::bf16hi(p1);
-  p2 = tc::pack_bf16x2(a, b);
-  p3 = tc::pack_bf16x2(a - tc::bf16lo(p2), b - tc::bf16hi(p2));
+// The two neighbours' next eight bits each: packed, and what is left of x.
+__device__ __forceinline__ uint32_t cut(float2& x) {
+  const uint32_t a = __float_as_uint(x.x), b = __float_as_uint(x.y);
+  x.x -= __uint_as_float(a & 0xFFFF0000u);
+  x.y -= __uint_as_float(b & 0xFFFF0000u);
+  return __byte_perm(a, b, 0x7632);
+}
+// Two neighbours as three bf16 parts by cutting: exactly x, 8 bits each.
+__device__ __forceinline__ void cut3(float a, float b, uint32_t& p1, uint32_t& p2, uint32_t& p3) {
+  float2 x = make_float2(a, b);
+  p1 = cut(x);
+  p2 = cut(x);
+  p3 = __byte_perm(__float_as_uint(x.x), __float_as_uint(x.y), 0x7632);
 }
 
 // Waits for this thread's tensor-memory loads; the registers are operands, so that no use of
@@ -383,9 +389,10 @@ __global__ void __launch_bounds__(128, 5)
         const int cc = 8 * c8 + 2 * u;
         const float2 b2 = *(const float2*)(beta_s + cc);
         const float2 x = *(const float2*)(Us + t * kP + cc), y = *(const float2*)(Ls + t * kP + cc);
-        uint32_t rest;
-        split3(x.x * b2.x, x.y * b2.y, w[0][u], w[2][u], w[4][u]);
-        split3(y.x * b2.x, y.y * b2.y, w[1][u], w[3][u], rest);
+        cut3(x.x * b2.x, x.y * b2.y, w[0][u], w[2][u], w[4][u]);
+        float2 gg = make_float2(y.x * b2.x, y.y * b2.y);
+        w[1][u] = cut(gg);
+        w[3][u] = tc::pack_bf16x2(gg.x, gg.y);
       }
     }
 #pragma unroll
@@ -453,18 +460,6 @@ struct Geo {
   static __device__ __forceinline__ int piece(int p) { return (p * kV & 63) >> 3; }
 };
 
-// x in three bf16 parts by cutting: exactly x (8 bits each), two neighbours packed.
-__device__ __forceinline__ void cut3(float a, float b, uint32_t& p1, uint32_t& p2, uint32_t& p3) {
-  const float2 x = make_float2(a, b);
-  const uint32_t ua = __float_as_uint(a), ub = __float_as_uint(b);
-  p1 = __byte_perm(ua, ub, 0x7632);
-  const float2 r = __fadd2_rn(x, make_float2(-__uint_as_float(ua & 0xFFFF0000u), -__uint_as_float(ub & 0xFFFF0000u)));
-  const uint32_t va = __float_as_uint(r.x), vb = __float_as_uint(r.y);
-  p2 = __byte_perm(va, vb, 0x7632);
-  const float2 z = __fadd2_rn(r, make_float2(-__uint_as_float(va & 0xFFFF0000u), -__uint_as_float(vb & 0xFFFF0000u)));
-  p3 = __byte_perm(__float_as_uint(z.x), __float_as_uint(z.y), 0x7632);
-}
-
 __device__ __forceinline__ void stmatrix4(uint32_t addr, const uint32_t (&r)[4]) {
   asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(r[0]), "r"(r[1]),
                "r"(r[2]), "r"(r[3])
@@ -515,14 +510,11 @@ __device__ __forceinline__ void sum_frag(uint32_t addr, int pitch, float (&x)[8 
 #pragma unroll
   for (int i = 0; i < kT; ++i)
 #pragma unroll
-    for (int e = 0; e < 8; e += 2) {
-      // the smallest first
-      float2 s = make_float2(__uint_as_float(y[kN - 1][i][e]), __uint_as_float(y[kN - 1][i][e + 1]));
+    for (int e = 0; e < 8; ++e) {
+      float s = __uint_as_float(y[kN - 1][i][e]);  // the smallest first
 #pragma unroll
-      for (int p = kN - 2; p >= 0; --p)
-        s = __fadd2_rn(s, make_float2(__uint_as_float(y[p][i][e]), __uint_as_float(y[p][i][e + 1])));
-      x[8 * i + e] = s.x;
-      x[8 * i + e + 1] = s.y;
+      for (int p = kN - 2; p >= 0; --p) s += __uint_as_float(y[p][i][e]);
+      x[8 * i + e] = s;
     }
 }
 
