@@ -9,7 +9,7 @@
 // A CTA of 128 threads holds 16 R rows of one (sequence, head)'s state in registers:
 // 8 threads per R rows, thread g of a group on the columns 32 m + 4 g + u (u < 4), so
 // that state loads and stores are 128-byte segments and the dot products over a row are
-// three shuffles.  Keys, queries, values and decays of 8 or 16 tokens at a time come in by
+// three shuffles.  Keys, queries, values and decays of 8 to 32 tokens at a time come in by
 // cp.async as they are stored (two buffers: the next tokens land while these are worked
 // on); outputs leave through shared memory.
 #include "common.cuh"
@@ -22,9 +22,12 @@ HLA_DEFINE_ERROR_WORD(gdn_recurrent)
 namespace {
 
 constexpr int kThreads = 128;
-// Tokens per staged segment: two segments of the widest rows fit in 48 KiB.
-template <typename Tio, bool kChan>
-constexpr int seg_len() { return sizeof(Tio) == 4 || kChan ? 8 : 16; }
+// Tokens per staged segment: as many as two buffers have room for in 40 KiB, up to 32.
+template <int D, int R, typename Tio, bool kChan, bool kOne>
+constexpr int seg_len() {
+  const int bytes = (2 * D + 16 * R) * (int)sizeof(Tio) + 4 * (kChan ? D : 1) + 4;
+  return kOne ? 1 : 64 * bytes <= 40960 ? 32 : 32 * bytes <= 40960 ? 16 : 8;
+}
 constexpr unsigned kFull = 0xFFFFFFFFu;
 
 __device__ __forceinline__ void cp16(void* dst, const void* src) {
@@ -55,9 +58,8 @@ __device__ __forceinline__ float group_sum(float v) {
   return v;
 }
 
-template <int D, int R, typename Tio, bool kChan>
+template <int D, int R, typename Tio, bool kChan, int kSeg>
 struct Stage {
-  static constexpr int kSeg = seg_len<Tio, kChan>();
   Tio k[kSeg][D];
   Tio q[kSeg][D];
   Tio v[kSeg][16 * R];
@@ -65,14 +67,28 @@ struct Stage {
   float b[kSeg];
 };
 
-template <int D, int R, typename Tio, bool kChan>
+// Row r's dot product over this thread's columns.
+template <int M>
+__device__ __forceinline__ float dot_cols(const float2 (&x)[2 * M], const float2 (&k)[2 * M]) {
+  float2 d0 = make_float2(0.0f, 0.0f), d1 = d0;
+#pragma unroll
+  for (int m = 0; m < M; ++m) {
+    d0 = __ffma2_rn(x[2 * m], k[2 * m], d0);
+    d1 = __ffma2_rn(x[2 * m + 1], k[2 * m + 1], d1);
+  }
+  return (d0.x + d0.y) + (d1.x + d1.y);
+}
+
+// kOne: one token per sequence (the step).  Otherwise token t's output and token t + 1's dot
+// product with its key are reduced together: one chain of three shuffles a token.
+template <int D, int R, typename Tio, bool kChan, bool kOne>
 __global__ void __launch_bounds__(kThreads) gdn_recurrent_kernel(GdnArgs a) {
   constexpr int kRows = 16 * R;
   constexpr int kSplit = D / kRows;   // CTAs per (sequence, head)
   constexpr int M = D / 32;           // 4-column groups per thread
   constexpr int kVec = 16 / (int)sizeof(Tio);
-  constexpr int kSeg = seg_len<Tio, kChan>();
-  __shared__ __align__(16) Stage<D, R, Tio, kChan> st[2];
+  constexpr int kSeg = seg_len<D, R, Tio, kChan, kOne>();
+  __shared__ __align__(16) Stage<D, R, Tio, kChan, kSeg> st[kOne ? 1 : 2];
   __shared__ float os[kSeg][kRows];
   // launched as a programmatic dependent: the next step's blocks may take their places while
   // this grid drains; all that is read comes after the wait for the grid before
@@ -90,7 +106,7 @@ __global__ void __launch_bounds__(kThreads) gdn_recurrent_kernel(GdnArgs a) {
   // the sequence's tokens and its state; what the device arrays cannot mean is refused
   // (nothing is read or written for that sequence)
   int t0 = seq, t1 = seq + 1;
-  if (a.cu != nullptr) {
+  if (!kOne) {
     t0 = a.cu[seq];
     t1 = a.cu[seq + 1];
   }
@@ -158,64 +174,83 @@ __global__ void __launch_bounds__(kThreads) gdn_recurrent_kernel(GdnArgs a) {
     }
 
   int w = 0;
-  for (int s0 = 0; s0 < len; s0 += kSeg, w ^= 1) {
+  for (int s0 = 0; s0 < len; s0 += kSeg, w ^= (kOne ? 0 : 1)) {
     const int ns = min(kSeg, len - s0);
-    if (s0 + kSeg < len) {
+    if (!kOne && s0 + kSeg < len) {
       stage(s0 + kSeg, w ^ 1);
       asm volatile("cp.async.wait_group 1;" ::: "memory");
     } else {
       asm volatile("cp.async.wait_group 0;" ::: "memory");
     }
     __syncthreads();
-    for (int t = 0; t < ns; ++t) {
-      float2 kr[2 * M];
+    // keys (and decays) of the token at hand; p[r] = the decayed row's product with the key
+    float2 kr[2 * M], ar[kChan ? 2 * M : 1];
+    float p_[R];
+    auto load_key = [&](int t, float2 (&k)[2 * M], float2 (&al)[kChan ? 2 * M : 1]) {
 #pragma unroll
-      for (int m = 0; m < M; ++m) ld4(&st[w].k[t][32 * m + 4 * g], kr[2 * m], kr[2 * m + 1]);
-      if (kChan) {
-#pragma unroll
-        for (int m = 0; m < M; ++m) {
-          const float4 al = *(const float4*)&st[w].a[t][32 * m + 4 * g];
-#pragma unroll
-          for (int r = 0; r < R; ++r) {
-            x[r][2 * m] = __fmul2_rn(x[r][2 * m], make_float2(al.x, al.y));
-            x[r][2 * m + 1] = __fmul2_rn(x[r][2 * m + 1], make_float2(al.z, al.w));
-          }
+      for (int m = 0; m < M; ++m) {
+        ld4(&st[w].k[t][32 * m + 4 * g], k[2 * m], k[2 * m + 1]);
+        if constexpr (kChan) {
+          const float4 f = *(const float4*)&st[w].a[t][32 * m + 4 * g];
+          al[2 * m] = make_float2(f.x, f.y);
+          al[2 * m + 1] = make_float2(f.z, f.w);
         }
       }
+    };
+    auto key_part = [&](const float2 (&xr)[2 * M], const float2 (&k)[2 * M], const float2 (&al)[kChan ? 2 * M : 1]) {
+      if constexpr (kChan) {
+        float2 ka[2 * M];
+#pragma unroll
+        for (int j = 0; j < 2 * M; ++j) ka[j] = __fmul2_rn(k[j], al[j]);
+        return dot_cols<M>(xr, ka);
+      } else {
+        return dot_cols<M>(xr, k);
+      }
+    };
+    load_key(0, kr, ar);
+#pragma unroll
+    for (int r = 0; r < R; ++r) p_[r] = group_sum(key_part(x[r], kr, ar));
+    for (int t = 0; t < ns; ++t) {
+      float2 qr[2 * M], kn[2 * M], an[kChan ? 2 * M : 1];
+#pragma unroll
+      for (int m = 0; m < M; ++m) ld4(&st[w].q[t][32 * m + 4 * g], qr[2 * m], qr[2 * m + 1]);
+      if (!kOne) load_key(min(t + 1, ns - 1), kn, an);  // (the last token's is not used)
       const float at = kChan ? 1.0f : st[w].a[t][0];
       const float bt = st[w].b[t];
-      float u[R];
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        float2 d0 = make_float2(0.0f, 0.0f), d1 = d0;
+        const float u = bt * (ldf(&st[w].v[t][p * R + r]) - at * p_[r]);
+        const float2 u2 = make_float2(u, u), a2 = make_float2(at, at);
 #pragma unroll
-        for (int m = 0; m < M; ++m) {
-          d0 = __ffma2_rn(x[r][2 * m], kr[2 * m], d0);
-          d1 = __ffma2_rn(x[r][2 * m + 1], kr[2 * m + 1], d1);
+        for (int j = 0; j < 2 * M; ++j) {
+          if constexpr (kChan)
+            x[r][j] = __ffma2_rn(u2, kr[j], __fmul2_rn(ar[j], x[r][j]));
+          else
+            x[r][j] = __ffma2_rn(u2, kr[j], __fmul2_rn(a2, x[r][j]));
         }
-        u[r] = (d0.x + d0.y) + (d1.x + d1.y);
+      }
+      float y[R];
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        y[r] = dot_cols<M>(x[r], qr);
+        if (!kOne) p_[r] = key_part(x[r], kn, an);
       }
 #pragma unroll
-      for (int r = 0; r < R; ++r) u[r] = bt * (ldf(&st[w].v[t][p * R + r]) - at * group_sum(u[r]));
+      for (int o = 1; o < 8; o <<= 1)
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        const float2 ur = make_float2(u[r], u[r]), ar = make_float2(at, at);
-#pragma unroll
-        for (int j = 0; j < 2 * M; ++j)
-          x[r][j] = kChan ? __ffma2_rn(ur, kr[j], x[r][j]) : __ffma2_rn(ur, kr[j], __fmul2_rn(ar, x[r][j]));
-      }
-#pragma unroll
-      for (int m = 0; m < M; ++m) ld4(&st[w].q[t][32 * m + 4 * g], kr[2 * m], kr[2 * m + 1]);
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        float2 d0 = make_float2(0.0f, 0.0f), d1 = d0;
-#pragma unroll
-        for (int m = 0; m < M; ++m) {
-          d0 = __ffma2_rn(x[r][2 * m], kr[2 * m], d0);
-          d1 = __ffma2_rn(x[r][2 * m + 1], kr[2 * m + 1], d1);
+        for (int r = 0; r < R; ++r) {
+          y[r] += __shfl_xor_sync(kFull, y[r], o);
+          if (!kOne) p_[r] += __shfl_xor_sync(kFull, p_[r], o);
         }
-        const float y = group_sum((d0.x + d0.y) + (d1.x + d1.y));
-        if (g == r) os[t][p * R + r] = y;
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+        if (g == r) os[t][p * R + r] = y[r];
+      if (!kOne) {
+#pragma unroll
+        for (int j = 0; j < 2 * M; ++j) {
+          kr[j] = kn[j];
+          if constexpr (kChan) ar[j] = an[j];
+        }
       }
     }
     __syncthreads();  // the segment's outputs are in shared memory and its buffer is free
@@ -246,16 +281,23 @@ cudaError_t launch_r(const GdnArgs& a, cudaStream_t s) {
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return a.alpha_vec ? cudaLaunchKernelEx(&cfg, gdn_recurrent_kernel<D, R, Tio, true>, a)
-                     : cudaLaunchKernelEx(&cfg, gdn_recurrent_kernel<D, R, Tio, false>, a);
+  if (a.cu == nullptr)
+    return a.alpha_vec ? cudaLaunchKernelEx(&cfg, gdn_recurrent_kernel<D, R, Tio, true, true>, a)
+                       : cudaLaunchKernelEx(&cfg, gdn_recurrent_kernel<D, R, Tio, false, true>, a);
+  return a.alpha_vec ? cudaLaunchKernelEx(&cfg, gdn_recurrent_kernel<D, R, Tio, true, false>, a)
+                     : cudaLaunchKernelEx(&cfg, gdn_recurrent_kernel<D, R, Tio, false, false>, a);
 }
 
 template <int D, typename Tio>
 cudaError_t launch_d(const GdnArgs& a, cudaStream_t s) {
-  // few (sequence, head) pairs: one row per group, so that four times as many CTAs share
-  // the work and each token's chain is shorter
-  const long pairs = (long)a.n_seq * a.H;
-  return pairs * (D / 64) >= 2L * num_sms() ? launch_r<D, 4, Tio>(a, s) : launch_r<D, 1, Tio>(a, s);
+  // Rows per group of threads: one while that leaves each SM a few CTAs at most (a token's
+  // chain is shortest), else two (a shared-memory read then feeds two rows; four take so many
+  // registers that the step slows down: 64 x 16 heads of 128, 24.0 us with two, 26 with four).
+  // Measured, 16 heads of 128, bf16: 256 tokens of one sequence 49 us with one row, 78 with
+  // two; of four sequences 152 and 95.  The step of 8 x 8 heads: 2.5 and 2.7; of 16 x 8: 4.1
+  // and 3.5.
+  const long ctas = (long)a.n_seq * a.H * (D / 16);
+  return ctas <= (a.cu == nullptr ? 4L : 2L) * num_sms() ? launch_r<D, 1, Tio>(a, s) : launch_r<D, 2, Tio>(a, s);
 }
 
 }  // namespace

@@ -753,9 +753,9 @@ static hla_status check_gdn(const gdn_config* c) {
 }
 
 // Chunks of 64 tokens on the tensor cores, or token by token: by the mean length, which is
-// what the host knows of the lengths.
+// what the host knows of the lengths.  The two meet between 36 and 56 tokens a sequence.
 static bool gdn_by_chunks(const gdn_config* c, int32_t T) {
-  return c->dtype == HLA_BF16 && c->dk == 128 && c->decay_mode == HLA_DECAY_SCALAR && T >= 32 * (int64_t)c->n_seq;
+  return c->dtype == HLA_BF16 && c->dk == 128 && c->decay_mode == HLA_DECAY_SCALAR && T >= 40 * (int64_t)c->n_seq;
 }
 
 size_t gdn_workspace_bytes(const gdn_config* cfg, int32_t T) {
