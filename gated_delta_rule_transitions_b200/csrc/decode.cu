@@ -143,37 +143,14 @@ __global__ void __launch_bounds__(128) decode_main_kernel(DecodeArgs a) {
   for (int p = cnt - 1; p >= 0; --p) {
     const int j = act_idx[p];
     const float g = act_g[p];
+    const Tio* A = (const Tio*)a.A + ((long)bh * a.max_chunks + j) * (long)D * D + (long)tid * D;
+    const Tio* Bm = (const Tio*)a.Bm + ((long)bh * a.max_chunks + j) * (long)D * D + (long)tid * D;
     float ax = 0.0f, bx = 0.0f;
-    if (a.format == HLA_CACHE_INT8) {
-      // A_j x = a_j x + sA (QA x), B_j x = sB (QB x): codes of row tid
-      const long slot = (long)bh * a.max_chunks + j;
-      const char4* A = (const char4*)((const int8_t*)a.A + slot * D * D + (long)tid * D);
-      const char4* Bm = (const char4*)((const int8_t*)a.Bm + slot * D * D + (long)tid * D);
-#pragma unroll 4
-      for (int c = 0; c < D / 4; ++c) {
-        const char4 qa = A[c], qb = Bm[c];
-        const float* xc = &xs[cur][4 * c];
-        ax = fmaf((float)qa.x, xc[0], ax);
-        ax = fmaf((float)qa.y, xc[1], ax);
-        ax = fmaf((float)qa.z, xc[2], ax);
-        ax = fmaf((float)qa.w, xc[3], ax);
-        bx = fmaf((float)qb.x, xc[0], bx);
-        bx = fmaf((float)qb.y, xc[1], bx);
-        bx = fmaf((float)qb.z, xc[2], bx);
-        bx = fmaf((float)qb.w, xc[3], bx);
-      }
-      const float4 sc = *(const float4*)(a.df + slot * 4);
-      ax = fmaf(sc.x, xs[cur][tid], sc.y * ax);
-      bx *= sc.z;
-    } else {
-      const Tio* A = (const Tio*)a.A + ((long)bh * a.max_chunks + j) * (long)D * D + (long)tid * D;
-      const Tio* Bm = (const Tio*)a.Bm + ((long)bh * a.max_chunks + j) * (long)D * D + (long)tid * D;
 #pragma unroll 8
-      for (int c = 0; c < D; ++c) {
-        const float xc = xs[cur][c];
-        ax = fmaf(ldf(A + c), xc, ax);
-        bx = fmaf(ldf(Bm + c), xc, bx);
-      }
+    for (int c = 0; c < D; ++c) {
+      const float xc = xs[cur][c];
+      ax = fmaf(ldf(A + c), xc, ax);
+      bx = fmaf(ldf(Bm + c), xc, bx);
     }
     y = fmaf(g, bx, y);
     xs[cur ^ 1][tid] = (1.0f - g) * xs[cur][tid] + g * ax;
@@ -413,6 +390,7 @@ static cudaError_t launch_close(const DecodeArgs& a, cudaStream_t s) {
 
 cudaError_t launch_decode_main(const DecodeArgs& a, cudaStream_t s) {
   if (a.format == HLA_CACHE_FACTORED) return launch_decode_stream_factored(a, s);
+  if (a.format == HLA_CACHE_INT8) return launch_decode8(a, s);
   if (a.d == 128 && a.dtype == HLA_BF16) return launch_decode_stream(a, s);
   if (a.d == 128) return a.dtype == HLA_BF16 ? launch_main<128, __nv_bfloat16>(a, s) : launch_main<128, float>(a, s);
   return a.dtype == HLA_BF16 ? launch_main<64, __nv_bfloat16>(a, s) : launch_main<64, float>(a, s);

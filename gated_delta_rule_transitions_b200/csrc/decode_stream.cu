@@ -624,269 +624,6 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (tid == 0 && *abort_s) report_device_error(kErrMbarTimeout);
 }
 
-// ---------------------------------------------------------------------------------
-// 8-bit cache (A_j ~ a_j I + sA QA, B_j ~ sB QB, int8 codes): the chain's two products
-// in whole numbers, on the tensor cores.  The running x is held in float32; before each
-// chunk it is written as a fixed-point number of 24 bits relative to its largest entry,
-//   x_c = 2^(e - 22) N_c,  |N_c| <= 2^22,  N_c = d0 + 2^8 d1 + 2^16 d2  (signed bytes),
-// and the three digit vectors are three columns of one right factor, so that QA x and QB x
-// are exact products of bytes (warp-level 16 x 8 x 32, 32-bit sums: at most 128 x 127 x 128
-// < 2^21).  The only error beside float32's own is the fixed point's half unit, 2^-23 of
-// the largest entry.  The matrices go from shared memory to the tensor cores as they lie,
-// 16 ldmatrix a warp and chunk; nothing is converted.
-//
-// A unit of the ring is one chunk: 16 KiB of QA, 16 KiB of QB (128 rows of 128 bytes, one
-// 128-byte-swizzled box each) and its four scales.  Warp w has rows 32 w .. + 31 of both;
-// lane l owns row 32 w + l / 4 + 8 (l % 4) of the vectors.
-constexpr int kU8Tile = kD * kD;                    // 16 KiB of codes
-constexpr int kU8Unit = 2 * kU8Tile;                // 32 KiB
-constexpr int kU8Units = 3;
-constexpr uint32_t kU8Tx = kU8Unit + 16;
-constexpr int kDigits = kD + 32;                    // pitch of a digit vector: three on 24 banks
-constexpr int kU8Vec = 3 * kDigits;                 // digits of one x
-
-// x (this thread's row) as digits; returns the unit 2^(e - 22).  A zero x has digits and unit
-// zero; one with an infinity or a NaN has unit NaN.  Contains one barrier.
-__device__ __forceinline__ float write_digits(float x, int row, uint32_t* mx, uint8_t* xd) {
-  const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(x) & 0x7FFFFFFFu);
-  if ((threadIdx.x & 31) == 0) mx[threadIdx.x >> 5] = m;
-  tc::bar_sync(1, kCompute);
-  const uint4 m4 = *(const uint4*)mx;
-  const uint32_t big = max(max(m4.x, m4.y), max(m4.z, m4.w));
-  // |x| < 2^e; below 2^-100 the fixed point stays where it is
-  const int e = max((int)(big >> 23) - 126, -100);
-  const float up = __uint_as_float((uint32_t)(127 + 22 - e) << 23);
-  const int n = __float2int_rn(x * up);
-  const int d0 = (int)(int8_t)n;
-  const int n1 = (n - d0) >> 8;
-  const int d1 = (int)(int8_t)n1;
-  xd[row] = (uint8_t)d0;
-  xd[kDigits + row] = (uint8_t)d1;
-  xd[2 * kDigits + row] = (uint8_t)((n1 - d1) >> 8);
-  if (big >= 0x7F800000u) return __uint_as_float(0x7FC00000u);
-  return __uint_as_float((uint32_t)(127 - 22 + e) << 23);
-}
-
-__device__ __forceinline__ void mma_s8(int (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%0, %1, %2, %3};"
-      : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-__device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-
-// The open chunk right to left by one warp (scalar decay): x = A_p q and y = B_p q into
-// shared memory.  Lane l has the 16 channels 16 (l % 8) .. of x (four copies, so that a dot
-// product is three shuffles) and the channels 4 l .. of y; the rows of four tokens come in
-// while the four before are worked on.
-__device__ __forceinline__ void sweep_warp(const DecodeArgs& a, int bh, int m, float* xs, float* ys) {
-  const int lane = threadIdx.x & 31;
-  const int g = lane & 7;
-  const __nv_bfloat16* bk = (const __nv_bfloat16*)a.buf_k + (long)bh * a.C * kD + 16 * g;
-  const __nv_bfloat16* bv = (const __nv_bfloat16*)a.buf_v + (long)bh * a.C * kD + 4 * lane;
-  const float* ba = a.buf_alpha + (long)bh * a.C;
-  const float* bb = a.buf_beta + (long)bh * a.C;
-  const uint4* q4 = (const uint4*)((const __nv_bfloat16*)a.q + (long)bh * kD + 16 * g);
-  float2 x[8], y[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-  {
-    const uint4 u = q4[0], w = q4[1];
-    const uint32_t qq[8] = {u.x, u.y, u.z, u.w, w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = tc::bf16x2_to_float2(qq[e]);
-  }
-  uint4 k0[4], k1[4];
-  uint2 v[4];
-  float al[4], be[4];
-  auto load = [&](int t, int i) {  // token t (nothing before the first)
-    if (t < 0) return;
-    k0[i] = *(const uint4*)(bk + (long)t * kD);
-    k1[i] = *(const uint4*)(bk + (long)t * kD + 8);
-    v[i] = *(const uint2*)(bv + (long)t * kD);
-    al[i] = ba[t];
-    be[i] = bb[t];
-  };
-#pragma unroll
-  for (int i = 0; i < 4; ++i) load(m - i, i);
-  for (int t0 = m; t0 >= 0; t0 -= 4) {
-    uint4 c0[4], c1[4];
-    uint2 cv[4];
-    float ca[4], cb[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      c0[i] = k0[i];
-      c1[i] = k1[i];
-      cv[i] = v[i];
-      ca[i] = al[i];
-      cb[i] = be[i];
-      load(t0 - 4 - i, i);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (t0 - i < 0) break;
-      const uint32_t kk[8] = {c0[i].x, c0[i].y, c0[i].z, c0[i].w, c1[i].x, c1[i].y, c1[i].z, c1[i].w};
-      float2 d0 = make_float2(0.0f, 0.0f), d1 = d0;
-#pragma unroll
-      for (int e = 0; e < 8; e += 2) {
-        d0 = tc::fma2(x[e], tc::bf16x2_to_float2(kk[e]), d0);
-        d1 = tc::fma2(x[e + 1], tc::bf16x2_to_float2(kk[e + 1]), d1);
-      }
-      float c = (d0.x + d0.y) + (d1.x + d1.y);
-      c += __shfl_xor_sync(0xFFFFFFFFu, c, 1);
-      c += __shfl_xor_sync(0xFFFFFFFFu, c, 2);
-      c += __shfl_xor_sync(0xFFFFFFFFu, c, 4);
-      c *= cb[i];
-      const float2 c2 = make_float2(c, c), nc = make_float2(-ca[i] * c, -ca[i] * c), a2 = make_float2(ca[i], ca[i]);
-      y[0] = tc::fma2(c2, tc::bf16x2_to_float2(cv[i].x), y[0]);
-      y[1] = tc::fma2(c2, tc::bf16x2_to_float2(cv[i].y), y[1]);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = tc::fma2(nc, tc::bf16x2_to_float2(kk[e]), tc::mul2(a2, x[e]));
-    }
-  }
-  if (lane < 8) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      *(float4*)(xs + 16 * g + 4 * e) = make_float4(x[2 * e].x, x[2 * e].y, x[2 * e + 1].x, x[2 * e + 1].y);
-  }
-  *(float4*)(ys + 4 * lane) = make_float4(y[0].x, y[0].y, y[1].x, y[1].y);
-}
-
-__global__ void __launch_bounds__(kThreads, 2)
-    decode_stream8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                          DecodeArgs a) {
-  // the gate kernel's programmatic dependent, like decode_stream_kernel
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  extern __shared__ __align__(1024) uint8_t smem_raw[];
-  uint8_t* ring = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-  float4* sc_s = (float4*)(ring + kU8Units * kU8Unit);  // [kU8Units] a, sA, sB, 0
-  uint8_t* xd = (uint8_t*)(sc_s + kU8Units);             // [2][3][kDigits] digits of x
-  uint32_t* mx = (uint32_t*)(xd + 2 * kU8Vec);           // [2][4]
-  uint64_t* full = (uint64_t*)(mx + 8);
-  uint64_t* empty = full + kU8Units;
-  float* xs = (float*)(empty + kU8Units);    // [kD] x after the open chunk
-  float* ys = xs + kD;                       // [kD] y of the open chunk
-  float* red = ys + kD;                      // [4]
-  int* wcount = (int*)(red + 4);             // [4]
-  volatile int* abort_s = (volatile int*)(wcount + 4);
-
-  const int bh = blockIdx.x;
-  const int b = bh / a.H;
-  const int tid = threadIdx.x;
-  const int n = a.n_chunks[b];
-  const int m = a.m_partial[b];
-  const int32_t* act_idx = a.act_idx + (long)bh * a.max_chunks;
-  const float* act_g = a.act_g + (long)bh * a.max_chunks;
-  const int cnt = a.act_cnt[bh];
-
-  if (tid == 0) {
-    for (int u = 0; u < kU8Units; ++u) {
-      tc::mbar_init(&full[u], 1);
-      tc::mbar_init(&empty[u], 1);
-    }
-    *abort_s = 0;
-    tc::mbar_fence_init();
-    tc::fence_async_smem();
-  }
-  __syncthreads();
-
-  if (tid >= kCompute) {
-    // ---------------- TMA producer (warp 4, lane 0): one unit per active chunk ----------------
-    if (tid == kCompute && cnt > 0) {
-      tc::tma_prefetch_desc(&tmA);
-      tc::tma_prefetch_desc(&tmB);
-      int u = 0;
-      for (int p = cnt - 1; p >= 0; --p, ++u) {
-        const int st = u % kU8Units;
-        const long slot = (long)bh * a.max_chunks + act_idx[p];
-        if (u >= kU8Units && !tc::mbar_wait(&empty[st], ((u / kU8Units) - 1) & 1, abort_s)) break;
-        const int row = (int)(slot * kD);
-        tc::mbar_arrive_expect_tx(&full[st], kU8Tx);
-        uint8_t* dst = ring + st * kU8Unit;
-        tc::tma_load_2d(dst, &tmA, 0, row, &full[st]);
-        tc::tma_load_2d(dst + kU8Tile, &tmB, 0, row, &full[st]);
-        tc::bulk_load_1d(sc_s + st, a.df + slot * 4, 16, &full[st]);
-      }
-      if (*abort_s)
-        for (int t = max(0, u - kU8Units); t < u; ++t)
-          tc::mbar_wait(&full[t % kU8Units], (t / kU8Units) & 1, nullptr, 200000000ull);
-    }
-    __syncwarp();
-  } else {
-    // ---------------- compute (warps 0-3) ----------------
-    const int warp = tid >> 5, lane = tid & 31;
-    const int row = 32 * warp + (lane >> 2) + 8 * (lane & 3);  // this thread's row of x and y
-    if (a.alpha_vec) {
-      float x, y0;
-      decode_prologue(a, bh, n, m, xs, red, wcount, x, y0, false, false, true, false);  // the sweep only
-      xs[tid] = x;
-      ys[tid] = y0;
-    } else if (warp == 0) {
-      sweep_warp(a, bh, m, xs, ys);
-    }
-    tc::bar_sync(1, kCompute);
-    float x = xs[row], y = 0.0f;
-    float g = cnt > 0 ? act_g[cnt - 1] : 0.0f;
-    float unit = write_digits(x, row, mx, xd);
-    // ldmatrix addresses: lane l gives row l % 16 of a 16-row tile, 16-byte piece l / 16 of a
-    // 32-byte step; the swizzle of a row is l % 8 in every tile
-    const uint32_t mrow = tc::smem_u32(ring) + (32 * warp + (lane & 15)) * 128;
-    const int mpiece = lane >> 4, mswz = lane & 7;
-    const int dcol = lane >> 2;  // digit vector of this lane's part of the right factor
-    for (int p = cnt - 1, u = 0; p >= 0; --p, ++u) {
-      const int st = u % kU8Units;
-      const uint8_t* xc = xd + (u & 1) * kU8Vec + dcol * kDigits + 4 * (lane & 3);
-      const float g_next = p > 0 ? act_g[p - 1] : 0.0f;
-      if (!tc::bar_all(1, kCompute, tc::mbar_wait(&full[st], (u / kU8Units) & 1, abort_s))) break;
-      uint32_t xb[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) xb[e] = dcol < 3 ? *(const uint32_t*)(xc + 16 * e) : 0u;
-      int acc[4][4] = {};  // QA rows 0-15, 16-31, QB rows 0-15, 16-31 of this warp's
-#pragma unroll
-      for (int ks = 0; ks < 4; ++ks) {
-        const uint32_t at = mrow + st * kU8Unit + (((2 * ks + mpiece) ^ mswz) << 4);
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          uint32_t f[4];
-          ldmatrix4(at + (t >> 1) * kU8Tile + (t & 1) * 2048, f);
-          mma_s8(acc[t], f, xb[2 * ks], xb[2 * ks + 1]);
-        }
-      }
-      // columns 0, 1 of a row are in lane 4 (row % 8), column 2 in the lane after it: join the
-      // digits there, then hand row 8 j + l / 4 to the lane with l % 4 = j
-      float sa = 0.0f, sb = 0.0f;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int t = j >> 1, c = 2 * (j & 1);
-        const int a2 = __shfl_xor_sync(0xFFFFFFFFu, acc[t][c], 1), b2 = __shfl_xor_sync(0xFFFFFFFFu, acc[2 + t][c], 1);
-        float va = fmaf((float)a2, 65536.0f, fmaf((float)acc[t][c + 1], 256.0f, (float)acc[t][c]));
-        float vb = fmaf((float)b2, 65536.0f, fmaf((float)acc[2 + t][c + 1], 256.0f, (float)acc[2 + t][c]));
-        va = __shfl_sync(0xFFFFFFFFu, va, lane & 28);
-        vb = __shfl_sync(0xFFFFFFFFu, vb, lane & 28);
-        if ((lane & 3) == j) {
-          sa = va;
-          sb = vb;
-        }
-      }
-      const float4 sc = sc_s[st];
-      y = fmaf(g * sc.z, sb * unit, y);
-      x = fmaf(1.0f - g, x, g * fmaf(sc.x, x, sc.y * (sa * unit)));
-      g = g_next;
-      // the digits of the new x; the barrier inside also says that this unit has been read
-      unit = write_digits(x, row, mx + 4 * ((u + 1) & 1), xd + ((u + 1) & 1) * kU8Vec);
-      if (tid == 0) tc::mbar_arrive(&empty[st]);
-    }
-    stf((__nv_bfloat16*)a.o + (long)bh * kD + row, y + ys[row]);
-  }
-  __syncthreads();
-  if (tid == 0 && *abort_s) report_device_error(kErrMbarTimeout);
-}
-
 }  // namespace
 
 cudaError_t launch_decode_stream_factored(const DecodeArgs& a, cudaStream_t s) {
@@ -903,37 +640,32 @@ cudaError_t launch_decode_stream_factored(const DecodeArgs& a, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-cudaError_t launch_decode_stream(const DecodeArgs& a, cudaStream_t s) {
-  const long rows = (long)a.B * a.H * a.max_chunks * kD;
-  const bool int8 = a.format == HLA_CACHE_INT8;
-  CUtensorMap tmA, tmB;
-  cudaError_t e;
-  if (int8) {  // a row of 128 codes as 64 two-byte elements
-    if (rows >= (1L << 31)) return cudaErrorNotSupported;  // tile coordinates are 32-bit
-    e = make_tmap_2d(&tmA, a.A, kD / 2, rows, kD, kD / 2, kD);
-    if (e == cudaSuccess) e = make_tmap_2d(&tmB, a.Bm, kD / 2, rows, kD, kD / 2, kD);
-  } else {
-    e = make_tmap_rows128(&tmA, a.A, rows);
-    if (e == cudaSuccess) e = make_tmap_rows128(&tmB, a.Bm, rows);
-  }
-  if (e != cudaSuccess) return e;
+cudaError_t launch_decode_gates(const DecodeArgs& a, cudaStream_t s) {
   // key pools (one per chunk; with window representatives the gates read them directly)
   CUtensorMap tmR;
   std::memset(&tmR, 0, sizeof(tmR));
   if (a.mode == HLA_GATES_ROUTED && a.win == 0) {
-    e = make_tmap_pools(&tmR, a.rk, (long)a.B * a.H * a.max_chunks, kPoolRows);
+    const cudaError_t e = make_tmap_pools(&tmR, a.rk, (long)a.B * a.H * a.max_chunks, kPoolRows);
     if (e != cudaSuccess) return e;
   }
   const size_t gsmem = 1024 + kGPieces * kUnit + 2 * kGPieces * 8 + (kD + 16) * 4;
-  e = cudaFuncSetAttribute(decode_gates_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)gsmem);
+  const cudaError_t e = cudaFuncSetAttribute(decode_gates_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)gsmem);
   if (e != cudaSuccess) return e;
   decode_gates_kernel<<<a.B * a.H, kThreads, gsmem, s>>>(tmR, a);
-  e = cudaGetLastError();
+  return cudaGetLastError();
+}
+
+cudaError_t launch_decode_stream(const DecodeArgs& a, cudaStream_t s) {
+  const long rows = (long)a.B * a.H * a.max_chunks * kD;
+  CUtensorMap tmA, tmB;
+  cudaError_t e = make_tmap_rows128(&tmA, a.A, rows);
   if (e != cudaSuccess) return e;
-  const size_t smem = int8 ? 1024 + kU8Units * (kU8Unit + 16) + 2 * kU8Vec + 32 + 2 * kU8Units * 8 + (2 * kD + 16) * 4
-                           : 1024 + kUnits * kUnit + 2 * kUnits * 8 + (4 * kD + 16) * 4;
-  auto* kern = int8 ? decode_stream8_kernel : decode_stream_kernel;
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  e = make_tmap_rows128(&tmB, a.Bm, rows);
+  if (e != cudaSuccess) return e;
+  e = launch_decode_gates(a, s);
+  if (e != cudaSuccess) return e;
+  const size_t smem = 1024 + kUnits * kUnit + 2 * kUnits * 8 + (4 * kD + 16) * 4;
+  e = cudaFuncSetAttribute(decode_stream_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   // programmatic dependent launch: the stream CTAs are scheduled while the gate grid
   // drains and wait (griddepcontrol.wait) for it to complete
@@ -947,7 +679,7 @@ cudaError_t launch_decode_stream(const DecodeArgs& a, cudaStream_t s) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, kern, tmA, tmB, a);
+  e = cudaLaunchKernelEx(&cfg, decode_stream_kernel, tmA, tmB, a);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }

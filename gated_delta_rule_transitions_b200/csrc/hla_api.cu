@@ -1333,6 +1333,8 @@ hla_status hla_device_status(int32_t clear, uint32_t* code_out) {
   word |= w;
   HLA_CUDA(hla::read_error_word_chan_prep(&w, clear != 0), "hla_device_status read");
   word |= w;
+  HLA_CUDA(hla::read_error_word_decode8(&w, clear != 0), "hla_device_status read");
+  word |= w;
   HLA_CUDA(hla::read_error_word_gdn_recurrent(&w, clear != 0), "hla_device_status read");
   word |= w;
   HLA_CUDA(hla::read_error_word_gdn_chunk(&w, clear != 0), "hla_device_status read");

@@ -263,6 +263,9 @@ cudaError_t read_error_word_decode(unsigned int* out, bool clear);
 cudaError_t read_error_word_compose_tc(unsigned int* out, bool clear);
 cudaError_t launch_compose_tc(const ComposeArgs& a, bool scan, cudaStream_t s);
 cudaError_t launch_decode_stream(const DecodeArgs& a, cudaStream_t s);
+cudaError_t launch_decode_gates(const DecodeArgs& a, cudaStream_t s);
+cudaError_t launch_decode8(const DecodeArgs& a, cudaStream_t s);
+cudaError_t read_error_word_decode8(unsigned int* out, bool clear);
 cudaError_t launch_transitions_tc(const TransArgs& t, cudaStream_t s, const ChanOperands* chan = nullptr);
 cudaError_t launch_factor_fill(const FactorFillArgs& f, cudaStream_t s);
 cudaError_t launch_decode_stream_factored(const DecodeArgs& a, cudaStream_t s);
