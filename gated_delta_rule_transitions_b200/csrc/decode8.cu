@@ -25,8 +25,8 @@
 // box each) and its four scales.  Warp w has rows 32 w .. + 31 of both; lane l owns row
 // 32 w + l / 4 + 8 (l % 4) of the vectors.
 //
-// decode_rows8_kernel (float32, d = 64): one kernel for all steps, dp4a on codes that a lane
-// loads 16 at a time straight from global memory, the next chunks' while these are worked on.
+// decode_rows8_kernel (float32, d = 64): one kernel for all steps, the same products on codes
+// that all threads bring in by cp.async, a ring of chunks ahead.
 #include "common.cuh"
 #include "kernels.cuh"
 #include "routing_recipe.cuh"
@@ -328,15 +328,32 @@ __global__ void __launch_bounds__(kThreads, 2)
 // ---- float32, or d = 64 ------------------------------------------------------------------
 //
 // One CTA of 4 warps per (sequence, head).  Warp 0 sweeps the open chunk while the other three
-// pool the route queries and gate the closed chunks; then the chain.  A row of codes is D / 16
-// lanes of 16 bytes; warp w has the rows D / 4 w .. of both matrices.
+// pool the route queries and gate the closed chunks; then the chain.  Warp w has the rows
+// D / 4 w .. of both matrices; of d = 64 a lane's row of the vectors is its neighbour's too.
+template <int D>
+constexpr int rows8_stages() { return D == 64 ? 6 : 3; }
+
+// Byte of 16-byte piece `piece` of row r of a matrix in shared memory: pieces turned within
+// 128 bytes, so that eight rows' pieces lie in eight bank groups.
+template <int D>
+__device__ __forceinline__ int code_at(int r, int piece) {
+  return r * D + ((D == 128 ? piece ^ (r & 7) : piece ^ ((r >> 1) & 3)) << 4);
+}
+
+__device__ __forceinline__ void cp16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(tc::smem_u32(dst)), "l"(src) : "memory");
+}
+
 template <int D, typename Tio>
 __global__ void __launch_bounds__(kCompute) decode_rows8_kernel(DecodeArgs a) {
-  constexpr int kLanes = D / 16;               // lanes per row
-  constexpr int kRowsAt = 32 / kLanes;         // rows per load
-  constexpr int kLoads = D / 4 / kRowsAt;      // loads per warp and matrix: 2 (d = 64), 8
-  constexpr int kAhead = D == 64 ? 4 : 1;      // chunks on their way
+  constexpr int kTiles = D / 64;               // 16-row tiles per warp and matrix
+  constexpr int kMat = D * D;                  // bytes of one matrix
+  constexpr int kPieces = D / 16;              // 16-byte pieces of a row
   constexpr int kGate = 96;                    // threads that pool and gate
+  constexpr int kStages = rows8_stages<D>();
+  extern __shared__ __align__(128) uint8_t ring[];  // [kStages][QA | QB]
+  __shared__ __align__(16) float4 sc_s[kStages];
+  __shared__ float g_s[kStages];
   __shared__ __align__(16) float xs[D], ys[D], rq[D];
   __shared__ __align__(16) uint8_t xd[2 * kU8Vec];
   __shared__ __align__(16) uint32_t mx[8];
@@ -440,109 +457,95 @@ __global__ void __launch_bounds__(kCompute) decode_rows8_kernel(DecodeArgs a) {
     if (t96 == 0) cnt_s = cnt;
   }
   __syncthreads();
-  // the chain.  Of each row this lane has the 16 codes from 16 (lane % kLanes); load i of a
-  // warp covers its rows kRowsAt i .. + kRowsAt - 1.  After the sums over a row's lanes this
-  // lane owns row `row` of the vectors (d = 64: with its neighbour).
+  // the chain
   const int cnt = cnt_s;
-  const int q = lane % kLanes, gr = lane / kLanes;
-  const int mine = kLoads == kLanes ? q : q >> 1;
-  const int row = D / 4 * warp + kRowsAt * mine + gr;
-  const int8_t* A = (const int8_t*)a.A + (long)bh * a.max_chunks * D * D + (long)(D / 4 * warp + gr) * D + 16 * q;
-  const int8_t* Bm = (const int8_t*)a.Bm + (long)bh * a.max_chunks * D * D + (long)(D / 4 * warp + gr) * D + 16 * q;
-  struct Chunk {
-    int4 a[kLoads], b[kLoads];
-    float4 sc;
-    float g;
-  };
-  auto load = [&](int p, Chunk& ck) {
-    if (p < 0) return;
-    const int j = act_idx[p];
-    ck.g = act_g[p];
-    ck.sc = *(const float4*)(a.df + ((long)bh * a.max_chunks + j) * 4);
+  const int own = kTiles == 2 ? lane & 3 : lane & 1;  // 8-row block of this lane's row
+  const int row = D / 4 * warp + (lane >> 2) + 8 * own;
+  const uint8_t* A = (const uint8_t*)a.A + (long)bh * a.max_chunks * kMat;
+  const uint8_t* Bm = (const uint8_t*)a.Bm + (long)bh * a.max_chunks * kMat;
+  int j_next = cnt > 0 ? act_idx[cnt - 1] : 0;  // list entries come a round before their chunk
+  auto issue = [&](int p, int st) {
+    if (p >= 0) {
+      const int j = j_next;
+      if (p > 0) j_next = act_idx[p - 1];
+      uint8_t* dst = ring + st * 2 * kMat;
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      ck.a[i] = *(const int4*)(A + (long)j * D * D + i * kRowsAt * D);
-      ck.b[i] = *(const int4*)(Bm + (long)j * D * D + i * kRowsAt * D);
+      for (int i = 0; i < kMat / 16 / kCompute; ++i) {
+        const int e = tid + i * kCompute, at = code_at<D>(e / kPieces, e % kPieces);
+        cp16(dst + at, A + (long)j * kMat + 16 * e);
+        cp16(dst + kMat + at, Bm + (long)j * kMat + 16 * e);
+      }
+      if (tid == 0) {
+        cp16(&sc_s[st], a.df + ((long)bh * a.max_chunks + j) * 4);
+        g_s[st] = act_g[p];
+      }
     }
+    asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  Chunk next[kAhead];
-#pragma unroll
-  for (int i = 0; i < kAhead; ++i) load(cnt - 1 - i, next[i]);
+  for (int i = 0; i < kStages - 1; ++i) issue(cnt - 1 - i, i);
   float x = xs[row], y = 0.0f;
   float unit = write_digits(x, row, mx, xd);
-  tc::bar_sync(1, kCompute);
-  int u = 0;
-  for (int p0 = cnt - 1; p0 >= 0; p0 -= kAhead) {
-    Chunk cur[kAhead];
+  const int dcol = lane >> 2;
+  for (int p = cnt - 1, u = 0; p >= 0; --p, ++u) {
+    const int st = u % kStages;
+    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+    tc::bar_sync(1, kCompute);  // the digits and every thread's share of the chunk are there
+    // the stage of the chunk before (read by all before the barrier in write_digits)
+    issue(p - (kStages - 1), (u + kStages - 1) % kStages);
+    const uint8_t* xc = xd + (u & 1) * kU8Vec + dcol * kDigits + 4 * (lane & 3);
+    const uint32_t at = tc::smem_u32(ring) + st * 2 * kMat;
+    int acc[2 * kTiles][4] = {};
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      cur[i] = next[i];
-      load(p0 - kAhead - i, next[i]);
-    }
+    for (int ks = 0; ks < D / 32; ++ks) {
+      const uint32_t x0 = dcol < 3 ? *(const uint32_t*)(xc + 32 * ks) : 0u;
+      const uint32_t x1 = dcol < 3 ? *(const uint32_t*)(xc + 32 * ks + 16) : 0u;
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      if (p0 - i < 0) break;
-      const uint8_t* xc = xd + (u & 1) * kU8Vec + 16 * q;
-      int4 dg[3];
-#pragma unroll
-      for (int k = 0; k < 3; ++k) dg[k] = *(const int4*)(xc + k * kDigits);
-      auto row_sum = [&](const int4& c) {
-        int s[3];
-#pragma unroll
-        for (int k = 0; k < 3; ++k)
-          s[k] = __dp4a(c.w, dg[k].w, __dp4a(c.z, dg[k].z, __dp4a(c.y, dg[k].y, __dp4a(c.x, dg[k].x, 0))));
-        return fmaf((float)s[2], 65536.0f, fmaf((float)s[1], 256.0f, (float)s[0]));
-      };
-      float va[kLoads], vb[kLoads];
-#pragma unroll
-      for (int e = 0; e < kLoads; ++e) {
-        va[e] = row_sum(cur[i].a[e]);
-        vb[e] = row_sum(cur[i].b[e]);
+      for (int t = 0; t < 2 * kTiles; ++t) {
+        uint32_t f[4];
+        const int r = D / 4 * warp + 16 * (t % kTiles) + (lane & 15);
+        ldmatrix4(at + (t / kTiles) * kMat + code_at<D>(r, 2 * ks + (lane >> 4)), f);
+        mma_s8(acc[t], f, x0, x1);
       }
-      // sums over a row's lanes, each step handing half of the rows to the lane across
-#pragma unroll
-      for (int o = kLanes / 2, k = kLoads; o > 0; o >>= 1) {
-        const bool up = (q & o) != 0;
-        if (k > 1) {
-          k >>= 1;
-#pragma unroll
-          for (int e = 0; e < kLoads / 2; ++e)
-            if (e < k) {
-              const float ga = up ? va[e] : va[e + k], gb = up ? vb[e] : vb[e + k];
-              va[e] = (up ? va[e + k] : va[e]) + __shfl_xor_sync(0xFFFFFFFFu, ga, o);
-              vb[e] = (up ? vb[e + k] : vb[e]) + __shfl_xor_sync(0xFFFFFFFFu, gb, o);
-            }
-        } else {
-          va[0] += __shfl_xor_sync(0xFFFFFFFFu, va[0], o);
-          vb[0] += __shfl_xor_sync(0xFFFFFFFFu, vb[0], o);
-        }
-      }
-      const float g = cur[i].g;
-      const float4 sc = cur[i].sc;
-      y = fmaf(g * sc.z, vb[0] * unit, y);
-      x = fmaf(1.0f - g, x, g * fmaf(sc.x, x, sc.y * (va[0] * unit)));
-      ++u;
-      unit = write_digits(x, row, mx + 4 * (u & 1), xd + (u & 1) * kU8Vec);
-      tc::bar_sync(1, kCompute);
     }
+    float sa = 0.0f, sb = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 2 * kTiles; ++k) {  // as in decode_stream8_kernel
+      const int t = k >> 1, c = 2 * (k & 1);
+      const int a2 = __shfl_xor_sync(0xFFFFFFFFu, acc[t][c], 1);
+      const int b2 = __shfl_xor_sync(0xFFFFFFFFu, acc[kTiles + t][c], 1);
+      float va = fmaf((float)a2, 65536.0f, fmaf((float)acc[t][c + 1], 256.0f, (float)acc[t][c]));
+      float vb = fmaf((float)b2, 65536.0f, fmaf((float)acc[kTiles + t][c + 1], 256.0f, (float)acc[kTiles + t][c]));
+      va = __shfl_sync(0xFFFFFFFFu, va, lane & 28);
+      vb = __shfl_sync(0xFFFFFFFFu, vb, lane & 28);
+      if (own == k) {
+        sa = va;
+        sb = vb;
+      }
+    }
+    const float g = g_s[st];
+    const float4 sc = sc_s[st];
+    y = fmaf(g * sc.z, sb * unit, y);
+    x = fmaf(1.0f - g, x, g * fmaf(sc.x, x, sc.y * (sa * unit)));
+    unit = write_digits(x, row, mx + 4 * ((u + 1) & 1), xd + ((u + 1) & 1) * kU8Vec);
   }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
   stf((Tio*)a.o + (long)bh * D + row, y + ys[row]);
+}
+
+template <int D, typename Tio>
+cudaError_t launch_rows8(const DecodeArgs& a, cudaStream_t s) {
+  const int smem = rows8_stages<D>() * 2 * D * D;
+  cudaError_t e = cudaFuncSetAttribute(decode_rows8_kernel<D, Tio>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  decode_rows8_kernel<D, Tio><<<a.B * a.H, kCompute, smem, s>>>(a);
+  return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_decode8(const DecodeArgs& a, cudaStream_t s) {
-  if (a.d == 64) {
-    if (a.dtype == HLA_BF16)
-      decode_rows8_kernel<64, __nv_bfloat16><<<a.B * a.H, kCompute, 0, s>>>(a);
-    else
-      decode_rows8_kernel<64, float><<<a.B * a.H, kCompute, 0, s>>>(a);
-    return cudaGetLastError();
-  }
-  if (a.dtype != HLA_BF16) {
-    decode_rows8_kernel<128, float><<<a.B * a.H, kCompute, 0, s>>>(a);
-    return cudaGetLastError();
-  }
+  if (a.d == 64) return a.dtype == HLA_BF16 ? launch_rows8<64, __nv_bfloat16>(a, s) : launch_rows8<64, float>(a, s);
+  if (a.dtype != HLA_BF16) return launch_rows8<128, float>(a, s);
   const long rows = (long)a.B * a.H * a.max_chunks * kD;
   if (rows >= (1L << 31)) return cudaErrorNotSupported;  // tile coordinates are 32-bit
   // a row of 128 codes as 64 two-byte elements
