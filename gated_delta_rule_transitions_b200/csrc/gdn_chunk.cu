@@ -539,7 +539,7 @@ __device__ __forceinline__ void store_frag(uint32_t dst, int q, int ch, int lane
 template <int kV>
 __global__ void __launch_bounds__(Geo<kV>::kThreads, 1)
     gdn_scan_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                    const __grid_constant__ CUtensorMap tmV, GdnArgs a, const uint8_t* ws) {
+                    const __grid_constant__ CUtensorMap tmV, GdnArgs a, const uint8_t* ws, bool longest_first) {
   using G = Geo<kV>;
   constexpr int kSplit = kD / kV;
   constexpr int kScThreads = G::kThreads;
@@ -563,8 +563,24 @@ __global__ void __launch_bounds__(Geo<kV>::kThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int v0 = (int)(blockIdx.x % kSplit) * kV;
   const int h = (int)((blockIdx.x / kSplit) % a.H);
-  const int seq = (int)((blockIdx.x / kSplit) / a.H);
+  int seq = (int)((blockIdx.x / kSplit) / a.H);
   const int hk = h / (a.H / a.Hk);
+  if (longest_first) {
+    // more CTAs than run at once: blocks in order of their sequences' lengths, so that the
+    // longest do not start last (block order -> the sequence of that rank; ties by index)
+    __shared__ int seq_s;
+    for (int s = tid; s < a.n_seq; s += kScThreads) {
+      const int mine = a.cu[s + 1] - a.cu[s];
+      int rank = 0;
+      for (int i = 0; i < a.n_seq; ++i) {
+        const int other = a.cu[i + 1] - a.cu[i];
+        rank += other > mine || (other == mine && i < s);
+      }
+      if (rank == seq) seq_s = s;
+    }
+    __syncthreads();
+    seq = seq_s;
+  }
   // what the device arrays cannot mean is refused: nothing is read or written for it
   int slot = seq;
   if (a.slots != nullptr) {
@@ -906,7 +922,9 @@ cudaError_t launch_scan(const CUtensorMap& tq, const CUtensorMap& tk, const CUte
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, gdn_scan_kernel<kV>, tq, tk, tv, a, ws);
+  // (512 sequences: the ranks cost 2 us)
+  const bool longest_first = (long)cfg.gridDim.x > num_sms() && a.n_seq > 1 && a.n_seq <= 512;
+  return cudaLaunchKernelEx(&cfg, gdn_scan_kernel<kV>, tq, tk, tv, a, ws, longest_first);
 }
 
 }  // namespace
