@@ -112,7 +112,8 @@ __device__ __forceinline__ void to_pairs(const uint4 (&w)[kN / 4], const float*,
 //   c = k_t . x;  y += beta_t c v_t;  x <- alpha_t (x - beta_t c k_t)
 // Lane l has the D / 8 channels from D / 8 (l % 8) of x (four copies, so that a dot product is
 // three shuffles) and the D / 32 channels from D / 32 l of y; the rows of the tokens to come
-// are on their way while these are worked on.
+// are on their way while these are worked on.  The step's own token (t = m) is read from the
+// call's arguments, so that the sweep need not wait for its place in the open chunk.
 template <int D, typename Tio, bool kChan>
 __device__ __forceinline__ void sweep_warp(const DecodeArgs& a, int bh, int m, float* xs, float* ys) {
   constexpr int E = D / 8, F = D / 32;
@@ -120,10 +121,7 @@ __device__ __forceinline__ void sweep_warp(const DecodeArgs& a, int bh, int m, f
   constexpr int kAhead = kChan || sizeof(Tio) == 4 ? 2 : 4;
   const int lane = threadIdx.x & 31;
   const int g = lane & 7;
-  const Tio* bk = (const Tio*)a.buf_k + (long)bh * a.C * D + E * g;
-  const Tio* bv = (const Tio*)a.buf_v + (long)bh * a.C * D + F * lane;
-  const float* ba = a.buf_alpha + (kChan ? (long)bh * a.C * D + E * g : (long)bh * a.C);
-  const float* bb = a.buf_beta + (long)bh * a.C;
+  const long tok = (long)bh * D, buf = (long)bh * a.C * D;
   struct Row {
     uint4 k[W];
     float4 al[kChan ? E / 4 : 1];
@@ -141,17 +139,22 @@ __device__ __forceinline__ void sweep_warp(const DecodeArgs& a, int bh, int m, f
   Row next[kAhead];
   auto load = [&](int t, Row& r) {  // token t (nothing before the first)
     if (t < 0) return;
+    const bool own = t == m;
+    const long at = buf + (long)t * D, one = (long)bh * a.C + t;
+    const Tio* k = (own ? (const Tio*)a.k + tok : (const Tio*)a.buf_k + at) + E * g;
+    const Tio* v = (own ? (const Tio*)a.v + tok : (const Tio*)a.buf_v + at) + F * lane;
 #pragma unroll
-    for (int i = 0; i < W; ++i) r.k[i] = ((const uint4*)(bk + (long)t * D))[i];
+    for (int i = 0; i < W; ++i) r.k[i] = ((const uint4*)k)[i];
     if constexpr (kChan) {
+      const float* al = (own ? a.alpha + tok : a.buf_alpha + at) + E * g;
 #pragma unroll
-      for (int i = 0; i < E / 4; ++i) r.al[i] = ((const float4*)(ba + (long)t * D))[i];
+      for (int i = 0; i < E / 4; ++i) r.al[i] = ((const float4*)al)[i];
     } else {
-      r.al[0].x = ba[t];
+      r.al[0].x = own ? a.alpha[bh] : a.buf_alpha[one];
     }
 #pragma unroll
-    for (int i = 0; i < F; ++i) r.v[i] = bv[(long)t * D + i];
-    r.b = bb[t];
+    for (int i = 0; i < F; ++i) r.v[i] = v[i];
+    r.b = own ? a.beta[bh] : a.buf_beta[one];
   };
 #pragma unroll
   for (int i = 0; i < kAhead; ++i) load(m - i, next[i]);
@@ -203,8 +206,9 @@ __device__ __forceinline__ void sweep_warp(const DecodeArgs& a, int bh, int m, f
 __global__ void __launch_bounds__(kThreads, 2)
     decode_stream8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                           DecodeArgs a) {
-  // the gate kernel's programmatic dependent, like decode_stream_kernel
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // launched as the gate kernel's programmatic dependent, early: the open chunk (but for the
+  // step's own token, an argument) and the counters are not that kernel's, so the sweep runs
+  // beside it; what it writes (the lists) is read after the wait
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* ring = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   float4* sc_s = (float4*)(ring + kU8Units * kU8Unit);  // [kU8Units] a, sA, sB, 0
@@ -222,7 +226,6 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int m = a.m_partial[b];
   const int32_t* act_idx = a.act_idx + (long)bh * a.max_chunks;
   const float* act_g = a.act_g + (long)bh * a.max_chunks;
-  const int cnt = a.act_cnt[bh];
 
   if (tid == 0) {
     for (int u = 0; u < kU8Units; ++u) {
@@ -237,6 +240,8 @@ __global__ void __launch_bounds__(kThreads, 2)
 
   if (tid >= kCompute) {
     // ---------------- TMA producer (warp 4, lane 0): one unit per active chunk ----------------
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int cnt = a.act_cnt[bh];
     if (tid == kCompute && cnt > 0) {
       tc::tma_prefetch_desc(&tmA);
       tc::tma_prefetch_desc(&tmB);
@@ -267,6 +272,8 @@ __global__ void __launch_bounds__(kThreads, 2)
       else
         sweep_warp<kD, __nv_bfloat16, false>(a, bh, m, xs, ys);
     }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int cnt = a.act_cnt[bh];
     tc::bar_sync(1, kCompute);
     float x = xs[row], y = 0.0f;
     float g = cnt > 0 ? act_g[cnt - 1] : 0.0f;

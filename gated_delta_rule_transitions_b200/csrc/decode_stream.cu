@@ -213,6 +213,8 @@ constexpr int kGPieces = 2;                          // ring of the gate kernel
 
 __global__ void __launch_bounds__(kThreads, 3)
     decode_gates_kernel(const __grid_constant__ CUtensorMap tmR, DecodeArgs a) {
+  // the 8-bit cache's chain kernel sweeps the open chunk beside this grid
+  if (a.format == HLA_CACHE_INT8) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* ring = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   uint64_t* full = (uint64_t*)(ring + kGPieces * kUnit);
