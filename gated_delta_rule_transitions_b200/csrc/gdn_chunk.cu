@@ -581,15 +581,23 @@ __global__ void __launch_bounds__(Geo<kV>::kThreads, 1)
     __syncthreads();
     seq = seq_s;
   }
+  // launched as gdn_wy_kernel's programmatic dependent: a block waits for that grid where it
+  // reads what it wrote (the loading warp), or here before it leaves, so that this grid never
+  // ends first
+  auto wait_wy = [] { asm volatile("griddepcontrol.wait;" ::: "memory"); };
   // what the device arrays cannot mean is refused: nothing is read or written for it
   int slot = seq;
   if (a.slots != nullptr) {
     slot = a.slots[seq];
-    if (slot < 0) return;  // padding of the batch
+    if (slot < 0) {  // padding of the batch
+      wait_wy();
+      return;
+    }
     bool twice = false;    // an earlier sequence has the same state
     for (int i = tid; i < seq; i += kScThreads) twice |= a.slots[i] == slot;
     if (__syncthreads_or(twice) || slot >= a.n_slots) {
       if (tid == 0) report_device_error(kErrBadIndex);
+      wait_wy();
       return;
     }
   }
@@ -601,6 +609,7 @@ __global__ void __launch_bounds__(Geo<kV>::kThreads, 1)
   if (!good_bounds(s0, s1, a.T) ||
       (nc > 0 && (slot_owner(a.cu, a.n_seq, base) != seq || slot_owner(a.cu, a.n_seq, base + nc - 1) != seq))) {
     if (tid == 0) report_device_error(kErrBadIndex);
+    wait_wy();
     return;
   }
   const long soff = ((long)slot * a.H + h) * kD * kD + (long)v0 * kD;  // this CTA's state rows
@@ -611,6 +620,7 @@ __global__ void __launch_bounds__(Geo<kV>::kThreads, 1)
         if (a.state_in != nullptr) w = ((const float4*)(a.state_in + soff))[e];
         ((float4*)(a.state_out + soff))[e] = w;
       }
+    wait_wy();
     return;
   }
 
@@ -647,9 +657,7 @@ __global__ void __launch_bounds__(Geo<kV>::kThreads, 1)
       tc::tma_prefetch_desc(&tmK);
       tc::tma_prefetch_desc(&tmV);
       const uint8_t* wy = ws + ((long)base * a.H + h) * kSlot;
-      // launched as gdn_wy_kernel's programmatic dependent: the workspace is its output (the
-      // call's inputs were there before that grid started)
-      asm volatile("griddepcontrol.wait;" ::: "memory");
+      wait_wy();  // the workspace; the call's inputs were there before that grid started
       auto load_stage = [&](int c) {
         const int st = c % kStages;
         if (c >= kStages && !tc::mbar_wait(&empty[st], ((c / kStages) - 1) & 1, abort_s)) return false;

@@ -298,7 +298,8 @@ hla_status hla_gate_mass(const hla_config* cfg, const float* gates, float* mass_
  * chunks' weights.  Entries of dst beyond the kept chunks are left as they were.
  * In:  src (its mass must be tracked), keep in [1, dst->max_chunks], recent in [0, keep].
  * Out: kept_out [B,H,keep] int32 (device): the kept chunks' old indices, ascending, then -1.
- * Any cache format.  Deterministic, no workspace.
+ * Any cache format.  Deterministic, no workspace.  Slices taken of a cache before it was
+ * tracked are not tracked.
  * Errors: INVALID_ARG, UNSUPPORTED, CUDA.
  */
 hla_status hla_cache_evict(const hla_config* cfg, const hla_cache* src, hla_cache* dst, int32_t keep,
@@ -314,7 +315,13 @@ hla_status hla_cache_evict(const hla_config* cfg, const hla_cache* src, hla_cach
  * A negative slot marks padding of a batch: that entry is left out, its outputs and state
  * stay as they were.  A slot >= n_slots, a slot that an earlier sequence of the call has,
  * or sequence bounds that fall or leave [0, T] leave that sequence out too and record code
- * 0x10, reported by hla_device_status.
+ * 0x10, reported by hla_device_status.  Keys are meant to be of length one or less with
+ * beta in [0, 1], as in the token rule above; o must not overlap the inputs.
+ * bf16 with d = 128, the scalar decay and at least 40 tokens a sequence in the mean run by
+ * chunks of 64 tokens on the tensor cores, with the state and everything that reaches it
+ * held to float32's precision; the others run the rule token by token on CUDA cores.
+ * Calls are deterministic.  Those whose kernels may overlap in time (other streams, two
+ * graphs) need workspaces and states of their own.
  */
 typedef struct gdn_config {
   int32_t n_seq;      /* sequences of the call                            */

@@ -277,3 +277,85 @@ def test_two_calls_on_two_streams(hla):
     torch.cuda.synchronize()
     for g, w in zip(got, want):
         assert torch.equal(g[0], w[0]) and torch.equal(g[1], w[1])
+
+
+@pytest.mark.parametrize("n,H,Hk", [(24, 4, 2), (7, 4, 4), (3, 16, 8), (40, 8, 8)])
+def test_many_sequences_of_mixed_lengths(hla, n, H, Hk):
+    """The chunked form over one to many CTAs per SM (16, 32 and 64 value columns per CTA,
+    longest sequences first), padded entries and a slot twice among them."""
+    gen = torch.Generator().manual_seed(n)
+    lens = [int(x) for x in torch.randint(1, 260, (n,), generator=gen)]
+    lens[0], lens[n // 2] = 300, 0
+    T, d = sum(lens), 128
+    q, k, v, al, be = R.tokens(gen, T, Hk, H, d, R.BF16)
+    cu = torch.tensor([0] + lens).cumsum(0).to(torch.int32)
+    slots = torch.randperm(n, generator=gen).to(torch.int32)
+    slots[1] = -1
+    if n > 10:
+        slots[9] = slots[4]
+    live = [i for i in range(n) if i != 1 and not (n > 10 and i == 9)]
+    S0 = torch.randn(n, H, d, d, generator=gen)
+    cfg = hla.make_gdn_config(n, H, d, "bf16", Hk=Hk, n_slots=n)
+    S, o = S0.cuda(), torch.full((T, H, d), 7.0, dtype=R.BF16, device="cuda")
+    hla.gdn_forward(cfg, *cuda(q, k, v, al, be, cu), o, state_in=S, state_out=S, slots=slots.cuda())
+    bounds = [(int(cu[i]), int(cu[i + 1])) for i in live]
+    ro, rS = R.gdn_reference(q, k, v, al, be, bounds, S0[slots[live].long()])
+    tol = state_tol(300, d, R.BF16, True)
+    got, o = S.cpu(), o.cpu()
+    for i, (a, e) in enumerate(bounds):
+        assert R.rel(got[int(slots[live[i]])], rS[i]) <= tol, i
+        if e > a:
+            assert R.rel(o[a:e], ro[a:e]) <= tol + R.half_step(R.BF16), i
+    for i in set(range(n)) - set(live):
+        assert torch.equal(o[int(cu[i]):int(cu[i + 1])], torch.full_like(o[int(cu[i]):int(cu[i + 1])], 7.0))
+    st, code = hla.hla_device_status()
+    assert code == (16 if n > 10 else 0)
+
+
+def test_agrees_with_the_gated_composition_of_weight_one(hla):
+    """HLA with every gate one is the rule itself: the prompt's outputs by gdn_forward and by
+    hla_prefill, then tokens by gdn_step from the state and by hla_decode_step over the cached
+    transitions, both to the composition's own bar (bf16 transitions: relative L2 2e-2)."""
+    import hla_synth as syn
+    w = syn.GDN_REDUCTION.with_(B=1, H=2, T=64 * 5 + 9)
+    inp = {k: v.cuda() for k, v in syn.make_gdn_inputs(w).items()}
+    H, d = 2, 128
+    mk = lambda T: hla.make_config(1, H, T, 64, d, "bf16", "one")
+    cache = hla.Cache(mk(w.T), 8)
+    o1, o2 = torch.empty_like(inp["q"]), torch.empty_like(inp["q"])
+    hla.hla_prefill(mk(w.T), inp["q"], inp["k"], inp["v"], inp["alpha"], inp["beta"], o1, cache=cache)
+    cfg = hla.make_gdn_config(1, H, d, "bf16")
+    S = torch.zeros(1, H, d, d, device="cuda")
+    cu = torch.tensor([0, w.T], dtype=torch.int32, device="cuda")
+    rows = {k: inp[k][0].contiguous() for k in inp}
+    hla.gdn_forward(cfg, rows["q"], rows["k"], rows["v"], rows["alpha"], rows["beta"], cu, o2[0], state_in=S,
+                    state_out=S)
+    for h in range(H):
+        assert R.rel(o1[0, :, h], o2[0, :, h]) <= 2e-2
+    for tok in syn.make_decode_tokens(w, 3):
+        t = {k: v.cuda() for k, v in tok.items()}
+        a, b = torch.empty_like(t["q"]), torch.empty_like(t["q"])
+        hla.hla_decode_step(mk(1), cache, t["q"], t["k"], t["v"], t["alpha"], t["beta"], a)
+        hla.gdn_step(cfg, t["q"], t["k"], t["v"], t["alpha"], t["beta"], S, b)
+        for h in range(H):
+            assert R.rel(a[0, h], b[0, h]) <= 2e-2
+    assert hla.hla_device_status() == (0, 0)
+
+
+def test_binding_refuses_wrong_sizes_and_types(hla):
+    gen = torch.Generator().manual_seed(1)
+    q, k, v, al, be = cuda(*R.tokens(gen, 2, 1, 2, 64, R.BF16))
+    cfg = hla.make_gdn_config(2, 2, 64, "bf16", Hk=1)
+    S, o = torch.zeros(2, 2, 64, 64, device="cuda"), torch.empty_like(v)
+    with pytest.raises(ValueError, match="q: expected"):
+        hla.gdn_step(cfg, v, k, v, al, be, S, o)
+    with pytest.raises(TypeError, match="state"):
+        hla.gdn_step(cfg, q, k, v, al, be, S.bfloat16(), o)
+    with pytest.raises(ValueError, match="contiguous"):
+        hla.gdn_step(cfg, q, k, v.transpose(0, 1).contiguous().transpose(0, 1), al, be, S, o)
+    with pytest.raises(TypeError, match="slots"):
+        hla.gdn_step(cfg, q, k, v, al, be, S, o, slots=torch.zeros(2, device="cuda"))
+    ws = torch.empty(128, dtype=torch.uint8, device="cuda")
+    cu = torch.tensor([0, 1, 2], dtype=torch.int32, device="cuda")
+    with pytest.raises(hla.HlaError, match="workspace"):
+        hla.gdn_forward(cfg, q, k, v, al, be, cu, o, workspace=ws)
