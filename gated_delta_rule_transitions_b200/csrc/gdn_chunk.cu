@@ -17,7 +17,8 @@
 // a product (S, R, U, T) goes in as three bf16 numbers, x = x1 + x2 + x3, each the eight bits
 // after the one before: exactly x (two would leave 2^-16 of it out, more than float32 sums
 // do).  K, Q and V are bf16 already.  Left out are the products of parts that are 2^-22 and
-// less.  G, which reaches the bf16 output and nothing else, goes in as two.  Decays are
+// less.  G, which reaches the bf16 output and nothing else, is made of factors rounded to
+// tf32 (2^-12, an eighth of the output's own rounding) and goes in as two parts.  Decays are
 // differences of 64-bit running sums.
 #include "common.cuh"
 #include "kernels.cuh"
@@ -111,6 +112,12 @@ __device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
 }
 
+__device__ __forceinline__ uint32_t tf32(float x) {
+  uint32_t r;
+  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(x));
+  return r;
+}
+
 // x as two tf32 numbers, cut (the instruction does not read the last 13 bits): off by 2^-21.
 __device__ __forceinline__ void cut_tf32(float x, uint32_t& h, uint32_t& l) {
   h = __float_as_uint(x) & 0xFFFFE000u;
@@ -118,25 +125,36 @@ __device__ __forceinline__ void cut_tf32(float x, uint32_t& h, uint32_t& l) {
 }
 
 // acc[j] += A (16 x 16) B (16 x 8 kN)'s column tile j, float32 in shared memory (row pitches
-// pa, pb).
-template <int kN>
+// pa, pb); kExact: of two tf32 numbers each, else of one (rounded: off by 2^-12).
+template <int kN, bool kExact>
 __device__ __forceinline__ void block16(float (&acc)[kN][4], const float* A, int pa, const float* B, int pb,
                                         int lane) {
   const int g = lane >> 2, q = lane & 3;
 #pragma unroll
   for (int k0 = 0; k0 < 16; k0 += 8) {
+    const float a[4] = {A[g * pa + k0 + q], A[(g + 8) * pa + k0 + q], A[g * pa + k0 + q + 4],
+                        A[(g + 8) * pa + k0 + q + 4]};
     uint32_t ah[4], al[4];
-    cut_tf32(A[g * pa + k0 + q], ah[0], al[0]);
-    cut_tf32(A[(g + 8) * pa + k0 + q], ah[1], al[1]);
-    cut_tf32(A[g * pa + k0 + q + 4], ah[2], al[2]);
-    cut_tf32(A[(g + 8) * pa + k0 + q + 4], ah[3], al[3]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (kExact)
+        cut_tf32(a[i], ah[i], al[i]);
+      else
+        ah[i] = tf32(a[i]);
 #pragma unroll
     for (int j = 0; j < kN; ++j) {
+      const float b[2] = {B[(k0 + q) * pb + 8 * j + g], B[(k0 + q + 4) * pb + 8 * j + g]};
       uint32_t bh[2], bl[2];
-      cut_tf32(B[(k0 + q) * pb + 8 * j + g], bh[0], bl[0]);
-      cut_tf32(B[(k0 + q + 4) * pb + 8 * j + g], bh[1], bl[1]);
-      mma_tf32(acc[j], ah, bl);
-      mma_tf32(acc[j], al, bh);
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        if (kExact)
+          cut_tf32(b[i], bh[i], bl[i]);
+        else
+          bh[i] = tf32(b[i]);
+      if (kExact) {
+        mma_tf32(acc[j], ah, bl);
+        mma_tf32(acc[j], al, bh);
+      }
       mma_tf32(acc[j], ah, bh);
     }
   }
@@ -327,7 +345,7 @@ __global__ void __launch_bounds__(128, 5)
     const int kb = blk - (ib * (ib - 1)) / 2;
     float acc[1][4] = {};
     float* at = Ls + 16 * ib * kP + 16 * kb + 8 * nh;
-    block16<1>(acc, Us + 16 * ib * kP + 16 * ib, kP, at, kP, lane);
+    block16<1, true>(acc, Us + 16 * ib * kP + 16 * ib, kP, at, kP, lane);
     __syncwarp();
     store16(at, kP, acc[0], 1.0f, lane);
   }
@@ -339,7 +357,7 @@ __global__ void __launch_bounds__(128, 5)
       float acc[1][4] = {};
 #pragma unroll
       for (int k = 0; k < lev; ++k)
-        block16<1>(acc, Ls + 16 * (jb + lev) * kP + 16 * (jb + k), kP, Us + 16 * (jb + k) * kP + 16 * jb + 8 * nh, kP,
+        block16<1, true>(acc, Ls + 16 * (jb + lev) * kP + 16 * (jb + k), kP, Us + 16 * (jb + k) * kP + 16 * jb + 8 * nh, kP,
                    lane);
       store16(Us + 16 * (jb + lev) * kP + 16 * jb + 8 * nh, kP, acc[0], -1.0f, lane);
     }
@@ -364,7 +382,7 @@ __global__ void __launch_bounds__(128, 5)
     if (u < blocks) {
       int i, j;
       g_at(u, i, j);
-      for (int k = j; k <= i; ++k) block16<2>(ga[u], Ls + 16 * i * kP + 16 * k, kP, Us + 16 * k * kP + 16 * j, kP, lane);
+      for (int k = j; k <= i; ++k) block16<2, false>(ga[u], Ls + 16 * i * kP + 16 * k, kP, Us + 16 * k * kP + 16 * j, kP, lane);
     }
   __syncthreads();
 #pragma unroll
@@ -378,10 +396,9 @@ __global__ void __launch_bounds__(128, 5)
   __syncthreads();
   // out: the parts of T and G as swizzled tiles, then gamma_t and gamma_C / gamma_t
   uint8_t* out = ws + ((long)slot * a.H + h) * kSlot;
-  const int t = tid & (kC - 1);
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    const int c8 = 4 * (tid >> 6) + e;
+    const int t = 16 * e + (tid >> 3), c8 = tid & 7;  // a warp writes four whole rows at once
     uint32_t w[5][4] = {};  // T1, G1, T2, G2, T3 (blocks above the diagonal are zero)
     if ((c8 >> 1) <= (t >> 4)) {
 #pragma unroll
