@@ -457,14 +457,15 @@ constexpr uint32_t kStTx = 5 * kTile + kScal;
 template <int kV>
 struct Geo {
   static constexpr int kAtoms = kV == 64 ? 3 : kV == 32 ? 2 : 1;
-  static constexpr int kHalf = 16;                  // columns per warp
+  static constexpr int kHalf = 16;                  // columns per warp (output() counts on it)
   static constexpr int kSets = kV / kHalf;          // warps per 32 rows
   static constexpr int kThreads = 64 + 128 * kSets;
   static constexpr int kPieces = kHalf / 8;   // 16-byte pieces of a row per warp and part
   static constexpr int kWyAt = kStages * kStage;         // [T1; G1], [T2; G2], [T3; 0]
   static constexpr int kSAt = kWyAt + 6 * kTile;         // S^T: 128 rows
   static constexpr int kRAt = kSAt + kAtoms * 2 * kTile; // R, then U: 64 rows
-  static constexpr int kSmallAt = kRAt + kAtoms * kTile;
+  static constexpr int kOutAt = kRAt + kAtoms * kTile;  // 512 bytes per warp: its part of the output
+  static constexpr int kSmallAt = kOutAt + 4 * kSets * 512;
   static constexpr int kSmem = kSmallAt + 160;
   static constexpr uint32_t kIdescA = tc::idesc_bf16_f32(128, 3 * kV, 0, 1);
   static constexpr uint32_t kIdescB2 = tc::idesc_bf16_f32(128, 2 * kV, 0, 1);
@@ -803,17 +804,22 @@ __global__ void __launch_bounds__(Geo<kV>::kThreads, 1)
       float x[kHalf / 2], z[kHalf / 2];
       sum_frag<2, kT>(lanes2 + G::kTmB, kV, x);
       sum_frag<1, kT>(lanes2 + G::kTmB2, kV, z);
-      const int n = len - c * kC;
-      __nv_bfloat16* orow =
-          (__nv_bfloat16*)a.o + ((long)(s0 + c * kC + ta) * a.H + h) * kD + v0 + kHalf * ch + 2 * (lane & 3);
+      // 16 tokens x 16 columns by way of shared memory, so that two lanes write a row's 32 bytes
+      uint32_t w[4];
 #pragma unroll
-      for (int e = 0; e < kHalf / 2; e += 2) {
-        const bool second = (e & 2) != 0;
-        const float g = second ? gb : ga;
-        if (ta + (second ? 8 : 0) < n)
-          *(uint32_t*)(orow + (second ? 8L * a.H * kD : 0) + 8 * (e >> 2)) =
-              tc::pack_bf16x2(fmaf(g, y[e], x[e] + z[e]), fmaf(g, y[e + 1], x[e + 1] + z[e + 1]));
+      for (int m = 0; m < 4; ++m) {  // matrix m: tokens 8 (m & 1) .., columns 8 (m >> 1) ..
+        const int e = 4 * (m >> 1) + 2 * (m & 1);
+        const float g = (m & 1) ? gb : ga;
+        w[m] = tc::pack_bf16x2(fmaf(g, y[e], x[e] + z[e]), fmaf(g, y[e + 1], x[e + 1] + z[e + 1]));
       }
+      uint8_t* stage = sm + G::kOutAt + (warp - 2) * 512;
+      __syncwarp();  // (the chunk before has been read)
+      stmatrix4(tc::smem_u32(stage) + (lane & 15) * 32 + (lane >> 4) * 16, w);
+      __syncwarp();
+      const uint4 row16 = *(const uint4*)(stage + lane * 16);
+      const int t = c * kC + 16 * q + (lane >> 1);
+      if (t < len)
+        *(uint4*)((__nv_bfloat16*)a.o + ((long)(s0 + t) * a.H + h) * kD + v0 + kHalf * ch + 8 * (lane & 1)) = row16;
     };
     bool ok = true;
     for (int c = 0; c < nc; ++c) {
