@@ -114,14 +114,8 @@ __global__ void __launch_bounds__(kThreads) gdn_recurrent_kernel(GdnArgs a) {
   if (a.slots != nullptr) {
     slot = a.slots[seq];
     if (slot < 0) return;  // padding of the batch
-    bool twice = false;    // an earlier sequence has the same state
-    for (int i = tid; i < seq; i += kThreads) twice |= a.slots[i] == slot;
-    if (__syncthreads_or(twice) || slot >= a.n_slots) {
-      if (tid == 0) report_device_error(kErrBadIndex);
-      return;
-    }
   }
-  if (t0 < 0 || t1 < t0 || t1 > a.T) {
+  if (t0 < 0 || t1 < t0 || t1 > a.T || slot >= a.n_slots) {
     if (tid == 0) report_device_error(kErrBadIndex);
     return;
   }
@@ -172,6 +166,16 @@ __global__ void __launch_bounds__(kThreads) gdn_recurrent_kernel(GdnArgs a) {
       x[r][2 * m] = make_float2(w.x, w.y);
       x[r][2 * m + 1] = make_float2(w.z, w.w);
     }
+
+  if (a.slots != nullptr) {  // (the state and the first tokens are on their way)
+    bool twice = false;      // an earlier sequence has the same state
+    for (int i = tid; i < seq; i += kThreads) twice |= a.slots[i] == slot;
+    if (__syncthreads_or(twice)) {
+      if (tid == 0) report_device_error(kErrBadIndex);
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+      return;
+    }
+  }
 
   int w = 0;
   for (int s0 = 0; s0 < len; s0 += kSeg, w ^= (kOne ? 0 : 1)) {
