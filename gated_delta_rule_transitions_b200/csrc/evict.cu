@@ -9,8 +9,9 @@
 // Three kernels:
 //   gate_mass_kernel   column sums of a gate matrix, each row weighted by its chunk's tokens;
 //   evict_select       one CTA per (sequence, head): the `recent` last chunks stay, the
-//                      others compete by (mass descending, index ascending): a radix select
-//                      over the 32 key bits, 8 at a time, then an ordered compaction;
+//                      others compete by (mass descending, index ascending): each chunk's
+//                      rank by counting up to 256 of them, else a radix select over the 32 key
+//                      bits, 8 at a time; then an ordered compaction;
 //   evict_move         moves every per-chunk array to its place.  A thread owns 16 bytes of
 //                      the chunk and takes the kept chunks in ascending order; entry i comes
 //                      from a chunk kept[i] >= i, and reads run ahead of writes, so the move
@@ -116,6 +117,8 @@ __device__ __forceinline__ int block_prefix(bool flag, int* wsum, int* sum) {
 }
 
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictArgs a) {
+  // the move's blocks take their places meanwhile (they wait for this grid)
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   __shared__ int hist[256];
   __shared__ int wsum[kSelThreads / 32];
   __shared__ int pick[2];  // digit, how many of the wanted lie above it
@@ -131,6 +134,20 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictArgs a) 
   }
   const int old = n - a.recent;        // chunks that compete
   int want = a.keep - a.recent;        // how many of them stay (< old)
+  if (n <= kSelThreads) {
+    // one chunk a thread: a chunk's rank is how many come before it
+    uint32_t* keys = (uint32_t*)hist;
+    const uint32_t mine = tid < old ? mass_key(mass[tid]) : 0u;
+    keys[tid] = mine;
+    __syncthreads();
+    int rank = 0;
+    for (int i = 0; i < old; ++i) rank += keys[i] > mine || (keys[i] == mine && i < tid);
+    const bool stays = tid < n && (tid >= old || rank < want);
+    int total;
+    const int at = block_prefix(stays, wsum, &total);
+    if (stays) kept[at] = tid;
+    return;
+  }
   // the key of the last one that stays (`prefix`), and how many with that key stay (`want`)
   uint32_t prefix = 0, mask = 0;
   if (want > 0) {
@@ -216,6 +233,7 @@ __device__ __forceinline__ void move_column(const uint4* src, uint4* dst, long p
 // Nothing here but that last step reads the counts (the list ends at its first -1), so it
 // may change them.
 __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(EvictArgs a, unsigned blocks) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const long bh = blockIdx.x / (blocks + 1);
   const unsigned blk = blockIdx.x % (blocks + 1);
   const int tid = threadIdx.x;
@@ -294,8 +312,16 @@ cudaError_t launch_evict(const EvictArgs& a, cudaStream_t s) {
   unsigned split = 1;
   if (!a.in_place)
     while (blocks * BH * split < 8L * num_sms() && (long)split * 2 * kMoveBatch <= a.keep) split *= 2;
-  evict_move_kernel<<<dim3((unsigned)(BH * (blocks + 1)), split), kMoveThreads, 0, s>>>(a, (unsigned)blocks);
-  return cudaGetLastError();
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(BH * (blocks + 1)), split);
+  cfg.blockDim = dim3(kMoveThreads);
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, evict_move_kernel, a, (unsigned)blocks);
 }
 
 }  // namespace hla
