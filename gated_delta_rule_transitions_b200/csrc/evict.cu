@@ -27,64 +27,75 @@ namespace {
 
 // ---- mass from a gate matrix -----------------------------------------------------------
 
-// One cluster of eight CTAs per (sequence, head) and 32 kQ columns: a warp reads kQ 128-byte
-// segments of a row, the cluster's 64 warps take the rows in turn (each its own in ascending
-// order), and the 64 sums of a column are added in warp order, the other CTAs' through
-// distributed shared memory: the same bits every time.  The row split evens out the triangle
-// (a tile's rows go from all to few) and leaves work for every SM where heads are few.
+// One cluster of up to eight CTAs per (sequence, head) and 32 kQ kVec columns: a lane reads kQ
+// groups of kVec neighbours of a row (kVec = 4 where rows start on 16 bytes), the cluster's
+// warps take the rows in turn (each its own in ascending order), and the warps' sums of a
+// column are added in warp order, the other CTAs' through distributed shared memory: the same
+// bits every time.  The row split evens out the triangle (a tile's rows go from all to few)
+// and leaves work for every SM where heads are few.
 constexpr int kMassWarps = 8;
-constexpr int kMassCtas = 8;
 
-template <int kQ>
-__global__ void __cluster_dims__(kMassCtas) __launch_bounds__(32 * kMassWarps) gate_mass_kernel(const float* __restrict__ gates, int N, int ncols,
-                                                                     int C, int T, float thr, float* __restrict__ mass,
-                                                                     long mass_stride) {
-  constexpr int kCols = 32 * kQ;
-  __shared__ float part[kMassWarps][kCols];
+template <int kQ, int kVec>
+__global__ void __launch_bounds__(32 * kMassWarps) gate_mass_kernel(
+    const float* __restrict__ gates, int N, int ncols, int C, int T, float thr, float* __restrict__ mass,
+    long mass_stride) {
   namespace cg = cooperative_groups;
   const cg::cluster_group cluster = cg::this_cluster();
-  const int rank = (int)cluster.block_rank();
-  constexpr int kStep = kMassWarps * kMassCtas;
+  const int rank = (int)cluster.block_rank(), ctas = (int)cluster.num_blocks();
+  const int step = kMassWarps * ctas;
+  constexpr int kCols = 32 * kQ * kVec;
+  __shared__ __align__(16) float part[kMassWarps][kCols];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int tiles = (ncols + kCols - 1) / kCols;
-  const long bh = blockIdx.x / kMassCtas / tiles;
-  const int j0 = (int)(blockIdx.x / kMassCtas % tiles) * kCols;
-  const float* G = gates + bh * (long)N * N + j0 + lane;
-  float acc[kQ] = {};
+  const long bh = blockIdx.x / ctas / tiles;
+  const int j0 = (int)(blockIdx.x / ctas % tiles) * kCols;
+  const float* G = gates + bh * (long)N * N + j0 + kVec * lane;
+  float acc[kQ][kVec] = {};
   // rows i > j hold a weight on chunk j; row i stands for the tokens of chunk i
   int i = j0 + 1 + rank * kMassWarps + w;
-  for (; i < min(N, j0 + kCols); i += kStep) {  // rows that meet the diagonal
+  for (; i < min(N, j0 + kCols); i += step) {  // rows that meet the diagonal
     const float wt = (float)min(C, T - i * C);
 #pragma unroll
     for (int q = 0; q < kQ; ++q)
-      if (j0 + 32 * q + lane < i) {
-        const float g = __ldg(G + (long)i * N + 32 * q);
-        if (thr <= 0.0f || g >= thr) acc[q] = fmaf(wt, g, acc[q]);
-      }
+#pragma unroll
+      for (int v = 0; v < kVec; ++v)
+        if (j0 + kVec * (32 * q + lane) + v < i) {
+          const float g = __ldg(G + (long)i * N + 32 * kVec * q + v);
+          if (thr <= 0.0f || g >= thr) acc[q][v] = fmaf(wt, g, acc[q][v]);
+        }
   }
-#pragma unroll(kQ == 8 ? 4 : 8)
-  for (; i < N; i += kStep) {  // below it every column of the tile counts (j0 + kCols <= i < N)
+#pragma unroll(kVec == 4 ? 8 : 4)
+  for (; i < N; i += step) {  // below it every column of the tile counts (j0 + kCols <= i < N)
     const float wt = (float)min(C, T - i * C);
 #pragma unroll
     for (int q = 0; q < kQ; ++q) {
-      const float g = __ldg(G + (long)i * N + 32 * q);
-      acc[q] = fmaf(wt, thr <= 0.0f || g >= thr ? g : 0.0f, acc[q]);
+      float g[kVec];
+      if constexpr (kVec == 4) {
+        const float4 f = __ldg((const float4*)(G + (long)i * N + 128 * q));
+        g[0] = f.x, g[1] = f.y, g[2] = f.z, g[3] = f.w;
+      } else {
+        g[0] = __ldg(G + (long)i * N + 32 * q);
+      }
+#pragma unroll
+      for (int v = 0; v < kVec; ++v) acc[q][v] = fmaf(wt, thr <= 0.0f || g[v] >= thr ? g[v] : 0.0f, acc[q][v]);
     }
   }
 #pragma unroll
-  for (int q = 0; q < kQ; ++q) part[w][32 * q + lane] = acc[q];
-  cluster.sync();
-  if (rank == 0)
-    for (int c = threadIdx.x; c < kCols; c += 32 * kMassWarps)
-      if (j0 + c < ncols) {
-        float s = 0.0f;
-        for (int r = 0; r < kMassCtas; ++r) {
-          const float* p = cluster.map_shared_rank(&part[0][0], r);
+  for (int q = 0; q < kQ; ++q)
 #pragma unroll
-          for (int k = 0; k < kMassWarps; ++k) s += p[k * kCols + c];
-        }
-        mass[bh * mass_stride + j0 + c] = s;
+    for (int v = 0; v < kVec; ++v) part[w][kVec * (32 * q + lane) + v] = acc[q][v];
+  cluster.sync();
+  // each CTA adds up its share of the columns
+  for (int c = rank * (kCols / ctas) + threadIdx.x; c < (rank + 1) * (kCols / ctas); c += 32 * kMassWarps)
+    if (j0 + c < ncols) {
+      float s = 0.0f;
+      for (int r = 0; r < ctas; ++r) {
+        const float* p = cluster.map_shared_rank(&part[0][0], r);
+#pragma unroll
+        for (int k = 0; k < kMassWarps; ++k) s += p[k * kCols + c];
       }
+      mass[bh * mass_stride + j0 + c] = s;
+    }
   cluster.sync();  // the other CTAs' shared memory stays until it has been read
 }
 
@@ -286,15 +297,30 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(EvictArgs a, u
 cudaError_t launch_gate_mass(const float* gates, int B, int H, int N, int ncols, int C, int T, float thr, float* mass,
                              long mass_stride, cudaStream_t s) {
   const long BH = (long)B * H;
-  // wide tiles while they fill the GPU, else narrow ones
-  auto fills = [&](int cols) { return BH * ((ncols + cols - 1) / cols) * kMassCtas >= 4L * num_sms(); };
-  const int cols = fills(256) ? 256 : fills(128) ? 128 : 32;
-  const long blocks = BH * ((ncols + cols - 1) / cols);
+  auto tiles = [&](int cols) { return BH * ((ncols + cols - 1) / cols); };
+  // Wide tiles while eight CTAs each reach every SM, else narrow ones; CTAs per tile until they
+  // fill the GPU and a warp has at most 32 rows.  (32 heads of 2048 chunks: 58 us with eight
+  // CTAs, 63 with four, 77 with two, 137 with one; 256 heads of 512: 49, 41, 43, 48; 1024 heads
+  // of 64: 37, 21, 14, 12.)
+  const int cols = tiles(256) * 8 >= num_sms() ? 256 : 32;
+  int ctas = 1;
+  while (ctas < 8 && (tiles(cols) * ctas < 4L * num_sms() || N > 32 * kMassWarps * ctas)) ctas *= 2;
+  const long blocks = tiles(cols) * ctas;
   if (blocks <= 0) return cudaSuccess;
-  if (blocks * kMassCtas >= (1L << 31)) return cudaErrorNotSupported;
-  auto* k = cols == 256 ? gate_mass_kernel<8> : cols == 128 ? gate_mass_kernel<4> : gate_mass_kernel<1>;
-  k<<<(unsigned)(blocks * kMassCtas), 32 * kMassWarps, 0, s>>>(gates, N, ncols, C, T, thr, mass, mass_stride);
-  return cudaGetLastError();
+  if (blocks >= (1L << 31)) return cudaErrorNotSupported;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)ctas;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)blocks);
+  cfg.blockDim = dim3(32 * kMassWarps);
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  auto* k = cols == 32 ? gate_mass_kernel<1, 1> : N % 4 == 0 ? gate_mass_kernel<2, 4> : gate_mass_kernel<8, 1>;
+  return cudaLaunchKernelEx(&cfg, k, gates, N, ncols, C, T, thr, mass, mass_stride);
 }
 
 cudaError_t launch_evict(const EvictArgs& a, cudaStream_t s) {
