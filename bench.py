@@ -85,8 +85,8 @@ NCU_TRAFFIC = {
     "compose": (2.0470e9, {"compose_tc.cu": "4b50659baac7102a", "tc_common.cuh": "c10beda371c1dd4b"}),
     # gate + stream kernels of one step, captured on 4 (dense) and 8 (planted) of the
     # 64 sequences and scaled by the sequence count (the traffic is per sequence)
-    "decode_main": (3.4638e10, {"decode_stream.cu": "8916b84931f22b4f", "tc_common.cuh": "c10beda371c1dd4b"}),
-    "decode_planted": (5.447e8, {"decode_stream.cu": "8916b84931f22b4f", "tc_common.cuh": "c10beda371c1dd4b"}),
+    "decode_main": (3.4638e10, {"decode_stream.cu": "90389899cb805966", "tc_common.cuh": "c10beda371c1dd4b"}),
+    "decode_planted": (5.447e8, {"decode_stream.cu": "90389899cb805966", "tc_common.cuh": "c10beda371c1dd4b"}),
 }
 
 # Datasheet figures of one B200, reported beside the measured denominators: dense
@@ -569,6 +569,8 @@ def run_ours(args):
     n_ctx = wd.T // wd.C
     if args.decode_cache == "factored":
         per_chunk = 3 * wd.C * wd.d * 2 + (wd.C + 4) * 4   # K, Wb, Ub bf16 + scales
+    elif args.decode_cache == "int8":
+        per_chunk = 2 * wd.d * wd.d + 16                     # A, B codes + scales
     else:
         per_chunk = 2 * wd.d * wd.d * 2                      # A, B bf16
     key_reps = wd.C // wd.window if wd.window else 1
@@ -924,8 +926,9 @@ def main(argv=None):
     ap.add_argument("--decode-workload", choices=["dense", "planted"], default="dense",
                     help="main decode line: every cached chunk active (dense) or the planted routes "
                          "(about 4 active chunks per sequence and head)")
-    ap.add_argument("--decode-cache", choices=["dense", "factored"], default="dense",
-                    help="dense: A_j/B_j d x d (the metric's workload); factored: K_j, Wb_j, Ub_j per chunk")
+    ap.add_argument("--decode-cache", choices=["dense", "factored", "int8"], default="dense",
+                    help="dense: A_j/B_j d x d (the metric's workload); factored: K_j, Wb_j, Ub_j per chunk; "
+                         "int8: A_j/B_j in 8 bits with scales per chunk and head")
     ap.add_argument("--chunk", type=int, choices=[64, 128, 256], default=64,
                     help="chunk size C of both workloads (the metric's workloads use 64)")
     ap.add_argument("--pool-window", type=int, default=0,

@@ -10,6 +10,11 @@
 // stored entry is off by at most sA / 2 or sB / 2.  A matrix of zeros has scale 0 and codes
 // 0; one that holds an infinity or a NaN has such a scale, so that it does not pass for a
 // number.  Half the bytes of the bf16 cache, a quarter of float32.
+//
+// A CTA per chunk and head reads A and B twice (the second time from L2): the scale has to be
+// known before the first code.  Holding the values in registers instead leaves one CTA per SM.
+// Measured: 256 chunks of 16 heads, d = 128, bf16: 144 us, 402 MB, 2.8 TB/s, bound by the
+// instructions per value (327 us with the values held); a prompt's fill, 5 % of its prefill.
 #include "common.cuh"
 #include "kernels.cuh"
 

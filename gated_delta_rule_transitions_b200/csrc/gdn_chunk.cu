@@ -10,8 +10,13 @@
 //   R = V - diag(gamma) K S^T,  U = T R,  O = diag(gamma) Q S^T + G R,
 //   S <- gamma_C S + U^T diag(gamma_C / gamma_t) K                 (gdn_scan_kernel)
 // T and G do not depend on the state: gdn_wy_kernel makes them for every chunk at once.
-// gdn_scan_kernel then walks the chunks of one (sequence, head) and one half of the value
-// dim, three products a chunk, each waiting for the one before.
+// gdn_scan_kernel then walks the chunks of one (sequence, head) and 16, 32 or 64 of its value
+// columns, three products a chunk, each waiting for the one before.
+//
+// What bounds it: the scan's chain of a chunk, 3,030 cycles with 16 columns and 6,000 with 64
+// (there shared memory's bandwidth as well); the tensor cores are active 16 % of the time.
+// Measured, 16 heads: 16384 tokens of one sequence 499 us (T and G 88, the scan 400), four
+// sequences of 4096 tokens 303 us (88 and 210).
 //
 // Precision.  The state is float32 and stays so: it is held in registers, and what goes into
 // a product (S, R, U, T) goes in as three bf16 numbers, x = x1 + x2 + x3, each the eight bits
