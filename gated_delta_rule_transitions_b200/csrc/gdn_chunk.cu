@@ -52,14 +52,19 @@ __device__ __forceinline__ int stacked(int t) { return 32 * (t >> 4) + (t & 15);
 
 __device__ __forceinline__ int swz(int row, int chunk) { return row * 128 + ((chunk ^ (row & 7)) << 4); }
 
-// Chunk slots.  Sequence s owns the slots cu[s] / 64 + s + c, c < ceil(len / 64): they never
-// meet the next sequence's, so no prefix sum over the lengths is needed.  The owner of a slot
-// is the last sequence whose first slot is not above it.
-__device__ __forceinline__ int slot_owner(const int32_t* cu, int n_seq, int slot) {
-  int lo = 0, hi = n_seq;  // owner in [lo, hi)
+// Chunk slots.  Sequence s owns the slots first_slot(s) + c, c < ceil(len / 64): they never meet
+// the next sequence's, so no prefix sum over the lengths is needed.  cu[s] / 64 + s is such a
+// numbering (T / 64 + n_seq slots); where sequences of 32 tokens and less go by rows and need
+// none, so is cu[s] / 32 (T / 32 + 1 slots).  The owner of a slot is the last sequence whose
+// first slot is not above it.
+__device__ __forceinline__ int first_slot(const GdnArgs& a, int seq) {
+  return a.half_slots ? a.cu[seq] / (kC / 2) : a.cu[seq] / kC + seq;
+}
+__device__ __forceinline__ int slot_owner(const GdnArgs& a, int slot) {
+  int lo = 0, hi = a.n_seq;  // owner in [lo, hi)
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (cu[mid] / kC + mid <= slot)
+    if (first_slot(a, mid) <= slot)
       lo = mid;
     else
       hi = mid;
@@ -202,10 +207,18 @@ __global__ void __launch_bounds__(128, 5)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int h = blockIdx.x % a.H;
   const int slot = blockIdx.x / a.H;
-  const int seq = slot_owner(a.cu, a.n_seq, slot);
+  const int seq = slot_owner(a, slot);
   const int s0 = a.cu[seq], s1 = a.cu[seq + 1];
-  const int c = slot - (s0 / kC + seq);
-  if (!good_bounds(s0, s1, a.T) || c < 0 || c >= (s1 - s0 + kC - 1) / kC) return;  // a slot of no chunk
+  const int c = slot - first_slot(a, seq);
+  // launched as a programmatic dependent where gdn_recurrent_kernel has the short sequences: this
+  // grid has nothing from it and waits (its first block) only so as not to end first
+  auto wait_first = [] {
+    if (blockIdx.x == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
+  };
+  if (!good_bounds(s0, s1, a.T) || s1 - s0 <= a.by_row || c < 0 || c >= (s1 - s0 + kC - 1) / kC) {
+    wait_first();  // a slot of no chunk
+    return;
+  }
   const int t0 = s0 + c * kC;
   const int n = min(kC, s1 - t0);
   const int hk = h / (a.H / a.Hk);
@@ -433,6 +446,7 @@ __global__ void __launch_bounds__(128, 5)
   tc::tc_fence_after();
   if (warp == 0) tc::tmem_dealloc(tm, 64);
   if (tid == 0 && *abort_s) report_device_error(kErrMbarTimeout);
+  wait_first();
 }
 
 // ---- the walk over a sequence's chunks ---------------------------------------------------
@@ -588,51 +602,71 @@ __global__ void __launch_bounds__(Geo<kV>::kThreads, 1)
   const int h = (int)((blockIdx.x / kSplit) % a.H);
   int seq = (int)((blockIdx.x / kSplit) / a.H);
   const int hk = h / (a.H / a.Hk);
+  // Launched as gdn_wy_kernel's programmatic dependent: the loading warp waits for that grid where
+  // it reads what it wrote; the first block waits in any case before it leaves, so that this grid
+  // never ends before the other.
+  auto wait_first = [] {
+    if (blockIdx.x == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
+  };
   if (longest_first) {
-    // more CTAs than run at once: blocks in order of their sequences' lengths, so that the
-    // longest do not start last (block order -> the sequence of that rank; ties by index)
+    // more CTAs than run at once, or fewer than sequences (the short ones go by rows): blocks in
+    // order of their sequences' lengths, so that the longest do not start last (block order ->
+    // the sequence of that rank; ties by index)
     __shared__ int seq_s;
-    for (int s = tid; s < a.n_seq; s += kScThreads) {
-      const int mine = a.cu[s + 1] - a.cu[s];
-      int rank = 0;
-      for (int i = 0; i < a.n_seq; ++i) {
-        const int other = a.cu[i + 1] - a.cu[i];
-        rank += other > mine || (other == mine && i < s);
+    int* length = (int*)sm;  // (the buffers are not in use yet)
+    int longer = 0;          // than by_row
+    for (int i0 = 0; i0 < a.n_seq; i0 += kScThreads) {
+      const int i = i0 + tid;
+      int len = -1;  // bounds that are none come last
+      if (i < a.n_seq) {
+        const int t0 = a.cu[i], t1 = a.cu[i + 1];
+        if (good_bounds(t0, t1, a.T)) len = t1 - t0;
+        length[i] = len;
       }
+      longer += __syncthreads_count(len > a.by_row);
+    }
+    if (a.by_row >= 0 && seq >= longer) {  // the rest is gdn_recurrent_kernel's
+      wait_first();
+      return;
+    }
+    for (int s = tid; s < a.n_seq; s += kScThreads) {
+      const int mine = length[s];
+      int rank = 0;
+      for (int i = 0; i < a.n_seq; ++i) rank += length[i] > mine || (length[i] == mine && i < s);
       if (rank == seq) seq_s = s;
     }
     __syncthreads();
     seq = seq_s;
   }
-  // launched as gdn_wy_kernel's programmatic dependent: a block waits for that grid where it
-  // reads what it wrote (the loading warp), or here before it leaves, so that this grid never
-  // ends first
-  auto wait_wy = [] { asm volatile("griddepcontrol.wait;" ::: "memory"); };
   // what the device arrays cannot mean is refused: nothing is read or written for it
   int slot = seq;
   if (a.slots != nullptr) {
     slot = a.slots[seq];
     if (slot < 0) {  // padding of the batch
-      wait_wy();
+      wait_first();
       return;
     }
     bool twice = false;    // an earlier sequence has the same state
     for (int i = tid; i < seq; i += kScThreads) twice |= a.slots[i] == slot;
     if (__syncthreads_or(twice) || slot >= a.n_slots) {
       if (tid == 0) report_device_error(kErrBadIndex);
-      wait_wy();
+      wait_first();
       return;
     }
   }
   const int s0 = a.cu[seq], s1 = a.cu[seq + 1];
   const int len = s1 - s0;
+  if (len >= 0 && len <= a.by_row) {  // gdn_recurrent_kernel's
+    wait_first();
+    return;
+  }
   const int nc = (len + kC - 1) / kC;
-  const int base = s0 / kC + seq;
+  const int base = first_slot(a, seq);
   // (a slot's owner is found by bisection: where the bounds are in order it is this sequence)
   if (!good_bounds(s0, s1, a.T) ||
-      (nc > 0 && (slot_owner(a.cu, a.n_seq, base) != seq || slot_owner(a.cu, a.n_seq, base + nc - 1) != seq))) {
+      (nc > 0 && (slot_owner(a, base) != seq || slot_owner(a, base + nc - 1) != seq))) {
     if (tid == 0) report_device_error(kErrBadIndex);
-    wait_wy();
+    wait_first();
     return;
   }
   const long soff = ((long)slot * a.H + h) * kD * kD + (long)v0 * kD;  // this CTA's state rows
@@ -643,7 +677,7 @@ __global__ void __launch_bounds__(Geo<kV>::kThreads, 1)
         if (a.state_in != nullptr) w = ((const float4*)(a.state_in + soff))[e];
         ((float4*)(a.state_out + soff))[e] = w;
       }
-    wait_wy();
+    wait_first();
     return;
   }
 
@@ -680,7 +714,8 @@ __global__ void __launch_bounds__(Geo<kV>::kThreads, 1)
       tc::tma_prefetch_desc(&tmK);
       tc::tma_prefetch_desc(&tmV);
       const uint8_t* wy = ws + ((long)base * a.H + h) * kSlot;
-      wait_wy();  // the workspace; the call's inputs were there before that grid started
+      // the workspace (the call's inputs were there before that grid started)
+      asm volatile("griddepcontrol.wait;" ::: "memory");
       auto load_stage = [&](int c) {
         const int st = c % kStages;
         if (c >= kStages && !tc::mbar_wait(&empty[st], ((c / kStages) - 1) & 1, abort_s)) return false;
@@ -940,11 +975,12 @@ __global__ void __launch_bounds__(Geo<kV>::kThreads, 1)
   tc::tc_fence_after();
   if (warp == 1) tc::tmem_dealloc(tm, G::kTmCols);
   if (tid == 0 && *abort_s) report_device_error(kErrMbarTimeout);
+  wait_first();
 }
 
 template <int kV>
 cudaError_t launch_scan(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const GdnArgs& a,
-                        const uint8_t* ws, cudaStream_t s) {
+                        const uint8_t* ws, long n, cudaStream_t s) {
   const int smem = 1024 + Geo<kV>::kSmem;
   cudaError_t e = cudaFuncSetAttribute(gdn_scan_kernel<kV>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
@@ -952,26 +988,36 @@ cudaError_t launch_scan(const CUtensorMap& tq, const CUtensorMap& tk, const CUte
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((long)a.n_seq * a.H * (kD / kV)));
+  cfg.gridDim = dim3((unsigned)(n * a.H * (kD / kV)));
   cfg.blockDim = dim3(Geo<kV>::kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  // (512 sequences: the ranks cost 2 us)
-  const bool longest_first = (long)cfg.gridDim.x > num_sms() && a.n_seq > 1 && a.n_seq <= 512;
+  const bool longest_first = n < a.n_seq || ((long)cfg.gridDim.x > num_sms() && n > 1 && n <= kGdnRankedSeqs);
   return cudaLaunchKernelEx(&cfg, gdn_scan_kernel<kV>, tq, tk, tv, a, ws, longest_first);
 }
 
 }  // namespace
 
-// Chunk slots of T tokens in n sequences (see slot_owner).
-static long gdn_slots(int T, int n_seq) { return (long)T / kC + n_seq; }
+// Chunk slots of T tokens in n sequences (see first_slot).
+static bool gdn_half_slots(int T, int n_seq, int by_row) {
+  return by_row >= kC / 2 - 1 && T / (kC / 2) + 1L < T / kC + (long)n_seq;
+}
+static long gdn_slots(int T, int n_seq, int by_row) {
+  return gdn_half_slots(T, n_seq, by_row) ? T / (kC / 2) + 1L : T / kC + (long)n_seq;
+}
 
-size_t gdn_chunk_workspace(int T, int n_seq, int H) { return (size_t)gdn_slots(T, n_seq) * H * kSlot; }
+size_t gdn_chunk_workspace(int T, int n_seq, int H, int by_row) {
+  return (size_t)gdn_slots(T, n_seq, by_row) * H * kSlot;
+}
 
-cudaError_t launch_gdn_chunk(const GdnArgs& a, void* ws, cudaStream_t s) {
-  const long wy = gdn_slots(a.T, a.n_seq) * a.H, pairs = (long)a.n_seq * a.H;
+cudaError_t launch_gdn_chunk(const GdnArgs& in, void* ws, cudaStream_t s) {
+  GdnArgs a = in;
+  a.half_slots = gdn_half_slots(a.T, a.n_seq, a.by_row);
+  // sequences that can be the chunks': all, or as many as fit T with more than by_row tokens
+  const long n = a.by_row < 0 ? a.n_seq : min((long)a.n_seq, (long)a.T / (a.by_row + 1));
+  const long wy = gdn_slots(a.T, a.n_seq, a.by_row) * a.H, pairs = n * a.H;
   if (wy >= (1L << 31) || pairs * 2 >= (1L << 31)) return cudaErrorNotSupported;
   const long rowk = (long)a.Hk * kD, rowv = (long)a.H * kD;
   CUtensorMap tq, tk, tq16, tk16, tv;
@@ -984,13 +1030,24 @@ cudaError_t launch_gdn_chunk(const GdnArgs& a, void* ws, cudaStream_t s) {
   const int wsm = 1024 + kWySmem;
   e = cudaFuncSetAttribute(gdn_wy_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, wsm);
   if (e != cudaSuccess) return e;
-  gdn_wy_kernel<<<(unsigned)wy, 128, wsm, s>>>(tq, tk, a, (uint8_t*)ws);
-  e = cudaGetLastError();
+  if (a.by_row >= 0) e = launch_gdn_recurrent(a, s);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)wy);
+  cfg.blockDim = dim3(128);
+  cfg.dynamicSmemBytes = wsm;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = a.by_row >= 0 ? 1 : 0;
+  e = cudaLaunchKernelEx(&cfg, gdn_wy_kernel, tq, tk, a, (uint8_t*)ws);
   if (e != cudaSuccess) return e;
   // the value columns go to as many CTAs as all run at once: each chunk's steps get shorter
-  if (pairs * 8 <= num_sms()) return launch_scan<16>(tq16, tk16, tv, a, (const uint8_t*)ws, s);
-  if (pairs * 4 <= num_sms()) return launch_scan<32>(tq16, tk16, tv, a, (const uint8_t*)ws, s);
-  return launch_scan<64>(tq16, tk16, tv, a, (const uint8_t*)ws, s);
+  if (pairs * 8 <= num_sms()) return launch_scan<16>(tq16, tk16, tv, a, (const uint8_t*)ws, n, s);
+  if (pairs * 4 <= num_sms()) return launch_scan<32>(tq16, tk16, tv, a, (const uint8_t*)ws, n, s);
+  return launch_scan<64>(tq16, tk16, tv, a, (const uint8_t*)ws, n, s);
 }
 
 }  // namespace hla

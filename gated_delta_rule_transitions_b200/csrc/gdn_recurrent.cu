@@ -123,6 +123,7 @@ __global__ void __launch_bounds__(kThreads) gdn_recurrent_kernel(GdnArgs a) {
     if (tid == 0) report_device_error(kErrBadIndex);
     return;
   }
+  if (!kOne && t1 - t0 > a.by_row) return;  // gdn_scan_kernel's
 
   const Tio* kin = (const Tio*)a.k + ((long)t0 * a.Hk + hk) * D;
   const Tio* qin = (const Tio*)a.q + ((long)t0 * a.Hk + hk) * D;

@@ -1,5 +1,6 @@
 // C ABI of libhla: argument checks, workspace and cache layout, launch sequence.
 // Every entry point validates on the host first and launches nothing on error.
+#include <climits>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -752,15 +753,28 @@ static hla_status check_gdn(const gdn_config* c) {
   return HLA_OK;
 }
 
-// Chunks of 64 tokens on the tensor cores, or token by token: by the mean length, which is
-// what the host knows of the lengths.  The two meet between 36 and 56 tokens a sequence.
-static bool gdn_by_chunks(const gdn_config* c, int32_t T) {
-  return c->dtype == HLA_BF16 && c->dk == 128 && c->decay_mode == HLA_DECAY_SCALAR && T >= 40 * (int64_t)c->n_seq;
+// Token by token, by chunks of 64 tokens on the tensor cores, or each sequence by its length.
+// The host knows T and n_seq alone.  Where all sequences were alike, rows and chunks would meet
+// at some 36 tokens (16 heads: 16 sequences at 36 to 56, 64 at 37).  They seldom are: one prompt
+// among single tokens holds up rows for as long as it is, and single tokens in chunks cost a
+// chunk each.  So the kernels share the batch wherever that can pay.  Measured, 16 heads:
+// 127 x 1 + 2048 tokens 803 us by rows, 175 shared; 60 x 1 + 4 x 1000 tokens 226 by chunks, 127
+// shared.  What it costs a batch that is all alike: 64 x 30 tokens 132 by rows, 145 shared; 64 x
+// 49 tokens 165 by chunks, 175 shared.  From 128 tokens in the mean up, short sequences' chunks
+// are few beside the others' (128 x 200 tokens: 734 us by chunks, 763 shared).
+constexpr int kGdnByRow = 36;
+static bool gdn_uses_chunks(const gdn_config* c, int32_t T) {
+  if (c->dtype != HLA_BF16 || c->dk != 128 || c->decay_mode != HLA_DECAY_SCALAR) return false;
+  return T >= 40 * (int64_t)c->n_seq || (c->n_seq <= hla::kGdnRankedSeqs && T - c->n_seq >= 128);
+}
+// With chunks in use: the longest sequence that goes by rows all the same.
+static int gdn_by_row(const gdn_config* c, int32_t T) {
+  return c->n_seq > hla::kGdnRankedSeqs || T >= 128 * (int64_t)c->n_seq ? -1 : kGdnByRow;
 }
 
 size_t gdn_workspace_bytes(const gdn_config* cfg, int32_t T) {
   if (check_gdn(cfg) != HLA_OK || T <= 0) return 0;
-  return gdn_by_chunks(cfg, T) ? align256(hla::gdn_chunk_workspace(T, cfg->n_seq, cfg->H)) : 256;
+  return gdn_uses_chunks(cfg, T) ? align256(hla::gdn_chunk_workspace(T, cfg->n_seq, cfg->H, gdn_by_row(cfg, T))) : 256;
 }
 
 static hla_status gdn_run(const gdn_config* cfg, const void* q, const void* k, const void* v, const float* alpha,
@@ -796,10 +810,13 @@ static hla_status gdn_run(const gdn_config* cfg, const void* q, const void* k, c
   a.state_in = state_in;
   a.state_out = state_out;
   a.o = o;
-  if (ws != nullptr && gdn_by_chunks(cfg, T))
+  a.by_row = gdn_by_row(cfg, T);
+  if (ws != nullptr && gdn_uses_chunks(cfg, T)) {
     HLA_CUDA(hla::launch_gdn_chunk(a, ws, s), "gated delta rule (chunks) launch");
-  else
+  } else {
+    a.by_row = INT_MAX;
     HLA_CUDA(hla::launch_gdn_recurrent(a, s), "gated delta rule launch");
+  }
   return HLA_OK;
 }
 

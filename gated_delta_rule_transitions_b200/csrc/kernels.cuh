@@ -234,6 +234,7 @@ struct EvictArgs {
 };
 
 // The gated delta rule with a carried state (float32 [n_slots,H,d,d], [v][k]).
+constexpr int kGdnRankedSeqs = 512;  // sequences that gdn_scan_kernel's blocks rank by length (512: 2 us)
 struct GdnArgs {
   int n_seq, Hk, H, d, dtype, alpha_vec, n_slots, T;
   const void* q;          // [T,Hk,d]
@@ -246,6 +247,8 @@ struct GdnArgs {
   const float* state_in;  // or null (zero)
   float* state_out;       // or null
   void* o;                // [T,H,d]
+  int by_row;             // sequences of at most so many tokens go token by token, the others by chunks
+  int half_slots;         // numbering of the chunk slots (gdn_chunk.cu)
 };
 
 cudaError_t launch_pools(const void* x0, const void* x1, float* r0, float* r1, int B, int T, int H, int d,
@@ -291,7 +294,7 @@ cudaError_t launch_gate_mass(const float* gates, int B, int H, int N, int ncols,
 cudaError_t launch_evict(const EvictArgs& a, cudaStream_t s);
 cudaError_t launch_cache8(const Cache8Args& a, bool close, cudaStream_t s);
 cudaError_t launch_gdn_recurrent(const GdnArgs& a, cudaStream_t s);
-size_t gdn_chunk_workspace(int T, int n_seq, int H);
+size_t gdn_chunk_workspace(int T, int n_seq, int H, int by_row);
 cudaError_t launch_gdn_chunk(const GdnArgs& a, void* ws, cudaStream_t s);
 cudaError_t read_error_word_gdn_chunk(unsigned int* out, bool clear);
 cudaError_t read_error_word_gdn_recurrent(unsigned int* out, bool clear);

@@ -5,11 +5,11 @@ Tolerances.  Every token's update of a state row is a float32 dot product of d t
 rank-one correction: with d / 8 terms in sequence and a handful of operations more it is off
 by less than (d / 8 + 8) 2^-24 of the row's size, and the rule contracts what it carries, so
 T tokens add up to at most min(T, 64) such errors (alpha averages 0.95: an error's weight
-after 64 tokens is below 4 %).  The tensor-core form (bf16, d = 128) holds each factor of its
-products as two bf16 numbers: each product is off by at most 2 x 2^-17 relative, at most six
-products stand between a state and the next, which makes 12 x 2^-17 = 9.2e-5 as the bound for
-one chunk if every error pointed the same way; rounding errors of independent elements add as
-their root, so 2e-5 is asked for.  An output is rounded once to its type on top."""
+after 64 tokens is below 4 %).  For the tensor-core form (bf16, d = 128) 2e-5 is asked for:
+with each factor of its products as two bf16 numbers, each product is off by at most 2 x 2^-17
+relative, at most six products stand between a state and the next, which makes 12 x 2^-17 =
+9.2e-5 for one chunk if every error pointed the same way, and rounding errors of independent
+elements add as their root (the kernels take three parts).  An output is rounded once to its type on top."""
 import pytest
 import torch
 
@@ -310,6 +310,76 @@ def test_many_sequences_of_mixed_lengths(hla, n, H, Hk):
         assert torch.equal(o[int(cu[i]):int(cu[i + 1])], torch.full_like(o[int(cu[i]):int(cu[i + 1])], 7.0))
     st, code = hla.hla_device_status()
     assert code == (16 if n > 10 else 0)
+
+
+MIXED = [[1] * 40 + [300], [1] * 31 + [200, 0, 65], [36, 37, 32, 33, 64, 65, 1, 128, 0, 31, 97, 38],
+         [40] * 12, [30] * 20, [700] + [2] * 70, [1] * 511 + [129], [1] * 512 + [30000 // 16], [5, 400] * 9]
+
+
+@pytest.mark.parametrize("lens", MIXED, ids=lambda x: f"{len(x)}x{max(x)}")
+def test_prompts_among_short_sequences(hla, lens):
+    """Batches that rows and chunks share: a prompt among single tokens, lengths on either side
+    of the kernels' border, all short, all long, as many sequences as are ranked and one more;
+    two calls and a step between them in place on one workspace, the second call replayed."""
+    gen = torch.Generator().manual_seed(len(lens))
+    n, T, d = len(lens), sum(lens), 128
+    H, Hk = (4, 2) if n < 100 else (1, 1)
+    cfg = hla.make_gdn_config(n, H, d, "bf16", Hk=Hk)
+    cu = torch.tensor([0] + lens).cumsum(0).to(torch.int32)
+    S0 = torch.randn(n, H, d, d, generator=gen)
+    parts = [R.tokens(gen, T, Hk, H, d, R.BF16), R.tokens(gen, n, Hk, H, d, R.BF16), R.tokens(gen, T, Hk, H, d, R.BF16)]
+    dev, S = [cuda(*p) for p in parts], S0.cuda()
+    outs = [torch.full((p[2].shape[0] + 3, H, d), 7.0, dtype=R.BF16, device="cuda") for p in parts]
+    cud, ws = cu.cuda(), torch.empty(hla.gdn_workspace_bytes(cfg, T), dtype=torch.uint8, device="cuda")
+    fwd = lambda i: hla.gdn_forward(cfg, *dev[i], cud, outs[i][:T], state_in=S, state_out=S, workspace=ws)
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        fwd(0)
+        S.copy_(S0)
+    torch.cuda.current_stream().wait_stream(side)
+    with torch.cuda.graph(graph):
+        fwd(2)
+    fwd(0)
+    hla.gdn_step(cfg, *dev[1], S, outs[1][:n])
+    graph.replay()
+    torch.cuda.synchronize()
+    assert hla.hla_device_status() == (0, 0)
+    bounds = [(int(cu[i]), int(cu[i + 1])) for i in range(n)]
+    ref = S0
+    for p, o, b in zip(parts, outs, (bounds, [(i, i + 1) for i in range(n)], bounds)):
+        ro, ref = R.gdn_reference(*p, b, ref)
+        o = o.cpu()
+        for i, (a, e) in enumerate(b):
+            if e > a:
+                assert R.rel(o[a:e], ro[a:e]) <= 2 * state_tol(max(lens), d, R.BF16, True) + R.half_step(R.BF16), i
+        assert torch.equal(o[b[-1][1]:], torch.full_like(o[b[-1][1]:], 7.0))
+    tol = 3 * state_tol(max(lens), d, R.BF16, True)
+    for i in range(n):
+        assert R.rel(S[i].cpu(), ref[i]) <= tol, i
+
+
+def test_bad_bounds_in_a_shared_batch(hla):
+    """Bounds that run backwards or leave the tokens among prompts and single tokens: their
+    sequences are left out and reported, the others are worked on."""
+    gen = torch.Generator().manual_seed(9)
+    T, H, d = 400, 2, 128
+    cu = torch.tensor([0, 1, 101, 102, 99, 140, 240, 241, 2 ** 30, 2 ** 30 + 50, 300, 301], dtype=torch.int32)
+    n = len(cu) - 1
+    q, k, v, al, be = R.tokens(gen, T, H, H, d, R.BF16)
+    S0 = torch.randn(n, H, d, d, generator=gen)
+    S, o = S0.cuda(), torch.full((T, H, d), 7.0, dtype=R.BF16, device="cuda")
+    hla.gdn_forward(hla.make_gdn_config(n, H, d, "bf16"), *cuda(q, k, v, al, be, cu), o, state_in=S, state_out=S)
+    st, code = hla.hla_device_status()
+    assert st == hla.HLA_ERR_INVALID_ARG and code == 16
+    S = S.cpu()
+    for i in (0, 1, 5, 6, 10):
+        a, e = int(cu[i]), int(cu[i + 1])
+        ro, rS = R.gdn_reference(q, k, v, al, be, [(a, e)], S0[i:i + 1])
+        assert R.rel(S[i], rS[0]) <= state_tol(100, d, R.BF16, True), i
+    for i in (3, 7, 8, 9):
+        assert torch.equal(S[i], S0[i])
+    assert torch.equal(o[301:].cpu(), torch.full((99, H, d), 7.0, dtype=R.BF16))
 
 
 def test_agrees_with_the_gated_composition_of_weight_one(hla):
