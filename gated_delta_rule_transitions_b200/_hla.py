@@ -229,6 +229,10 @@ class CacheSlice:
         self.parent = None
         self.max_chunks = 0
 
+    @property
+    def device_index(self):
+        return self.parent.device_index
+
 
 class Cache:
     """A decode cache: one caller-owned device block plus the C struct of views."""
@@ -284,11 +288,15 @@ class Cache:
         self.max_chunks = max_chunks
         return self
 
+    @property
+    def device_index(self):
+        return (self.mem if self.mem is not None else self.buffers["rk"]).get_device()
+
     def track_mass(self, mass=None, stream=None):
         """Accumulate every closed chunk's gate weight from now on; returns the
         [B, H, max_chunks] float32 tensor that holds it (given or made here, zeroed)."""
         s = self.struct
-        device = (self.mem if self.mem is not None else self.buffers["rk"]).get_device()
+        device = self.device_index
         shape = (s.B, s.H, s.max_chunks)
         if mass is None:
             mass = torch.empty(shape, dtype=torch.float32, device=torch.device("cuda", device))
@@ -349,6 +357,9 @@ def hla_cache_evict(cfg, src, dst, keep, recent, kept_out, stream=None):
     """Keep per (sequence, head) the `recent` last chunks of `src` and the heaviest others,
     `keep` in all; `dst` is `src` (in place) or another cache."""
     dev = _device(kept_out, "kept_out")
+    for name, c in (("src", src), ("dst", dst)):
+        if c.device_index != dev:
+            raise ValueError(f"{name} is on cuda:{c.device_index}, kept_out on cuda:{dev}")
     p = _arg(kept_out, "kept_out", torch.int32, cfg.B * cfg.H * keep, dev)
     _run(dev, stream, lib().hla_cache_evict, ctypes.byref(cfg), ctypes.byref(src.struct),
          ctypes.byref(dst.struct), keep, recent, p)
@@ -381,9 +392,9 @@ def gdn_forward(cfg: GdnConfig, q, k, v, alpha, beta, cu_seqlens, o, state_in=No
     pq, pk, pv, pa, pb, po = _gdn_args(cfg, T, dev, q, k, v, alpha, beta, o)
     ns = cfg.n_slots * cfg.H * cfg.dv * cfg.dk
     if workspace is None:
-        workspace = torch.empty(max(gdn_workspace_bytes(cfg, T), 256), dtype=torch.uint8, device=q.device)
-        if stream is not None:
-            workspace.record_stream(stream)
+        # (torch hands memory out in the order of the stream it is asked on)
+        with torch.cuda.stream(stream):
+            workspace = torch.empty(max(gdn_workspace_bytes(cfg, T), 256), dtype=torch.uint8, device=q.device)
     nb = workspace.numel() * workspace.element_size()
     _run(dev, stream, lib().gdn_forward, ctypes.byref(cfg), pq, pk, pv, pa, pb,
          _arg(cu_seqlens, "cu_seqlens", torch.int32, cfg.n_seq + 1, dev), T,

@@ -317,9 +317,11 @@ hla_status hla_cache_evict(const hla_config* cfg, const hla_cache* src, hla_cach
  * or sequence bounds that fall or leave [0, T] leave that sequence out too and record code
  * 0x10, reported by hla_device_status.  Keys are meant to be of length one or less with
  * beta in [0, 1], as in the token rule above; o must not overlap the inputs.
- * bf16 with d = 128, the scalar decay and at least 40 tokens a sequence in the mean run by
- * chunks of 64 tokens on the tensor cores, with the state and everything that reaches it
- * held to float32's precision; the others run the rule token by token on CUDA cores.
+ * bf16 with d = 128 and the scalar decay runs long sequences by chunks of 64 tokens on the
+ * tensor cores, with the state and everything that reaches it held to float32's precision;
+ * short ones and the others run the rule token by token on CUDA cores.  A NaN or an infinity
+ * among a sequence's tokens makes its state and outputs undefined from 63 tokens before it
+ * on; other sequences, and rows of no sequence, are never mixed in.
  * Calls are deterministic.  Those whose kernels may overlap in time (other streams, two
  * graphs) need workspaces and states of their own.
  */
@@ -339,8 +341,9 @@ size_t gdn_workspace_bytes(const gdn_config* cfg, int32_t T);
 /*
  * gdn_forward -- ragged sequences of any length through the rule, states in and out.
  * In:  q, k [T,Hk,d], v [T,H,d] dtype; alpha [T,H] (CHANNEL: [T,H,d]) and beta [T,H]
- *      float32, alpha in [0,1] (these two, where scalar, only 4-byte aligned); cu_seqlens [n_seq + 1] int32 (device): sequence i is rows
- *      cu_seqlens[i] .. cu_seqlens[i+1] - 1 (an empty one passes its state on);
+ *      float32, alpha in [0,1] (these two, where scalar, only 4-byte aligned); cu_seqlens
+ *      [n_seq + 1] int32 (device): sequence i is rows cu_seqlens[i] .. cu_seqlens[i+1] - 1
+ *      (an empty one passes its state on);
  *      slots [n_seq] int32 (device) or NULL; state_in or NULL (zero states).
  * Out: o [T,H,d] dtype (rows of no sequence are left as they were); state_out or NULL.
  *      state_out may be state_in; otherwise the two must not overlap.

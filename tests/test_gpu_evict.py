@@ -214,3 +214,15 @@ def test_prefill_evict_decode_together(hla, fmt):
         # float32 arithmetic on the stored values: the output's own rounding is what shows
         assert R.rel(out.cpu(), ref) <= 2.0 ** -8 + 1e-4
     assert hla.hla_device_status() == (0, 0)
+
+
+def test_caches_on_another_device_are_refused(hla):
+    import types
+    c = hla.make_config(1, 1, 1, 64, 64, "f32")
+    cache = hla.Cache(c, 2)
+    cache.track_mass()
+    away = types.SimpleNamespace(device_index=1, struct=cache.struct)
+    kept = torch.empty(1, dtype=torch.int32, device="cuda:0")
+    for src, dst, name in ((away, cache, "src"), (cache, away, "dst")):
+        with pytest.raises(ValueError, match=name):
+            hla.hla_cache_evict(c, src, dst, 1, 0, kept)

@@ -382,6 +382,33 @@ def test_bad_bounds_in_a_shared_batch(hla):
     assert torch.equal(o[301:].cpu(), torch.full((99, H, d), 7.0, dtype=R.BF16))
 
 
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("f32", 64)])
+@pytest.mark.parametrize("lens", [[100, 70, 200], [3, 1, 300, 1, 40, 5, 90, 36]], ids=str)
+def test_nan_of_one_sequence_stays_there(hla, lens, dtype, d):
+    """Tokens and state of every other sequence are NaN: the rest does not see them, though
+    tiles of 64 tokens reach over a sequence's end."""
+    gen, dt, H = torch.Generator().manual_seed(3), R.DT[dtype], 2
+    n, T = len(lens), sum(lens)
+    cu = torch.tensor([0] + lens).cumsum(0).to(torch.int32)
+    x = R.tokens(gen, T, H, H, d, dt)
+    S0 = torch.randn(n, H, d, d, generator=gen)
+    for i in range(1, n, 2):
+        for t in x:
+            t[int(cu[i]):int(cu[i + 1])] = float("nan")
+        S0[i] = float("nan")
+    S, o = S0.cuda(), torch.empty(T, H, d, dtype=dt, device="cuda")
+    hla.gdn_forward(hla.make_gdn_config(n, H, d, dtype), *cuda(*x, cu), o, state_in=S, state_out=S)
+    assert hla.hla_device_status() == (0, 0)
+    tol = state_tol(max(lens), d, dt, dtype == "bf16" and d == 128)
+    for i in range(n):
+        a, e = int(cu[i]), int(cu[i + 1])
+        if i % 2:
+            assert bool(S[i].isnan().all()) and bool(o[a:e].isnan().all())
+        else:
+            ro, rS = R.gdn_reference(*x, [(a, e)], S0[i:i + 1])
+            assert R.rel(S[i].cpu(), rS[0]) <= tol and R.rel(o[a:e].cpu(), ro[a:e]) <= tol + R.half_step(dt)
+
+
 def test_agrees_with_the_gated_composition_of_weight_one(hla):
     """HLA with every gate one is the rule itself: the prompt's outputs by gdn_forward and by
     hla_prefill, then tokens by gdn_step from the state and by hla_decode_step over the cached
