@@ -18,9 +18,10 @@
 // decode_stream8_kernel (bf16, d = 128; after decode_gates_kernel): one CTA per (sequence,
 // head), two per SM.  The three digit vectors are three columns of one right factor on the
 // tensor cores (warp-level 16 x 8 x 32); the matrices go there from shared memory as they lie,
-// 16 ldmatrix a warp and chunk, nothing is converted.  (As dp4a the products took 880 cycles
-// a chunk, as they are 300; 64 sequences x 16 heads x 512 chunks: 2.60 and 2.52 ms, 1.05 of
-// the measured copy rate; 8 x 16 heads with 90 active chunks: 144 and 100 us.)  A unit of the
+// 16 ldmatrix a warp and chunk, nothing is converted.  (As dp4a a chunk took 1,410
+// cycles, 880 of them the products, as they are some 1,100; 64 sequences x 16 heads x 512
+// chunks: 2.60 and 2.55 ms, 1.04 of the measured copy rate; 8 x 16 heads with some 90 active
+// chunks: 144 and 97 us.  A ring of six units, or x and y on four warps each: no faster.)  A unit of the
 // ring is one chunk: 16 KiB of QA, 16 KiB of QB (128 rows of 128 bytes, one 128-byte-swizzled
 // box each) and its four scales.  Warp w has rows 32 w .. + 31 of both; lane l owns row
 // 32 w + l / 4 + 8 (l % 4) of the vectors.
