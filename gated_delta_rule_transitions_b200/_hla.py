@@ -174,10 +174,13 @@ def _arg(t, name, dtype, numel, device):
     `device` (None stays None)."""
     if t is None:
         return None
-    # the checks in one expression first: a step's binding is most of its time
-    if (isinstance(t, torch.Tensor) and t.is_cuda and t.get_device() == device and t.dtype is dtype
-            and t.numel() == numel and t.is_contiguous()):
-        return t.data_ptr()
+    # the checks in one expression first: a step's binding is most of its time (8 arguments, a
+    # launch of 3.5 us: 9.9 us in all with a check of the type and a Stream object, 7.8 without)
+    try:
+        if t.get_device() == device and t.dtype is dtype and t.numel() == numel and t.is_contiguous():
+            return t.data_ptr()  # (a CPU tensor's device is -1)
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor")
     if not t.is_cuda:
@@ -200,11 +203,16 @@ def _device(t, name):
     return t.get_device()
 
 
+# handle of a device's current stream: without a Stream object where torch offers that
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
 def _run(device, stream, fn, *args):
     """Call fn(*args, stream) with CUDA device number `device` current, on its current stream
     by default."""
     if stream is None:
-        s = torch.cuda.current_stream(device).cuda_stream
+        s = _raw_stream(device)
     elif stream.device.index != device:
         raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{device}")
     else:
