@@ -16,8 +16,8 @@
 //                      the chunk and takes the kept chunks in ascending order; entry i comes
 //                      from a chunk kept[i] >= i, and reads run ahead of writes, so the move
 //                      is safe in place without any barrier.
-// The move is bound by HBM: 16 sequences x 16 heads, 384 of 512 chunks kept, 13.0 GB in 2.01 ms,
-// 0.98 of the measured copy rate; one sequence of 29 chunks 16 us, two launches' latency.
+// The move is bound by HBM: 16 sequences x 16 heads, 384 of 512 chunks kept, 13.0 GB in 1.97 ms,
+// 1.0 of the measured copy rate; one sequence of 29 chunks 14.5 us, two launches' latency.
 #include <cooperative_groups.h>
 
 #include "common.cuh"
@@ -220,7 +220,9 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictArgs a) 
 // ---- moving ---------------------------------------------------------------------------
 
 constexpr int kMoveThreads = 128;
-constexpr int kMoveBatch = 8;
+// Chunks in flight per thread (8, 10, 12, 16: 16 sequences x 16 heads, 384 of 512 kept, 2012, 1995,
+// 1971, 1980 us; one sequence, 21 of 29, 15.7, 14.3, 14.5, 18.3).
+constexpr int kMoveBatch = 12;
 
 // One 16-byte column of one array, over the kept chunks [i0, i1) in ascending order.
 __device__ __forceinline__ void move_column(const uint4* src, uint4* dst, long pitch, const int32_t* kept, int i0,
