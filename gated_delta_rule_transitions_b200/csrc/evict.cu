@@ -49,8 +49,8 @@ __global__ void __launch_bounds__(32 * kMassWarps) gate_mass_kernel(
   __shared__ __align__(16) float part[kMassWarps][kCols];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int tiles = (ncols + kCols - 1) / kCols;
-  const long bh = blockIdx.x / ctas / tiles;
-  const int j0 = (int)(blockIdx.x / ctas % tiles) * kCols;
+  const long heads = gridDim.x / ctas / tiles, bh = blockIdx.x / ctas % heads;
+  const int j0 = (int)(blockIdx.x / ctas / heads) * kCols;  // (tiles of many rows start first)
   const float* G = gates + bh * (long)N * N + j0 + kVec * lane;
   float acc[kQ][kVec] = {};
   // rows i > j hold a weight on chunk j; row i stands for the tokens of chunk i
@@ -66,20 +66,33 @@ __global__ void __launch_bounds__(32 * kMassWarps) gate_mass_kernel(
           if (thr <= 0.0f || g >= thr) acc[q][v] = fmaf(wt, g, acc[q][v]);
         }
   }
-#pragma unroll(kVec == 4 ? 8 : 4)
-  for (; i < N; i += step) {  // below it every column of the tile counts (j0 + kCols <= i < N)
-    const float wt = (float)min(C, T - i * C);
+  // below it every column of the tile counts (j0 + kCols <= i < N): kRows rows in flight (32 heads
+  // of 2048 chunks: 2, 4, 6, 8 rows 55, 51, 58, 76 us; left to the compiler's unrolling 57)
+  constexpr int kRows = 4;
+  for (; i < N; i += kRows * step) {
+    float g[kRows][kQ][kVec];
 #pragma unroll
-    for (int q = 0; q < kQ; ++q) {
-      float g[kVec];
-      if constexpr (kVec == 4) {
-        const float4 f = __ldg((const float4*)(G + (long)i * N + 128 * q));
-        g[0] = f.x, g[1] = f.y, g[2] = f.z, g[3] = f.w;
-      } else {
-        g[0] = __ldg(G + (long)i * N + 32 * q);
+    for (int r = 0; r < kRows; ++r)
+#pragma unroll
+      for (int q = 0; q < kQ; ++q) {
+        const float* p = G + (long)(i + r * step) * N + 32 * kVec * q;
+        if (i + r * step >= N) break;
+        if constexpr (kVec == 4) {
+          const float4 f = __ldg((const float4*)p);
+          g[r][q][0] = f.x, g[r][q][1] = f.y, g[r][q][2] = f.z, g[r][q][3] = f.w;
+        } else {
+          g[r][q][0] = __ldg(p);
+        }
       }
 #pragma unroll
-      for (int v = 0; v < kVec; ++v) acc[q][v] = fmaf(wt, thr <= 0.0f || g[v] >= thr ? g[v] : 0.0f, acc[q][v]);
+    for (int r = 0; r < kRows; ++r) {
+      const int t = i + r * step;
+      const float wt = (float)min(C, T - t * C);
+#pragma unroll
+      for (int q = 0; q < kQ; ++q)
+#pragma unroll
+        for (int v = 0; v < kVec; ++v)
+          if (t < N && (thr <= 0.0f || g[r][q][v] >= thr)) acc[q][v] = fmaf(wt, g[r][q][v], acc[q][v]);
     }
   }
 #pragma unroll
@@ -303,12 +316,12 @@ cudaError_t launch_gate_mass(const float* gates, int B, int H, int N, int ncols,
   const long BH = (long)B * H;
   auto tiles = [&](int cols) { return BH * ((ncols + cols - 1) / cols); };
   // Wide tiles while eight CTAs each reach every SM, else narrow ones; CTAs per tile until they
-  // fill the GPU and a warp has at most 32 rows.  (32 heads of 2048 chunks: 58 us with eight
-  // CTAs, 63 with four, 77 with two, 137 with one; 256 heads of 512: 49, 41, 43, 48; 1024 heads
-  // of 64: 37, 21, 14, 12.)
+  // fill the GPU and a warp has at most 64 rows.  (32 heads of 2048 chunks: 49 us with four CTAs,
+  // 58 with eight; 256 heads of 512: 35.9 with one, 37.4 with two; 64 heads of 512: 10.3 with
+  // four, 14.4 with eight.)
   const int cols = tiles(256) * 8 >= num_sms() ? 256 : 32;
   int ctas = 1;
-  while (ctas < 8 && (tiles(cols) * ctas < 4L * num_sms() || N > 32 * kMassWarps * ctas)) ctas *= 2;
+  while (ctas < 8 && (tiles(cols) * ctas < 2L * num_sms() || N > 64 * kMassWarps * ctas)) ctas *= 2;
   const long blocks = tiles(cols) * ctas;
   if (blocks <= 0) return cudaSuccess;
   if (blocks >= (1L << 31)) return cudaErrorNotSupported;
