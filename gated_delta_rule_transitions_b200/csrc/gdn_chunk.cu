@@ -15,16 +15,17 @@
 //
 // What bounds it: the scan's chain of a chunk, 3,030 cycles with 16 columns and 6,000 with 64
 // (there shared memory's bandwidth as well); the tensor cores are active 16 % of the time.
-// Measured, 16 heads: 16384 tokens of one sequence 499 us (T and G 88, the scan 400), four
-// sequences of 4096 tokens 303 us (88 and 210).
+// Measured, 16 heads: 16384 tokens of one sequence 524 us, four sequences of 4096 tokens 314 us.
 //
 // Precision.  The state is float32 and stays so: it is held in registers, and what goes into
 // a product (S, R, U, T) goes in as three bf16 numbers, x = x1 + x2 + x3, each the eight bits
 // after the one before: exactly x (two would leave 2^-16 of it out, more than float32 sums
 // do).  K, Q and V are bf16 already.  Left out are the products of parts that are 2^-22 and
-// less.  G, which reaches the bf16 output and nothing else, is made of factors rounded to
-// tf32 (2^-12, an eighth of the output's own rounding) and goes in as two parts.  Decays are
-// differences of 64-bit running sums.
+// less.  T and G are made of products of two tf32 numbers a factor (off by 2^-20).  G goes in as
+// three parts too, and the output sums all three of S: made of single tf32 factors, in two parts
+// each, it was off by 2^-12 before its own rounding and by 8e-4 of its size after it.  Decays are
+// differences of 64-bit running sums of float32 logarithms: log alpha is off by 2^-24 of itself,
+// so a decay e^l by at most |l| e^l 2^-24 < 2^-25.
 #include "common.cuh"
 #include "kernels.cuh"
 #include "tc_common.cuh"
@@ -41,7 +42,7 @@ namespace {
 constexpr int kD = 128;
 constexpr int kC = 64;
 constexpr int kTile = kC * 128;               // 8 KiB: 64 rows of 128 bytes, 128-byte swizzle
-constexpr int kWy = 5 * kTile;                // [T1; G1], [T2; G2], T3 of a chunk, as they lie in shared memory
+constexpr int kWy = 6 * kTile;                // [T1; G1], [T2; G2], [T3; G3] of a chunk, as they lie in shared memory
 constexpr int kScal = 2 * kC * 4;             // gamma_t, gamma_C / gamma_t
 constexpr int kSlot = kWy + kScal;            // workspace bytes per (chunk slot, head)
 
@@ -122,12 +123,6 @@ __device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
 }
 
-__device__ __forceinline__ uint32_t tf32(float x) {
-  uint32_t r;
-  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(x));
-  return r;
-}
-
 // x as two tf32 numbers, cut (the instruction does not read the last 13 bits): off by 2^-21.
 __device__ __forceinline__ void cut_tf32(float x, uint32_t& h, uint32_t& l) {
   h = __float_as_uint(x) & 0xFFFFE000u;
@@ -135,8 +130,8 @@ __device__ __forceinline__ void cut_tf32(float x, uint32_t& h, uint32_t& l) {
 }
 
 // acc[j] += A (16 x 16) B (16 x 8 kN)'s column tile j, float32 in shared memory (row pitches
-// pa, pb); kExact: of two tf32 numbers each, else of one (rounded: off by 2^-12).
-template <int kN, bool kExact>
+// pa, pb), of two tf32 numbers a factor.
+template <int kN>
 __device__ __forceinline__ void block16(float (&acc)[kN][4], const float* A, int pa, const float* B, int pb,
                                         int lane) {
   const int g = lane >> 2, q = lane & 3;
@@ -147,24 +142,16 @@ __device__ __forceinline__ void block16(float (&acc)[kN][4], const float* A, int
     uint32_t ah[4], al[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      if (kExact)
-        cut_tf32(a[i], ah[i], al[i]);
-      else
-        ah[i] = tf32(a[i]);
+      cut_tf32(a[i], ah[i], al[i]);
 #pragma unroll
     for (int j = 0; j < kN; ++j) {
       const float b[2] = {B[(k0 + q) * pb + 8 * j + g], B[(k0 + q + 4) * pb + 8 * j + g]};
       uint32_t bh[2], bl[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i)
-        if (kExact)
-          cut_tf32(b[i], bh[i], bl[i]);
-        else
-          bh[i] = tf32(b[i]);
-      if (kExact) {
-        mma_tf32(acc[j], ah, bl);
-        mma_tf32(acc[j], al, bh);
-      }
+        cut_tf32(b[i], bh[i], bl[i]);
+      mma_tf32(acc[j], ah, bl);
+      mma_tf32(acc[j], al, bh);
       mma_tf32(acc[j], ah, bh);
     }
   }
@@ -363,7 +350,7 @@ __global__ void __launch_bounds__(128, 5)
     const int kb = blk - (ib * (ib - 1)) / 2;
     float acc[1][4] = {};
     float* at = Ls + 16 * ib * kP + 16 * kb + 8 * nh;
-    block16<1, true>(acc, Us + 16 * ib * kP + 16 * ib, kP, at, kP, lane);
+    block16<1>(acc, Us + 16 * ib * kP + 16 * ib, kP, at, kP, lane);
     __syncwarp();
     store16(at, kP, acc[0], 1.0f, lane);
   }
@@ -375,7 +362,7 @@ __global__ void __launch_bounds__(128, 5)
       float acc[1][4] = {};
 #pragma unroll
       for (int k = 0; k < lev; ++k)
-        block16<1, true>(acc, Ls + 16 * (jb + lev) * kP + 16 * (jb + k), kP, Us + 16 * (jb + k) * kP + 16 * jb + 8 * nh, kP,
+        block16<1>(acc, Ls + 16 * (jb + lev) * kP + 16 * (jb + k), kP, Us + 16 * (jb + k) * kP + 16 * jb + 8 * nh, kP,
                    lane);
       store16(Us + 16 * (jb + lev) * kP + 16 * jb + 8 * nh, kP, acc[0], -1.0f, lane);
     }
@@ -400,7 +387,7 @@ __global__ void __launch_bounds__(128, 5)
     if (u < blocks) {
       int i, j;
       g_at(u, i, j);
-      for (int k = j; k <= i; ++k) block16<2, false>(ga[u], Ls + 16 * i * kP + 16 * k, kP, Us + 16 * k * kP + 16 * j, kP, lane);
+      for (int k = j; k <= i; ++k) block16<2>(ga[u], Ls + 16 * i * kP + 16 * k, kP, Us + 16 * k * kP + 16 * j, kP, lane);
     }
   __syncthreads();
 #pragma unroll
@@ -417,7 +404,7 @@ __global__ void __launch_bounds__(128, 5)
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     const int t = 16 * e + (tid >> 3), c8 = tid & 7;  // a warp writes four whole rows at once
-    uint32_t w[5][4] = {};  // T1, G1, T2, G2, T3 (blocks above the diagonal are zero)
+    uint32_t w[6][4] = {};  // T1, G1, T2, G2, T3, G3 (blocks above the diagonal are zero)
     if ((c8 >> 1) <= (t >> 4)) {
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
@@ -425,14 +412,12 @@ __global__ void __launch_bounds__(128, 5)
         const float2 b2 = *(const float2*)(beta_s + cc);
         const float2 x = *(const float2*)(Us + t * kP + cc), y = *(const float2*)(Ls + t * kP + cc);
         cut3(x.x * b2.x, x.y * b2.y, w[0][u], w[2][u], w[4][u]);
-        float2 gg = make_float2(y.x * b2.x, y.y * b2.y);
-        w[1][u] = cut(gg);
-        w[3][u] = tc::pack_bf16x2(gg.x, gg.y);
+        cut3(y.x * b2.x, y.y * b2.y, w[1][u], w[3][u], w[5][u]);
       }
     }
 #pragma unroll
-    for (int p = 0; p < 5; ++p) {
-      const int row = p < 4 ? stacked(t) + 16 * (p & 1) : t;
+    for (int p = 0; p < 6; ++p) {
+      const int row = stacked(t) + 16 * (p & 1);
       *(uint4*)(out + 2 * (p >> 1) * kTile + swz(row, c8)) = make_uint4(w[p][0], w[p][1], w[p][2], w[p][3]);
     }
   }
@@ -457,7 +442,7 @@ __global__ void __launch_bounds__(128, 5)
 //   A  [K; Q] (128 x 128) x [S1 | S2 | S3]     -> K S^T and Q S^T (rows as in stacked())
 //      R_t = V_t - gamma_t (K S^T)_t into shared memory (three parts); gamma_t (Q S^T)_t stays
 //      in registers
-//   B  [T1; G1] (128 x 64) x [R1 | R2 | R3], [T2; G2] x [R1 | R2], [T3; 0] x R1
+//   B  [T1; G1] (128 x 64) x [R1 | R2 | R3], [T2; G2] x [R1 | R2], [T3; G3] x R1
 //      diag(gamma_C / gamma_t) U (three parts) over R; the output is written beside the next A
 //   C  K^T (128 x 64) x [U1 | U2 | U3]          -> S's update, one row k a thread:
 //      S <- gamma_C S + update in registers, and its parts for the next A.
@@ -480,7 +465,7 @@ struct Geo {
   static constexpr int kSets = kV / kHalf;          // warps per 32 rows
   static constexpr int kThreads = 64 + 128 * kSets;
   static constexpr int kPieces = kHalf / 8;   // 16-byte pieces of a row per warp and part
-  static constexpr int kWyAt = kStages * kStage;         // [T1; G1], [T2; G2], [T3; 0]
+  static constexpr int kWyAt = kStages * kStage;         // [T1; G1], [T2; G2], [T3; G3]
   static constexpr int kSAt = kWyAt + 6 * kTile;         // S^T: 128 rows
   static constexpr int kRAt = kSAt + kAtoms * 2 * kTile; // R, then U: 64 rows
   static constexpr int kOutAt = kRAt + kAtoms * kTile;  // 512 bytes per warp: its part of the output
@@ -697,10 +682,7 @@ __global__ void __launch_bounds__(Geo<kV>::kThreads, 1)
     *abort_s = 0;
     tc::mbar_fence_init();
   }
-  // [T3; 0]: the loads write the rows of T3 alone
-  for (int e = tid; e < 2 * kTile / 16; e += kScThreads)
-    *(uint4*)(sm + G::kWyAt + 4 * kTile + 16 * e) = make_uint4(0u, 0u, 0u, 0u);
-  tc::fence_async_smem();
+  tc::fence_async_smem();  // (lengths have been written where the copies land)
   if (warp == 1) tc::tmem_alloc(tmem_s, G::kTmCols);
   tc::tc_fence_before();
   __syncthreads();
@@ -741,10 +723,7 @@ __global__ void __launch_bounds__(Geo<kV>::kThreads, 1)
         const uint8_t* src = wy + (long)c * a.H * kSlot;
         uint8_t* dst = sm + G::kWyAt;
         tc::mbar_arrive_expect_tx(wfull, kWy);
-        tc::bulk_load_1d(dst, src, 4 * kTile, wfull);
-#pragma unroll
-        for (int g = 0; g < 4; ++g)
-          tc::bulk_load_1d(dst + 4 * kTile + g * 4096, src + 4 * kTile + g * 2048, 2048, wfull);
+        tc::bulk_load_1d(dst, src, kWy, wfull);
         if (c + 1 < nc) {
           if (!load_stage(c + 1)) {
             ++c;
@@ -842,8 +821,8 @@ __global__ void __launch_bounds__(Geo<kV>::kThreads, 1)
     // the output of chunk c's tokens ta and ta + 8, with c's ga, gb and y
     auto output = [&](int c) {
       float x[kHalf / 2], z[kHalf / 2];
-      sum_frag<2, kT>(lanes2 + G::kTmB, kV, x);
-      sum_frag<1, kT>(lanes2 + G::kTmB2, kV, z);
+      sum_frag<3, kT>(lanes2 + G::kTmB, kV, x);
+      sum_frag<2, kT>(lanes2 + G::kTmB2, kV, z);
       // 16 tokens x 16 columns by way of shared memory, so that two lanes write a row's 32 bytes
       uint32_t w[4];
 #pragma unroll
@@ -927,7 +906,7 @@ __global__ void __launch_bounds__(Geo<kV>::kThreads, 1)
       tc::tc_fence_before();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(r_ready);
-      sum_frag<2, kT>(lanes2 + G::kTmA, kV, y);  // Q S^T, off by 2^-15: it goes to a bf16 output
+      sum_frag<3, kT>(lanes2 + G::kTmA, kV, y);  // Q S^T
       ok = __all_sync(0xFFFFFFFFu, tc::mbar_wait(doneB, par, abort_s));
       if (!ok) break;
       tc::tc_fence_after();
