@@ -157,6 +157,23 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _scratch(nbytes, device, stream):
+    """Device memory for the kernels of one call on `stream` (None: the current one): the allocator
+    hands memory out, and on to the next, in the order of the stream that it is asked on."""
+    with torch.cuda.stream(stream):
+        return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
+
+
+def _kept(shape, dtype, device, stream):
+    """Device memory that a call on `stream` clears and the caller keeps: taken from that stream,
+    and, once it is let go, not handed on while the stream that is current here still uses it."""
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if stream is not None:
+        t.record_stream(torch.cuda.current_stream(t.get_device()))
+    return t
+
+
 def cache_bytes(cfg: HlaConfig, max_chunks: int) -> int:
     return int(lib().hla_cache_bytes(ctypes.byref(cfg), max_chunks))
 
@@ -249,7 +266,7 @@ class Cache:
         nbytes = cache_bytes(cfg, max_chunks)
         if nbytes == 0:
             raise HlaError(HLA_ERR_UNSUPPORTED, "unsupported cache config")
-        self.mem = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        self.mem = _kept(nbytes, torch.uint8, device, stream)
         self.struct = HlaCache()
         _check(lib().hla_cache_init(ctypes.byref(cfg), max_chunks, _ptr(self.mem), nbytes,
                                     ctypes.byref(self.struct), _stream(stream)))
@@ -307,7 +324,7 @@ class Cache:
         device = self.device_index
         shape = (s.B, s.H, s.max_chunks)
         if mass is None:
-            mass = torch.empty(shape, dtype=torch.float32, device=torch.device("cuda", device))
+            mass = _kept(shape, torch.float32, torch.device("cuda", device), stream)
         p = _arg(mass, "mass", torch.float32, s.B * s.H * s.max_chunks, device)
         _run(device, stream, lib().hla_cache_track_mass, ctypes.byref(s), p)
         self.mass = mass
@@ -400,9 +417,7 @@ def gdn_forward(cfg: GdnConfig, q, k, v, alpha, beta, cu_seqlens, o, state_in=No
     pq, pk, pv, pa, pb, po = _gdn_args(cfg, T, dev, q, k, v, alpha, beta, o)
     ns = cfg.n_slots * cfg.H * cfg.dv * cfg.dk
     if workspace is None:
-        # (torch hands memory out in the order of the stream it is asked on)
-        with torch.cuda.stream(stream):
-            workspace = torch.empty(max(gdn_workspace_bytes(cfg, T), 256), dtype=torch.uint8, device=q.device)
+        workspace = _scratch(gdn_workspace_bytes(cfg, T), q.device, stream)
     nb = workspace.numel() * workspace.element_size()
     _run(dev, stream, lib().gdn_forward, ctypes.byref(cfg), pq, pk, pv, pa, pb,
          _arg(cu_seqlens, "cu_seqlens", torch.int32, cfg.n_seq + 1, dev), T,
@@ -426,7 +441,7 @@ def hla_prefill(cfg, q, k, v, alpha, beta, o, q_route=None, k_route=None, user_g
                 active_idx_out=None, active_cnt_out=None, cache: Cache | None = None, workspace=None,
                 stream=None):
     if workspace is None:
-        workspace = torch.empty(max(prefill_workspace_bytes(cfg), 256), dtype=torch.uint8, device=q.device)
+        workspace = _scratch(prefill_workspace_bytes(cfg), q.device, stream)
     _check(lib().hla_prefill(ctypes.byref(cfg), _ptr(q), _ptr(k), _ptr(v), _ptr(alpha), _ptr(beta),
                              _ptr(q_route), _ptr(k_route), _ptr(user_gates), _ptr(o), _ptr(gates_out),
                              _ptr(active_idx_out), _ptr(active_cnt_out),
@@ -438,8 +453,7 @@ def hla_prefill(cfg, q, k, v, alpha, beta, o, q_route=None, k_route=None, user_g
 def hla_decode_step(cfg, cache: Cache, q, k, v, alpha, beta, o, q_route=None, k_route=None, workspace=None,
                     stream=None):
     if workspace is None:
-        workspace = torch.empty(max(decode_workspace_bytes(cfg, cache.max_chunks), 256), dtype=torch.uint8,
-                                device=q.device)
+        workspace = _scratch(decode_workspace_bytes(cfg, cache.max_chunks), q.device, stream)
     _check(lib().hla_decode_step(ctypes.byref(cfg), ctypes.byref(cache.struct), _ptr(q), _ptr(k), _ptr(v),
                                  _ptr(alpha), _ptr(beta), _ptr(q_route), _ptr(k_route), _ptr(o),
                                  _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)))

@@ -1,0 +1,94 @@
+"""Memory that the binding takes for a call comes from the call's own stream (the allocator hands
+memory out in the order of the stream it is asked on: taken from another one, it may still be in
+use there, or be handed on while the call's kernels run).  No GPU: library and allocator are fakes."""
+import contextlib
+import types
+
+import pytest
+import torch
+
+
+class Stream:
+    cuda_stream, device = 0x5500, torch.device("cuda", 0)
+
+
+class Memory:
+    """A tensor as far as the binding looks at one."""
+
+    dtype = torch.uint8
+
+    def __init__(self, stream):
+        self.stream, self.recorded = stream, []
+
+    def numel(self):
+        return 1 << 30
+
+    def element_size(self):
+        return 1
+
+    def data_ptr(self):
+        return 0x100000
+
+    def get_device(self):
+        return 0
+
+    def record_stream(self, s):
+        self.recorded.append(s)
+
+
+@pytest.fixture
+def hla(monkeypatch):
+    from gated_delta_rule_transitions_b200 import _hla
+    from gated_delta_rule_transitions_b200 import build as b
+    b.build()
+    current, taken, calls = [], [], []
+
+    @contextlib.contextmanager
+    def stream(s):
+        current.append(s)
+        yield
+        current.pop()
+
+    def empty(*a, **k):
+        taken.append(Memory(current[-1] if current else None))
+        return taken[-1]
+
+    real = _hla.lib()
+    sizes = {"hla_cache_bytes", "hla_prefill_workspace_bytes", "hla_decode_workspace_bytes", "gdn_workspace_bytes"}
+
+    class Library:
+        def __getattr__(self, name):
+            return getattr(real, name) if name in sizes else lambda *a: calls.append((name, a[-1])) or 0
+
+    monkeypatch.setattr(torch.cuda, "stream", stream)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: "current")
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch, "empty", empty)
+    monkeypatch.setattr(_hla, "lib", Library)
+    monkeypatch.setattr(_hla, "_ptr", lambda t: None)
+    monkeypatch.setattr(_hla, "_arg", lambda t, *a: None if t is None else t.data_ptr())
+    monkeypatch.setattr(_hla, "_device", lambda *a: 0)
+    return types.SimpleNamespace(m=_hla, taken=taken, calls=calls)
+
+
+def test_transient_workspaces(hla):
+    x, s = types.SimpleNamespace(device="cuda:0", shape=(64,), data_ptr=lambda: 0x100000), Stream()
+    cfg = hla.m.make_config(1, 1, 128, 64, 128, "bf16", cache_format="int8")
+    cache = types.SimpleNamespace(struct=hla.m.HlaCache(), max_chunks=4)
+    hla.m.hla_prefill(cfg, x, x, x, x, x, x, stream=s)
+    hla.m.hla_decode_step(cfg, cache, x, x, x, x, x, x, stream=s)
+    hla.m.gdn_forward(hla.m.make_gdn_config(1, 1, 128, "bf16"), x, x, x, x, x, x, x, stream=s)
+    assert [t.stream for t in hla.taken] == [s] * 3
+    assert [getattr(c, "value", c) for _, c in hla.calls] == [s.cuda_stream] * 3
+
+
+def test_kept_memory(hla):
+    """A cache's memory and its weights are cleared on the call's stream: taken from it, and not
+    given to another call while the stream that was current still uses them."""
+    s = Stream()
+    cache = hla.m.Cache(hla.m.make_config(1, 1, 1, 64, 128, "bf16"), 4, stream=s)
+    mass = cache.track_mass(stream=s)
+    assert hla.taken == [cache.mem, mass]
+    for t in hla.taken:
+        assert t.stream is s and t.recorded == ["current"]
+    assert [getattr(c, "value", c) for _, c in hla.calls] == [s.cuda_stream] * 2
