@@ -268,8 +268,8 @@ class Cache:
             raise HlaError(HLA_ERR_UNSUPPORTED, "unsupported cache config")
         self.mem = _kept(nbytes, torch.uint8, device, stream)
         self.struct = HlaCache()
-        _check(lib().hla_cache_init(ctypes.byref(cfg), max_chunks, _ptr(self.mem), nbytes,
-                                    ctypes.byref(self.struct), _stream(stream)))
+        _run(self.mem.get_device(), stream, lib().hla_cache_init, ctypes.byref(cfg), max_chunks, _ptr(self.mem),
+             nbytes, ctypes.byref(self.struct))
         self.cfg = cfg
         self.max_chunks = max_chunks
 
@@ -351,20 +351,20 @@ class Cache:
 
 
 def gdn_chunk_transitions(cfg, k, v, alpha, beta, A_out, B_out, stream=None):
-    _check(lib().gdn_chunk_transitions(ctypes.byref(cfg), _ptr(k), _ptr(v), _ptr(alpha), _ptr(beta),
-                                       _ptr(A_out), _ptr(B_out), _stream(stream)))
+    _run(_device(k, "k"), stream, lib().gdn_chunk_transitions, ctypes.byref(cfg), _ptr(k), _ptr(v), _ptr(alpha),
+         _ptr(beta), _ptr(A_out), _ptr(B_out))
 
 
 def hla_routing(cfg, q_route, k_route, rq_out, rk_out, gates_out=None, active_idx_out=None,
                 active_cnt_out=None, stream=None):
-    _check(lib().hla_routing(ctypes.byref(cfg), _ptr(q_route), _ptr(k_route), _ptr(rq_out), _ptr(rk_out),
-                             _ptr(gates_out), _ptr(active_idx_out), _ptr(active_cnt_out), _stream(stream)))
+    _run(_device(q_route, "q_route"), stream, lib().hla_routing, ctypes.byref(cfg), _ptr(q_route), _ptr(k_route),
+         _ptr(rq_out), _ptr(rk_out), _ptr(gates_out), _ptr(active_idx_out), _ptr(active_cnt_out))
 
 
 def hla_gate_support(cfg, gates, mass_out=None, support_out=None, stream=None):
     """Routing mass and effective support per query chunk from a gate matrix."""
-    _check(lib().hla_gate_support(ctypes.byref(cfg), _ptr(gates), _ptr(mass_out), _ptr(support_out),
-                                  _stream(stream)))
+    _run(_device(gates, "gates"), stream, lib().hla_gate_support, ctypes.byref(cfg), _ptr(gates), _ptr(mass_out),
+         _ptr(support_out))
 
 
 def hla_gate_mass(cfg, gates, mass_out, stream=None):
@@ -440,31 +440,31 @@ def gdn_step(cfg: GdnConfig, q, k, v, alpha, beta, state, o, slots=None, stream=
 def hla_prefill(cfg, q, k, v, alpha, beta, o, q_route=None, k_route=None, user_gates=None, gates_out=None,
                 active_idx_out=None, active_cnt_out=None, cache: Cache | None = None, workspace=None,
                 stream=None):
+    dev = _device(q, "q")
     if workspace is None:
         workspace = _scratch(prefill_workspace_bytes(cfg), q.device, stream)
-    _check(lib().hla_prefill(ctypes.byref(cfg), _ptr(q), _ptr(k), _ptr(v), _ptr(alpha), _ptr(beta),
-                             _ptr(q_route), _ptr(k_route), _ptr(user_gates), _ptr(o), _ptr(gates_out),
-                             _ptr(active_idx_out), _ptr(active_cnt_out),
-                             ctypes.byref(cache.struct) if cache is not None else None,
-                             _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)))
+    _run(dev, stream, lib().hla_prefill, ctypes.byref(cfg), _ptr(q), _ptr(k), _ptr(v), _ptr(alpha), _ptr(beta),
+         _ptr(q_route), _ptr(k_route), _ptr(user_gates), _ptr(o), _ptr(gates_out), _ptr(active_idx_out),
+         _ptr(active_cnt_out), ctypes.byref(cache.struct) if cache is not None else None, _ptr(workspace),
+         workspace.numel() * workspace.element_size())
     return o
 
 
 def hla_decode_step(cfg, cache: Cache, q, k, v, alpha, beta, o, q_route=None, k_route=None, workspace=None,
                     stream=None):
+    dev = _device(q, "q")
     if workspace is None:
         workspace = _scratch(decode_workspace_bytes(cfg, cache.max_chunks), q.device, stream)
-    _check(lib().hla_decode_step(ctypes.byref(cfg), ctypes.byref(cache.struct), _ptr(q), _ptr(k), _ptr(v),
-                                 _ptr(alpha), _ptr(beta), _ptr(q_route), _ptr(k_route), _ptr(o),
-                                 _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)))
+    _run(dev, stream, lib().hla_decode_step, ctypes.byref(cfg), ctypes.byref(cache.struct), _ptr(q), _ptr(k), _ptr(v),
+         _ptr(alpha), _ptr(beta), _ptr(q_route), _ptr(k_route), _ptr(o), _ptr(workspace),
+         workspace.numel() * workspace.element_size())
     return o
 
 
 def hla_decode_step_static(cfg, cache: Cache, q, k, v, alpha, beta, o, q_route=None, k_route=None, stream=None):
     """hla_decode_step with the library's fixed device scratch array: allocates nothing."""
-    _check(lib().hla_decode_step_static(ctypes.byref(cfg), ctypes.byref(cache.struct), _ptr(q), _ptr(k), _ptr(v),
-                                        _ptr(alpha), _ptr(beta), _ptr(q_route), _ptr(k_route), _ptr(o),
-                                        _stream(stream)))
+    _run(_device(q, "q"), stream, lib().hla_decode_step_static, ctypes.byref(cfg), ctypes.byref(cache.struct), _ptr(q),
+         _ptr(k), _ptr(v), _ptr(alpha), _ptr(beta), _ptr(q_route), _ptr(k_route), _ptr(o))
     return o
 
 

@@ -92,3 +92,46 @@ def test_kept_memory(hla):
     for t in hla.taken:
         assert t.stream is s and t.recorded == ["current"]
     assert [getattr(c, "value", c) for _, c in hla.calls] == [s.cuda_stream] * 2
+
+
+def test_calls_run_on_their_tensors_device(hla, monkeypatch):
+    """Tensors on another device than the current one: the call runs there, on that device's
+    current stream; a stream of a third device is refused."""
+    now = [0]
+
+    @contextlib.contextmanager
+    def device(d):
+        before, now[0] = now[0], d
+        yield
+        now[0] = before
+
+    ran = []
+    monkeypatch.setattr(torch.cuda, "device", device)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: now[0])
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda d=None: types.SimpleNamespace(cuda_stream=100 + now[0]))
+    monkeypatch.setattr(hla.m, "_raw_stream", lambda d: 100 + d)
+    monkeypatch.setattr(hla.m, "_device", lambda *a: 1)
+    real = hla.m.lib()
+
+    class Library:
+        def __getattr__(self, name):
+            if "bytes" in name:
+                return getattr(real, name)
+            return lambda *a: ran.append((name, now[0], getattr(a[-1], "value", a[-1]))) or 0
+
+    monkeypatch.setattr(hla.m, "lib", Library)
+    x, ws = types.SimpleNamespace(device="cuda:1", shape=(64,), data_ptr=lambda: 0x100000), Memory(None)
+    cfg = hla.m.make_config(1, 1, 128, 64, 128, "bf16")
+    cache = types.SimpleNamespace(struct=hla.m.HlaCache(), max_chunks=4)
+    hla.m.hla_prefill(cfg, x, x, x, x, x, x, workspace=ws)
+    hla.m.hla_decode_step(cfg, cache, x, x, x, x, x, x, workspace=ws)
+    hla.m.hla_decode_step_static(cfg, cache, x, x, x, x, x, x)
+    hla.m.hla_routing(cfg, x, x, x, x)
+    hla.m.hla_gate_support(cfg, x, x)
+    hla.m.gdn_chunk_transitions(cfg, x, x, x, x, x, x)
+    assert len(ran) == 6 and all(r[1:] == (1, 101) for r in ran), ran
+    with pytest.raises(ValueError, match="stream is on"):
+        hla.m.hla_decode_step(cfg, cache, x, x, x, x, x, x, workspace=ws, stream=Stream())
+    monkeypatch.setattr(Memory, "get_device", lambda self: 1)
+    hla.m.Cache(cfg, 4, device="cuda:1")
+    assert ran[-1] == ("hla_cache_init", 1, 101)
