@@ -252,6 +252,7 @@ class CacheSlice:
     def __init__(self):
         self.struct = HlaCache()
         self.parent = None
+        self.mass = None  # the weights that it points at (the parent may be tracked anew)
         self.max_chunks = 0
 
     @property
@@ -266,6 +267,7 @@ class Cache:
         nbytes = cache_bytes(cfg, max_chunks)
         if nbytes == 0:
             raise HlaError(HLA_ERR_UNSUPPORTED, "unsupported cache config")
+        self.mass = None  # the weights that it keeps, if any (track_mass)
         self.mem = _kept(nbytes, torch.uint8, device, stream)
         self.struct = HlaCache()
         _run(self.mem.get_device(), stream, lib().hla_cache_init, ctypes.byref(cfg), max_chunks, _ptr(self.mem),
@@ -309,6 +311,7 @@ class Cache:
             setattr(st, name, _arg(t, name, *want[name], device))
         self.mem = None
         self.buffers = dict(buffers)  # keeps the memory alive
+        self.mass = buffers.get("mass")
         self.cfg = cfg
         self.max_chunks = max_chunks
         return self
@@ -334,6 +337,7 @@ class Cache:
         """The cache of sequences [b0, b0 + nb) (shares this cache's memory)."""
         sub = CacheSlice()
         sub.parent = self
+        sub.mass = self.mass
         sub.max_chunks = self.max_chunks
         _check(lib().hla_cache_slice(ctypes.byref(self.struct), b0, nb, ctypes.byref(sub.struct)))
         return sub
