@@ -344,8 +344,8 @@ class Cache:
 
     def view(self, field: str, shape, dtype):
         """Torch view of one cache buffer (for tests and inspection)."""
-        if self.mem is None:
-            return self.buffers[field].view(dtype).view(*shape)
+        if field == "mass" or self.mem is None:
+            return (self.mass if field == "mass" else self.buffers[field]).view(dtype).view(*shape)
         off = getattr(self.struct, field) - self.mem.data_ptr()
         n = 1
         for s in shape:

@@ -37,3 +37,13 @@ def test_a_slice_keeps_the_weights_it_points_at(hla):
     del sub
     gc.collect()
     assert first() is None
+
+
+def test_view_of_the_weights(hla):
+    """The weights lie in memory of their own, not in the cache's block; tracked anew, not in the
+    buffer that a cache over given tensors started with either."""
+    cache = tracked(hla, torch.arange(16.0).view(2, 2, 4))
+    cache.buffers["mass"] = torch.zeros(2, 2, 4)
+    assert torch.equal(cache.view("mass", (2, 2, 4), torch.float32), cache.mass)
+    cache.mem = torch.zeros(64, dtype=torch.uint8)
+    assert torch.equal(cache.view("mass", (16,), torch.float32), torch.arange(16.0))
