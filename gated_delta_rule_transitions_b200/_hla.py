@@ -322,7 +322,8 @@ class Cache:
 
     def track_mass(self, mass=None, stream=None):
         """Accumulate every closed chunk's gate weight from now on; returns the
-        [B, H, max_chunks] float32 tensor that holds it (given or made here, zeroed)."""
+        [B, H, max_chunks] float32 tensor that holds it (given or made here, zeroed).
+        untrack_mass stops it."""
         s = self.struct
         device = self.device_index
         shape = (s.B, s.H, s.max_chunks)
@@ -332,6 +333,11 @@ class Cache:
         _run(device, stream, lib().hla_cache_track_mass, ctypes.byref(s), p)
         self.mass = mass
         return mass
+
+    def untrack_mass(self, stream=None):
+        """Stop accumulating weights (slices taken before go on with theirs)."""
+        _run(self.device_index, stream, lib().hla_cache_track_mass, ctypes.byref(self.struct), None)
+        self.mass = None
 
     def slice(self, b0: int, nb: int):
         """The cache of sequences [b0, b0 + nb) (shares this cache's memory)."""

@@ -47,3 +47,14 @@ def test_view_of_the_weights(hla):
     assert torch.equal(cache.view("mass", (2, 2, 4), torch.float32), cache.mass)
     cache.mem = torch.zeros(64, dtype=torch.uint8)
     assert torch.equal(cache.view("mass", (16,), torch.float32), torch.arange(16.0))
+
+
+def test_tracking_stops(hla, monkeypatch):
+    """untrack_mass: the C call with NULL; nothing is launched, the weights are let go."""
+    cache = tracked(hla, torch.zeros(2, 2, 4))
+    monkeypatch.setattr(hla.Cache, "device_index", 0)
+    monkeypatch.setattr(hla, "_raw_stream", lambda d: 0)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    cache.untrack_mass()
+    assert cache.struct.mass is None and cache.mass is None
+    assert cache.slice(0, 1).struct.mass is None
