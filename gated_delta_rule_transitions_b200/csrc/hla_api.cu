@@ -1285,9 +1285,11 @@ hla_status hla_decode_step_static(const hla_config* cfg, hla_cache* cache, const
   if (need > kStaticScratchBytes)
     return fail(HLA_ERR_WORKSPACE,
                 "decode scratch for B=%d H=%d max_chunks=%d is %zu bytes; the static array holds %zu "
-                "(8 B per (sequence, head, chunk) and 4 B per (sequence, head), each part rounded up to "
+                "(8 B per (sequence, head, chunk) and 4 B per (sequence, head)%s, each part rounded up to "
                 "256 B); use hla_decode_step with a caller workspace",
-                cfg->B, cfg->H, cache->max_chunks, need, kStaticScratchBytes);
+                cfg->B, cfg->H, cache->max_chunks, need, kStaticScratchBytes,
+                cfg->cache_format == HLA_CACHE_INT8 ? ", and of an 8-bit cache two d x d matrices per (sequence, head)"
+                                                    : "");
   void* ws = nullptr;
   HLA_TRY(static_scratch_ptr(&ws));
   return hla_decode_step(cfg, cache, q, k, v, alpha, beta, q_route, k_route, o, ws, kStaticScratchBytes, stream);

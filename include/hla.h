@@ -414,7 +414,8 @@ hla_status hla_prefill(const hla_config* cfg, const void* q, const void* k, cons
  *      rule run row by row).  Gate modes ROUTED, ONE and ZERO.
  * workspace: device, >= hla_decode_workspace_bytes(cfg, cache->max_chunks): the
  *      active lists and gates ([B,H,max_chunks] int32 and float32) and one list length
- *      per (sequence, head), each part rounded up to 256 bytes.
+ *      per (sequence, head), each part rounded up to 256 bytes; for an 8-bit cache also a
+ *      closing chunk's A and B before they are rounded ([B,H,d,d] dtype each).
  * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE (also: cache full), CUDA.
  */
 hla_status hla_decode_step(const hla_config* cfg, hla_cache* cache, const void* q,
@@ -433,6 +434,9 @@ hla_status hla_decode_step(const hla_config* cfg, hla_cache* cache, const void* 
  * HLA_DECODE_STATIC_SCRATCH_BYTES long: it holds hla_decode_workspace_bytes(cfg,
  * max_chunks) when 8 B per (sequence, head, chunk) plus 4 B per (sequence, head), each
  * part rounded up to 256 B, fit in it (for example B*H = 1024 with max_chunks = 1023).
+ * An 8-bit cache needs room for a closing chunk's two d x d matrices per (sequence, head)
+ * as well, which is what fills the array there: B*H up to 127 in bf16 with d = 128 (64 KiB
+ * a pair), 63 in float32; 508 and 254 with d = 64.
  * A larger cache is rejected with HLA_ERR_WORKSPACE before anything is launched.
  * No call allocates or frees device memory.
  * Set-up: the first call on a device (the current one) looks up the array's
