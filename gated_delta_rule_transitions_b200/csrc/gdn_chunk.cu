@@ -15,7 +15,8 @@
 //
 // What bounds it: the scan's chain of a chunk, 3,030 cycles with 16 columns and 6,000 with 64
 // (there shared memory's bandwidth as well); the tensor cores are active 16 % of the time.
-// Measured, 16 heads: 16384 tokens of one sequence 524 us, four sequences of 4096 tokens 314 us.
+// Measured, 16 heads: 16384 tokens of one sequence 534 us (T and G 96), four sequences of
+// 4096 tokens 318 us (T and G 99).
 //
 // Precision.  The state is float32 and stays so: it is held in registers, and what goes into
 // a product (S, R, U, T) goes in as three bf16 numbers, x = x1 + x2 + x3, each the eight bits
@@ -26,6 +27,15 @@
 // each, it was off by 2^-12 before its own rounding and by 8e-4 of its size after it.  Decays are
 // differences of 64-bit running sums of float32 logarithms: log alpha is off by 2^-24 of itself,
 // so a decay e^l by at most |l| e^l 2^-24 < 2^-25.
+//
+// NaN and infinities.  The entries of T and G above the diagonal are zeros that are multiplied all
+// the same, so a token that is no number would spoil the 63 before it.  Therefore: gdn_wy_kernel
+// keeps T and G finite and writes an undefined gamma from the first token on whose key, decay or
+// beta is none; gdn_scan_kernel takes such tokens, and values that are none, as zeros, and makes
+// undefined what they reach.  (A bad query has a row of its own.  The checks cost 3 %: 16384
+// tokens 524 -> 535 us.)
+#include <climits>
+
 #include "common.cuh"
 #include "kernels.cuh"
 #include "tc_common.cuh"
@@ -110,7 +120,7 @@ constexpr int kWyQK = 0;                      // [kb][Q | K][64 rows][128 B]; on
 constexpr int kWyL = 0;                       //   L, then L' (off the diagonal blocks), then P, then G
 constexpr int kWyU = kMat;                    //   (I + L)^{-1}
 constexpr int kWySmall = 2 * kMat;
-constexpr int kWySmem = kWySmall + kC * 8 + 3 * kC * 4 + 2 * 8 + 32;
+constexpr int kWySmem = kWySmall + kC * 8 + 3 * kC * 4 + 2 * 8 + 40;
 static_assert(2 * kMat >= 4 * kTile, "the tiles fit under L and U");
 constexpr uint32_t kIdescWy = tc::idesc_bf16_f32(128, 64, 0, 0);
 constexpr float kProductRange = 40.0f;
@@ -188,6 +198,7 @@ __global__ void __launch_bounds__(128, 5)
   uint32_t* lmax = (uint32_t*)(wsum + 1);       // [2]
   uint32_t* tmem_s = lmax + 2;
   volatile int* abort_s = (volatile int*)(tmem_s + 1);
+  int* bad_s = (int*)tmem_s + 2;                // first token whose products with keys are no numbers
 
   // gdn_scan_kernel's blocks may take their places while this grid drains
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -214,6 +225,7 @@ __global__ void __launch_bounds__(128, 5)
     tc::mbar_init(&bars[0], 1);
     tc::mbar_init(&bars[1], 1);
     *abort_s = 0;
+    *bad_s = kC;
     tc::mbar_fence_init();
     tc::fence_async_smem();
   }
@@ -239,6 +251,12 @@ __global__ void __launch_bounds__(128, 5)
       const float x = logf(a.alpha[at]);
       la = x < -200.0f ? -200.0 : (double)x;
       be = a.beta[at];
+      // T and G have no other number than these: an infinite or undefined beta (or decay) becomes
+      // an undefined gamma from its token on, by which gdn_scan_kernel knows
+      if (!(fabsf(be) < INFINITY)) {
+        la = (double)NAN;
+        be = 0.0f;
+      }
     }
     beta_s[tid] = be;
 #pragma unroll
@@ -282,6 +300,14 @@ __global__ void __launch_bounds__(128, 5)
     tc::mma_commit(&bars[1]);
   }
   if (ok) ok = tc::bar_all(1, 128, tid == 0 ? tc::mbar_wait(&bars[1], 0, abort_s) : true);
+  // An entry of L or U that is no number is left out, and its token (its row) noted: as zero times
+  // NaN it would reach the rows before, while its own row and those after it are undefined anyway.
+  auto finite_or_note = [&](float& x, int t) {
+    if (!(fabsf(x) < INFINITY)) {
+      x = 0.0f;
+      atomicMin(bad_s, t);
+    }
+  };
   // rows 0-63 (warps 0, 1): P = tril(Gamma o Q K^T); rows 64-127 (warps 2, 3): L; each when asked
   auto masked = [&](bool isL) {
     const int t = tid & (kC - 1);
@@ -290,6 +316,7 @@ __global__ void __launch_bounds__(128, 5)
     const int last = isL ? t - 1 : t;  // columns up to and with `last`
     const bool product = max(lmax[0], lmax[1]) <= __float_as_uint(kProductRange);
     const float gt = gam[t] * bt;
+    float4 z = make_float4(0.0f, 0.0f, 0.0f, 0.0f);  // becomes NaN with an entry that is no number
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
       uint32_t x[32];
@@ -306,15 +333,21 @@ __global__ void __launch_bounds__(128, 5)
           v.z = s + 2 <= last ? gt * i4.z * __uint_as_float(x[e + 2]) : 0.0f;
           v.w = s + 3 <= last ? gt * i4.w * __uint_as_float(x[e + 3]) : 0.0f;
           *(float4*)(row + s) = v;
+          if (isL) z = make_float4(fmaf(v.x, 0.0f, z.x), fmaf(v.y, 0.0f, z.y), fmaf(v.z, 0.0f, z.z), fmaf(v.w, 0.0f, z.w));
         }
       } else {
         const double lt = ell[t];
 #pragma unroll
         for (int e = 0; e < 32; ++e) {
           const int s = 32 * half + e;
-          row[s] = s <= last ? bt * expf((float)(lt - ell[s])) * __uint_as_float(x[e]) : 0.0f;
+          const float v = s <= last ? bt * expf((float)(lt - ell[s])) * __uint_as_float(x[e]) : 0.0f;
+          row[s] = v;
+          if (isL) z.x = fmaf(v, 0.0f, z.x);
         }
       }
+    }
+    if (isL && (z.x + z.y) + (z.z + z.w) != 0.0f) {
+      for (int s = 0; s <= last; ++s) finite_or_note(row[s], t);
     }
   };
   if (ok) tc::tc_fence_after();
@@ -338,6 +371,13 @@ __global__ void __launch_bounds__(128, 5)
         if (s4 + 3 < tl) v = fmaf(-w.w, x[s4 + 3], v);
       }
       x[tl] = v;
+    }
+    float z = 0.0f;
+#pragma unroll
+    for (int tl = 0; tl < 16; ++tl) z = fmaf(x[tl], 0.0f, z);
+    if (z != 0.0f) {
+#pragma unroll
+      for (int tl = 0; tl < 16; ++tl) finite_or_note(x[tl], 16 * k + tl);
     }
 #pragma unroll
     for (int tl = 0; tl < 16; ++tl) Us[(16 * k + tl) * kP + 16 * k + cc] = x[tl];
@@ -364,6 +404,10 @@ __global__ void __launch_bounds__(128, 5)
       for (int k = 0; k < lev; ++k)
         block16<1>(acc, Ls + 16 * (jb + lev) * kP + 16 * (jb + k), kP, Us + 16 * (jb + k) * kP + 16 * jb + 8 * nh, kP,
                    lane);
+      if (acc[0][0] * 0.0f + acc[0][1] * 0.0f + acc[0][2] * 0.0f + acc[0][3] * 0.0f != 0.0f) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) finite_or_note(acc[0][e], 16 * (jb + lev) + (lane >> 2) + 8 * (e >> 1));
+      }
       store16(Us + 16 * (jb + lev) * kP + 16 * jb + 8 * nh, kP, acc[0], -1.0f, lane);
     }
     __syncthreads();
@@ -422,10 +466,10 @@ __global__ void __launch_bounds__(128, 5)
     }
   }
   float* sc = (float*)(out + kWy);
-  if (tid < kC)
-    sc[tid] = gam[tid];
+  if ((tid & (kC - 1)) >= *bad_s)
+    sc[tid] = NAN;
   else
-    sc[tid] = exp64(ell[kC - 1] - ell[tid - kC]);
+    sc[tid] = tid < kC ? gam[tid] : exp64(ell[kC - 1] - ell[tid - kC]);
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
@@ -470,7 +514,7 @@ struct Geo {
   static constexpr int kRAt = kSAt + kAtoms * 2 * kTile; // R, then U: 64 rows
   static constexpr int kOutAt = kRAt + kAtoms * kTile;  // 512 bytes per warp: its part of the output
   static constexpr int kSmallAt = kOutAt + 4 * kSets * 512;
-  static constexpr int kSmem = kSmallAt + 160;
+  static constexpr int kSmem = kSmallAt + 128 + 4 * kV;
   static constexpr uint32_t kIdescA = tc::idesc_bf16_f32(128, 3 * kV, 0, 1);
   static constexpr uint32_t kIdescB2 = tc::idesc_bf16_f32(128, 2 * kV, 0, 1);
   static constexpr uint32_t kIdescB3 = tc::idesc_bf16_f32(128, kV, 0, 1);
@@ -514,6 +558,13 @@ template <int kN>
 __device__ __forceinline__ void after_wait(uint32_t (&r)[kN]) {
 #pragma unroll
   for (int i = 0; i < kN; ++i) asm volatile("" : "+r"(r[i]));
+}
+
+// Two bf16 numbers times zero: zeros, or NaN where one is infinite or none.
+__device__ __forceinline__ uint32_t times_zero(uint32_t w) {
+  uint32_t r;
+  asm("fma.rn.bf16x2 %0, %1, %2, %2;" : "=r"(r) : "r"(w), "r"(0u));
+  return r;
 }
 
 // Sum of kN accumulators, `pitch` columns apart, on 16 lanes x 16 kT columns (ld_frag's layout).
@@ -581,6 +632,8 @@ __global__ void __launch_bounds__(Geo<kV>::kThreads, 1)
   uint64_t* fin = u_ready + 1;
   uint32_t* tmem_s = (uint32_t*)(fin + 1);
   volatile int* abort_s = (volatile int*)(tmem_s + 1);
+  volatile int* any_bad = abort_s + 1;
+  int* first_bad = (int*)(sm + G::kSmallAt + 128);  // [kV] first token of the sequence that makes a column undefined
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int v0 = (int)(blockIdx.x % kSplit) * kV;
@@ -680,8 +733,10 @@ __global__ void __launch_bounds__(Geo<kV>::kThreads, 1)
     tc::mbar_init(u_ready, 4 * G::kSets);
     tc::mbar_init(fin, 1);
     *abort_s = 0;
+    *any_bad = 0;
     tc::mbar_fence_init();
   }
+  if (tid < kV) first_bad[tid] = INT_MAX;
   tc::fence_async_smem();  // (lengths have been written where the copies land)
   if (warp == 1) tc::tmem_alloc(tmem_s, G::kTmCols);
   tc::tc_fence_before();
@@ -818,18 +873,27 @@ __global__ void __launch_bounds__(Geo<kV>::kThreads, 1)
     for (int v = 0; v < kHalf; ++v) S[v] = a.state_in != nullptr ? a.state_in[srow + (long)v * kD] : 0.0f;
     float ga = 0.0f, gb = 0.0f;       // gamma of tokens ta, ta + 8
     float y[kHalf / 2];                // Q S^T of the chunk, until its output is written
+    // column of the CTA that register pair e of a fragment (sum_frag) starts at, and its token
+    auto frag_col = [&](int e) { return kHalf * ch + 8 * (e >> 2) + 2 * (lane & 3); };
+    auto frag_row = [&](int e) { return ta + ((e & 2) ? 8 : 0); };
     // the output of chunk c's tokens ta and ta + 8, with c's ga, gb and y
-    auto output = [&](int c) {
+    auto output = [&](int c, bool undefined) {  // undefined: a column is, from some token on
       float x[kHalf / 2], z[kHalf / 2];
       sum_frag<3, kT>(lanes2 + G::kTmB, kV, x);
       sum_frag<2, kT>(lanes2 + G::kTmB2, kV, z);
       // 16 tokens x 16 columns by way of shared memory, so that two lanes write a row's 32 bytes
+#pragma unroll
+      for (int e = 0; e < kHalf / 2; ++e) x[e] = fmaf((e & 2) ? gb : ga, y[e], x[e] + z[e]);
+      if (undefined) {
+#pragma unroll
+        for (int e = 0; e < kHalf / 2; ++e)
+          if (c * kC + frag_row(e) >= first_bad[frag_col(e) + (e & 1)]) x[e] = NAN;
+      }
       uint32_t w[4];
 #pragma unroll
       for (int m = 0; m < 4; ++m) {  // matrix m: tokens 8 (m & 1) .., columns 8 (m >> 1) ..
         const int e = 4 * (m >> 1) + 2 * (m & 1);
-        const float g = (m & 1) ? gb : ga;
-        w[m] = tc::pack_bf16x2(fmaf(g, y[e], x[e] + z[e]), fmaf(g, y[e + 1], x[e + 1] + z[e + 1]));
+        w[m] = tc::pack_bf16x2(x[e], x[e + 1]);
       }
       uint8_t* stage = sm + G::kOutAt + (warp - 2) * 512;
       __syncwarp();  // (the chunk before has been read)
@@ -845,6 +909,7 @@ __global__ void __launch_bounds__(Geo<kV>::kThreads, 1)
       const uint32_t par = (uint32_t)c & 1;
       uint8_t* stage = sm + (c % kStages) * kStage;
       const int n = min(kC, len - c * kC);
+      const bool undefined = *any_bad != 0;
       // S's parts: row r, columns of set ch
 #pragma unroll
       for (int i = 0; i < G::kPieces; ++i) {
@@ -873,7 +938,7 @@ __global__ void __launch_bounds__(Geo<kV>::kThreads, 1)
       // while A runs: the output of the chunk before (B's accumulators are not written again
       // before r_ready), and what the next steps need of this chunk (read before r_ready: the
       // stage may be refilled once C is done)
-      if (c > 0) output(c - 1);
+      if (c > 0) output(c - 1, undefined);
       ok = __all_sync(0xFFFFFFFFu, tc::mbar_wait(&full[c % kStages], (uint32_t)(c / kStages) & 1, abort_s));
       if (!ok) break;
       const float* sc = (const float*)(stage + kStScal);
@@ -883,13 +948,30 @@ __global__ void __launch_bounds__(Geo<kV>::kThreads, 1)
 #pragma unroll
       for (int i = 0; i < kT; ++i)
         ldmatrix4(tc::smem_u32(stage + kStV) + swz(16 * q + (lane & 15), vpiece + 2 * i + (lane >> 4)), vw[i]);
+      // A value that is no number goes into the products as zero, for the tokens before it; from its
+      // token on its column is undefined: output() and the end see to that.
+      static_assert(kHalf == 16, "eight values a thread");
+      if (((times_zero(vw[0][0]) | times_zero(vw[0][1]) | times_zero(vw[0][2]) | times_zero(vw[0][3])) & 0x7FFF7FFFu)) {
+#pragma unroll
+        for (int e = 0; e < kHalf / 2; ++e) {
+          uint32_t& w = vw[0][2 * (e >> 2) + ((e >> 1) & 1)];
+          const uint32_t mask = (e & 1) ? 0xFFFF0000u : 0xFFFFu;
+          if (frag_row(e) < n && (times_zero(w & mask) & 0x7FFF7FFFu)) {
+            atomicMin(&first_bad[frag_col(e) + (e & 1)], c * kC + frag_row(e));
+            *any_bad = 1;
+            w &= ~mask;
+          }
+        }
+      }
       ok = __all_sync(0xFFFFFFFFu, tc::mbar_wait(doneA, par, abort_s));
       if (!ok) break;
       tc::tc_fence_after();
       float x[kHalf / 2];
       sum_frag<3, kT>(lanes + G::kTmA, kV, x);
       {
-        const bool la = ta < n, lb = ta + 8 < n;  // R is zero behind the sequence
+        // R is zero behind the sequence, and where gamma is undefined: that token would reach those
+        // before it as zero times NaN (its own output and the state get gamma as well)
+        const bool la = ta < n && fabsf(ga) < INFINITY, lb = ta + 8 < n && fabsf(gb) < INFINITY;
 #pragma unroll
         for (int i = 0; i < kT; ++i)
 #pragma unroll
@@ -943,8 +1025,13 @@ __global__ void __launch_bounds__(Geo<kV>::kThreads, 1)
                           __uint_as_float(z[0][v >> 4][v & 15]));
       }
     }
-    if (ok) output(nc - 1);
+    if (ok) output(nc - 1, *any_bad != 0);
     if (ok && a.state_out != nullptr) {
+      if (*any_bad) {
+#pragma unroll
+        for (int v = 0; v < kHalf; ++v)
+          if (first_bad[kHalf * ch + v] != INT_MAX) S[v] = NAN;
+      }
 #pragma unroll
       for (int v = 0; v < kHalf; ++v) a.state_out[srow + (long)v * kD] = S[v];
     }

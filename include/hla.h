@@ -319,9 +319,12 @@ hla_status hla_cache_evict(const hla_config* cfg, const hla_cache* src, hla_cach
  * beta in [0, 1], as in the token rule above; o must not overlap the inputs.
  * bf16 with d = 128 and the scalar decay runs long sequences by chunks of 64 tokens on the
  * tensor cores, with the state and everything that reaches it held to float32's precision;
- * short ones and the others run the rule token by token on CUDA cores.  A NaN or an infinity
- * among a sequence's tokens makes its state and outputs undefined from 63 tokens before it
- * on; other sequences, and rows of no sequence, are never mixed in.
+ * short ones and the others run the rule token by token on CUDA cores.  By either way a NaN or
+ * an infinity among a sequence's tokens spoils what the rule lets it reach and no more: a query
+ * its own output, a value its own column of the outputs and row of the state from its token on,
+ * the others all of the head from their token on.  (Finite states, values and keys whose
+ * products overflow float32 may, by chunks, spoil up to 63 tokens before as well.)  Other
+ * sequences, and rows of no sequence, are never mixed in.
  * Calls are deterministic.  Those whose kernels may overlap in time (other streams, two
  * graphs) need workspaces and states of their own.
  */
