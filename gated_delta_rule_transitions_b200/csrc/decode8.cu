@@ -9,14 +9,17 @@
 // active chunk, half of bf16's.
 //
 // The products are whole-number ones.  The running x is held in float32; before each chunk
-// it is written as a fixed-point number of 24 bits relative to its largest entry,
-//   x_c = 2^(e - 22) N_c,  |N_c| <= 2^22,  N_c = d0 + 2^8 d1 + 2^16 d2  (signed bytes),
-// so that QA x and QB x are three exact dot products of bytes each (32-bit sums: at most
+// it is written as a fixed-point number of 32 bits relative to its largest entry,
+//   x_c = 2^(e - 30) N_c,  |N_c| <= 127 x 2^24,  N_c = d0 + 2^8 d1 + 2^16 d2 + 2^24 d3  (signed bytes),
+// so that QA x and QB x are four exact dot products of bytes each (32-bit sums: at most
 // 128 x 127 x 128 < 2^21).  The only error beside float32's own is the fixed point's half
-// unit, 2^-23 of the largest entry.
+// unit, some 2^-32 to 2^-31 of the largest entry (2^-127 where that is below 2^-96): an entry
+// keeps all its bits down to 2^-6 of the largest.  (With three digits, 24 bits, entries 2^-7
+// below came out with a relative error of 1e-5; the fourth is a column that the product has
+// to spare.)
 //
 // decode_stream8_kernel (bf16, d = 128; after decode_gates_kernel): one CTA per (sequence,
-// head), two per SM.  The three digit vectors are three columns of one right factor on the
+// head), two per SM.  The four digit vectors are four columns of one right factor on the
 // tensor cores (warp-level 16 x 8 x 32); the matrices go there from shared memory as they lie,
 // 16 ldmatrix a warp and chunk, nothing is converted.  (As dp4a a chunk took 1,410
 // cycles, 880 of them the products, as they are some 1,100; 64 sequences x 16 heads x 512
@@ -49,29 +52,39 @@ constexpr int kU8Tile = kD * kD;                    // 16 KiB of codes
 constexpr int kU8Unit = 2 * kU8Tile;                // 32 KiB
 constexpr int kU8Units = 3;
 constexpr uint32_t kU8Tx = kU8Unit + 16;
-constexpr int kDigits = kD + 32;                    // pitch of a digit vector: three on 24 banks
-constexpr int kU8Vec = 3 * kDigits;                 // digits of one x
+constexpr int kDigits = kD + 32;                    // pitch of a digit vector: four on 32 banks
+constexpr int kU8Vec = 4 * kDigits;                 // digits of one x
 
-// x (this thread's row) as digits; returns the unit 2^(e - 22).  A zero x has digits and unit
-// zero; one with an infinity or a NaN has unit NaN.  Contains one barrier.
+// x (this thread's row) as digits; returns the unit 2^(e - 30).  The digits of a zero x are zero;
+// one with an infinity or a NaN has unit NaN.  Contains one barrier.
 __device__ __forceinline__ float write_digits(float x, int row, uint32_t* mx, uint8_t* xd) {
   const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(x) & 0x7FFFFFFFu);
   if ((threadIdx.x & 31) == 0) mx[threadIdx.x >> 5] = m;
   tc::bar_sync(1, kCompute);
   const uint4 m4 = *(const uint4*)mx;
   const uint32_t big = max(max(m4.x, m4.y), max(m4.z, m4.w));
-  // |x| < 2^e; below 2^-100 the fixed point stays where it is
-  const int e = max((int)(big >> 23) - 126, -100);
-  const float up = __uint_as_float((uint32_t)(127 + 22 - e) << 23);
+  // |x| < 127/128 2^(e + 1), so that the last digit stays a signed byte; below 2^-96 the fixed
+  // point stays where it is
+  const int e = max((int)((big + 0x20000u) >> 23) - 127, -96);
+  const float up = __uint_as_float((uint32_t)(127 + 30 - e) << 23);
   const int n = __float2int_rn(x * up);
   const int d0 = (int)(int8_t)n;
   const int n1 = (n - d0) >> 8;
   const int d1 = (int)(int8_t)n1;
+  const int n2 = (n1 - d1) >> 8;
+  const int d2 = (int)(int8_t)n2;
   xd[row] = (uint8_t)d0;
   xd[kDigits + row] = (uint8_t)d1;
-  xd[2 * kDigits + row] = (uint8_t)((n1 - d1) >> 8);
+  xd[2 * kDigits + row] = (uint8_t)d2;
+  xd[3 * kDigits + row] = (uint8_t)((n2 - d2) >> 8);
   if (big >= 0x7F800000u) return __uint_as_float(0x7FC00000u);
-  return __uint_as_float((uint32_t)(127 - 22 + e) << 23);
+  return __uint_as_float((uint32_t)(127 - 30 + e) << 23);
+}
+
+// Two digits' sums joined (below 2^30); the other two lie in the neighbouring lane.
+__device__ __forceinline__ float join2(int lo, int hi) { return (float)(lo + 256 * hi); }
+__device__ __forceinline__ float join4(float lo) {
+  return fmaf(__shfl_xor_sync(0xFFFFFFFFu, lo, 1), 65536.0f, lo);
 }
 
 __device__ __forceinline__ void mma_s8(int (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -291,7 +304,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (!tc::bar_all(1, kCompute, tc::mbar_wait(&full[st], (u / kU8Units) & 1, abort_s))) break;
       uint32_t xb[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) xb[e] = dcol < 3 ? *(const uint32_t*)(xc + 16 * e) : 0u;
+      for (int e = 0; e < 8; ++e) xb[e] = dcol < 4 ? *(const uint32_t*)(xc + 16 * e) : 0u;
       int acc[4][4] = {};  // QA rows 0-15, 16-31, QB rows 0-15, 16-31 of this warp's
 #pragma unroll
       for (int ks = 0; ks < 4; ++ks) {
@@ -303,15 +316,14 @@ __global__ void __launch_bounds__(kThreads, 2)
           mma_s8(acc[t], f, xb[2 * ks], xb[2 * ks + 1]);
         }
       }
-      // columns 0, 1 of a row are in lane 4 (row % 8), column 2 in the lane after it: join the
+      // columns 0, 1 of a row are in lane 4 (row % 8), 2 and 3 in the lane after it: join the
       // digits there, then hand row 8 j + l / 4 to the lane with l % 4 = j
       float sa = 0.0f, sb = 0.0f;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int t = j >> 1, c = 2 * (j & 1);
-        const int a2 = __shfl_xor_sync(0xFFFFFFFFu, acc[t][c], 1), b2 = __shfl_xor_sync(0xFFFFFFFFu, acc[2 + t][c], 1);
-        float va = fmaf((float)a2, 65536.0f, fmaf((float)acc[t][c + 1], 256.0f, (float)acc[t][c]));
-        float vb = fmaf((float)b2, 65536.0f, fmaf((float)acc[2 + t][c + 1], 256.0f, (float)acc[2 + t][c]));
+        float va = join4(join2(acc[t][c], acc[t][c + 1]));
+        float vb = join4(join2(acc[2 + t][c], acc[2 + t][c + 1]));
         va = __shfl_sync(0xFFFFFFFFu, va, lane & 28);
         vb = __shfl_sync(0xFFFFFFFFu, vb, lane & 28);
         if ((lane & 3) == j) {
@@ -505,8 +517,8 @@ __global__ void __launch_bounds__(kCompute) decode_rows8_kernel(DecodeArgs a) {
     int acc[2 * kTiles][4] = {};
 #pragma unroll
     for (int ks = 0; ks < D / 32; ++ks) {
-      const uint32_t x0 = dcol < 3 ? *(const uint32_t*)(xc + 32 * ks) : 0u;
-      const uint32_t x1 = dcol < 3 ? *(const uint32_t*)(xc + 32 * ks + 16) : 0u;
+      const uint32_t x0 = dcol < 4 ? *(const uint32_t*)(xc + 32 * ks) : 0u;
+      const uint32_t x1 = dcol < 4 ? *(const uint32_t*)(xc + 32 * ks + 16) : 0u;
 #pragma unroll
       for (int t = 0; t < 2 * kTiles; ++t) {
         uint32_t f[4];
@@ -519,10 +531,8 @@ __global__ void __launch_bounds__(kCompute) decode_rows8_kernel(DecodeArgs a) {
 #pragma unroll
     for (int k = 0; k < 2 * kTiles; ++k) {  // as in decode_stream8_kernel
       const int t = k >> 1, c = 2 * (k & 1);
-      const int a2 = __shfl_xor_sync(0xFFFFFFFFu, acc[t][c], 1);
-      const int b2 = __shfl_xor_sync(0xFFFFFFFFu, acc[kTiles + t][c], 1);
-      float va = fmaf((float)a2, 65536.0f, fmaf((float)acc[t][c + 1], 256.0f, (float)acc[t][c]));
-      float vb = fmaf((float)b2, 65536.0f, fmaf((float)acc[kTiles + t][c + 1], 256.0f, (float)acc[kTiles + t][c]));
+      float va = join4(join2(acc[t][c], acc[t][c + 1]));
+      float vb = join4(join2(acc[kTiles + t][c], acc[kTiles + t][c + 1]));
       va = __shfl_sync(0xFFFFFFFFu, va, lane & 28);
       vb = __shfl_sync(0xFFFFFFFFu, vb, lane & 28);
       if (own == k) {
