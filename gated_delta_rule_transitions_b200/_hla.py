@@ -8,6 +8,7 @@ library or a CUDA device is missing, calls raise.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 
 import torch
@@ -186,15 +187,16 @@ def decode_workspace_bytes(cfg: HlaConfig, max_chunks: int) -> int:
     return int(lib().hla_decode_workspace_bytes(ctypes.byref(cfg), max_chunks))
 
 
-def _arg(t, name, dtype, numel, device):
-    """Device pointer of a tensor argument of the given dtype and size on CUDA device number
-    `device` (None stays None)."""
+def _arg(t, name, dtype, shape, device):
+    """Device pointer of a tensor argument of the given dtype and shape (or, flattened or split,
+    as many elements in another number of dimensions) on CUDA device number `device` (None stays
+    None)."""
     if t is None:
         return None
     # the checks in one expression first: a step's binding is most of its time (8 arguments, a
     # launch of 3.5 us: 9.9 us in all with a check of the type and a Stream object, 7.8 without)
     try:
-        if t.get_device() == device and t.dtype is dtype and t.numel() == numel and t.is_contiguous():
+        if t.get_device() == device and t.dtype is dtype and t.shape == shape and t.is_contiguous():
             return t.data_ptr()  # (a CPU tensor's device is -1)
     except AttributeError:
         pass
@@ -206,13 +208,19 @@ def _arg(t, name, dtype, numel, device):
         raise ValueError(f"{name} is on {t.device}, the call's other tensors on cuda:{device}")
     if t.dtype != dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    if t.numel() != numel:
-        raise ValueError(f"{name}: expected {numel} elements, got {tuple(t.shape)}")
-    raise ValueError(f"{name} must be contiguous")
+    if t.dim() == len(shape) and t.shape != shape:
+        raise ValueError(f"{name}: expected {tuple(shape)}, got {tuple(t.shape)}")
+    if t.numel() != math.prod(shape):
+        raise ValueError(f"{name}: expected {math.prod(shape)} elements, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
 
 def _device(t, name):
     """CUDA device number of the tensor that says where a call runs."""
+    if type(t) is torch.Tensor and (device := t.get_device()) >= 0:
+        return device
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor")
     if not t.is_cuda:
@@ -220,7 +228,9 @@ def _device(t, name):
     return t.get_device()
 
 
+# the current device's number (tensors on a device exist, so CUDA is up: no look at that) and the
 # handle of a device's current stream: without a Stream object where torch offers that
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda device: torch.cuda.current_stream(device).cuda_stream)
 
@@ -234,7 +244,7 @@ def _run(device, stream, fn, *args):
         raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{device}")
     else:
         s = stream.cuda_stream
-    if device == torch.cuda.current_device():
+    if device == _current_device():
         st = fn(*args, s)
     else:
         with torch.cuda.device(device):
@@ -243,7 +253,8 @@ def _run(device, stream, fn, *args):
         _check(st)
 
 
-_DTYPES = {HLA_F32: torch.float32, HLA_BF16: torch.bfloat16}
+_F32, _I32 = torch.float32, torch.int32
+_DTYPES = {HLA_F32: _F32, HLA_BF16: torch.bfloat16}
 
 
 class CacheSlice:
@@ -286,17 +297,17 @@ class Cache:
         if cfg.cache_format == HLA_CACHE_FACTORED and not (cfg.dtype == HLA_BF16 and d == 128 and C == 64):
             raise HlaError(HLA_ERR_UNSUPPORTED, "a factored cache needs bf16, d = 128 and C = 64")
         dt, f32, i32 = _DTYPES[cfg.dtype], torch.float32, torch.int32
-        n = B * H * max_chunks
+        n = (B, H, max_chunks)
         reps = C // cfg.pool_window if cfg.pool_window else 1
-        want = {"rk": (f32, n * reps * d), "buf_alpha": (f32, B * H * C * (d if cfg.decay_mode else 1)),
-                "buf_beta": (f32, B * H * C), "n_chunks": (i32, B), "m_partial": (i32, B), "mass": (f32, n)}
-        want.update({f: (dt, B * H * C * d) for f in ("buf_k", "buf_v", "buf_qr", "buf_kr")})
+        want = {"rk": (f32, n + (reps, d)), "buf_alpha": (f32, (B, H, C, d) if cfg.decay_mode else (B, H, C)),
+                "buf_beta": (f32, (B, H, C)), "n_chunks": (i32, (B,)), "m_partial": (i32, (B,)), "mass": (f32, n)}
+        want.update({f: (dt, (B, H, C, d)) for f in ("buf_k", "buf_v", "buf_qr", "buf_kr")})
         if cfg.cache_format == HLA_CACHE_FACTORED:
-            want.update({f: (dt, n * C * d) for f in ("Kf", "Wf", "Uf")}, df=(f32, n * (C + 4)))
+            want.update({f: (dt, n + (C, d)) for f in ("Kf", "Wf", "Uf")}, df=(f32, n + (C + 4,)))
         elif cfg.cache_format == HLA_CACHE_INT8:
-            want.update(A=(torch.int8, n * d * d), Bm=(torch.int8, n * d * d), df=(f32, n * 4))
+            want.update(A=(torch.int8, n + (d, d)), Bm=(torch.int8, n + (d, d)), df=(f32, n + (4,)))
         else:
-            want.update(A=(dt, n * d * d), Bm=(dt, n * d * d))
+            want.update(A=(dt, n + (d, d)), Bm=(dt, n + (d, d)))
         if set(buffers) - set(want) or set(want) - set(buffers) - {"mass"}:
             raise ValueError(f"expected the buffers {sorted(set(want) - {'mass'})} (and mass), got {sorted(buffers)}")
         self = cls.__new__(cls)
@@ -329,7 +340,7 @@ class Cache:
         shape = (s.B, s.H, s.max_chunks)
         if mass is None:
             mass = _kept(shape, torch.float32, torch.device("cuda", device), stream)
-        p = _arg(mass, "mass", torch.float32, s.B * s.H * s.max_chunks, device)
+        p = _arg(mass, "mass", torch.float32, shape, device)
         _run(device, stream, lib().hla_cache_track_mass, ctypes.byref(s), p)
         self.mass = mass
         return mass
@@ -380,10 +391,9 @@ def hla_gate_support(cfg, gates, mass_out=None, support_out=None, stream=None):
 def hla_gate_mass(cfg, gates, mass_out, stream=None):
     """Weight that every chunk carried over a prompt, from its gate matrix."""
     n = (cfg.T + cfg.C - 1) // cfg.C if cfg.C > 0 else 0
-    bh = cfg.B * cfg.H
     dev = _device(gates, "gates")
-    g = _arg(gates, "gates", torch.float32, bh * n * n, dev)
-    m = _arg(mass_out, "mass_out", torch.float32, bh * n, dev)
+    g = _arg(gates, "gates", torch.float32, (cfg.B, cfg.H, n, n), dev)
+    m = _arg(mass_out, "mass_out", torch.float32, (cfg.B, cfg.H, n), dev)
     _run(dev, stream, lib().hla_gate_mass, ctypes.byref(cfg), g, m)
     return mass_out
 
@@ -395,7 +405,7 @@ def hla_cache_evict(cfg, src, dst, keep, recent, kept_out, stream=None):
     for name, c in (("src", src), ("dst", dst)):
         if c.device_index != dev:
             raise ValueError(f"{name} is on cuda:{c.device_index}, kept_out on cuda:{dev}")
-    p = _arg(kept_out, "kept_out", torch.int32, cfg.B * cfg.H * keep, dev)
+    p = _arg(kept_out, "kept_out", torch.int32, (cfg.B, cfg.H, keep), dev)
     _run(dev, stream, lib().hla_cache_evict, ctypes.byref(cfg), ctypes.byref(src.struct),
          ctypes.byref(dst.struct), keep, recent, p)
     return kept_out
@@ -411,39 +421,35 @@ def gdn_workspace_bytes(cfg: GdnConfig, T: int) -> int:
     return int(lib().gdn_workspace_bytes(ctypes.byref(cfg), T))
 
 
-def _gdn_args(cfg, T, dev, q, k, v, alpha, beta, o):
-    dt, d, f32 = _DTYPES.get(cfg.dtype), cfg.dk, torch.float32
-    nk, nb = T * cfg.Hk * d, T * cfg.H
-    nv = nb * d
-    return (_arg(q, "q", dt, nk, dev), _arg(k, "k", dt, nk, dev), _arg(v, "v", dt, nv, dev),
-            _arg(alpha, "alpha", f32, nv if cfg.decay_mode else nb, dev), _arg(beta, "beta", f32, nb, dev),
-            _arg(o, "o", dt, nv, dev))
+def _gdn_args(cfg, T, H, d, dev, q, k, v, alpha, beta, o):
+    dt, hk, hv, h = _DTYPES.get(cfg.dtype), (T, cfg.Hk, d), (T, H, d), (T, H)
+    return (_arg(q, "q", dt, hk, dev), _arg(k, "k", dt, hk, dev), _arg(v, "v", dt, hv, dev),
+            _arg(alpha, "alpha", _F32, hv if cfg.decay_mode else h, dev), _arg(beta, "beta", _F32, h, dev),
+            _arg(o, "o", dt, hv, dev))
 
 
 def gdn_forward(cfg: GdnConfig, q, k, v, alpha, beta, cu_seqlens, o, state_in=None, state_out=None, slots=None,
                 workspace=None, stream=None):
     """Ragged sequences through the gated delta rule, states in and out (include/hla.h)."""
-    T, dev = v.shape[0], _device(q, "q")
-    pq, pk, pv, pa, pb, po = _gdn_args(cfg, T, dev, q, k, v, alpha, beta, o)
-    ns = cfg.n_slots * cfg.H * cfg.dv * cfg.dk
+    T, dev, n, H, d = v.shape[0], _device(q, "q"), cfg.n_seq, cfg.H, cfg.dk
+    pq, pk, pv, pa, pb, po = _gdn_args(cfg, T, H, d, dev, q, k, v, alpha, beta, o)
+    states = (cfg.n_slots, H, cfg.dv, d)
     if workspace is None:
         workspace = _scratch(gdn_workspace_bytes(cfg, T), q.device, stream)
     nb = workspace.numel() * workspace.element_size()
     _run(dev, stream, lib().gdn_forward, ctypes.byref(cfg), pq, pk, pv, pa, pb,
-         _arg(cu_seqlens, "cu_seqlens", torch.int32, cfg.n_seq + 1, dev), T,
-         _arg(slots, "slots", torch.int32, cfg.n_seq, dev), _arg(state_in, "state_in", torch.float32, ns, dev),
-         _arg(state_out, "state_out", torch.float32, ns, dev), po,
-         _arg(workspace, "workspace", workspace.dtype, workspace.numel(), dev), nb)
+         _arg(cu_seqlens, "cu_seqlens", _I32, (n + 1,), dev), T, _arg(slots, "slots", _I32, (n,), dev),
+         _arg(state_in, "state_in", _F32, states, dev), _arg(state_out, "state_out", _F32, states, dev), po,
+         _arg(workspace, "workspace", workspace.dtype, workspace.shape, dev), nb)
     return o
 
 
 def gdn_step(cfg: GdnConfig, q, k, v, alpha, beta, state, o, slots=None, stream=None):
     """One token per sequence through the gated delta rule, the states updated in place."""
-    dev = _device(q, "q")
-    pq, pk, pv, pa, pb, po = _gdn_args(cfg, cfg.n_seq, dev, q, k, v, alpha, beta, o)
-    _run(dev, stream, lib().gdn_step, ctypes.byref(cfg), pq, pk, pv, pa, pb,
-         _arg(slots, "slots", torch.int32, cfg.n_seq, dev),
-         _arg(state, "state", torch.float32, cfg.n_slots * cfg.H * cfg.dv * cfg.dk, dev), po)
+    dev, n, H, d = _device(q, "q"), cfg.n_seq, cfg.H, cfg.dk
+    pq, pk, pv, pa, pb, po = _gdn_args(cfg, n, H, d, dev, q, k, v, alpha, beta, o)
+    _run(dev, stream, lib().gdn_step, ctypes.byref(cfg), pq, pk, pv, pa, pb, _arg(slots, "slots", _I32, (n,), dev),
+         _arg(state, "state", _F32, (cfg.n_slots, H, cfg.dv, d), dev), po)
     return o
 
 

@@ -54,7 +54,7 @@ def test_tracking_stops(hla, monkeypatch):
     cache = tracked(hla, torch.zeros(2, 2, 4))
     monkeypatch.setattr(hla.Cache, "device_index", 0)
     monkeypatch.setattr(hla, "_raw_stream", lambda d: 0)
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(hla, "_current_device", lambda: 0)
     cache.untrack_mass()
     assert cache.struct.mass is None and cache.mass is None
     assert cache.slice(0, 1).struct.mass is None

@@ -15,7 +15,7 @@ class Stream:
 class Memory:
     """A tensor as far as the binding looks at one."""
 
-    dtype = torch.uint8
+    dtype, shape = torch.uint8, (1 << 30,)
 
     def __init__(self, stream):
         self.stream, self.recorded = stream, []
@@ -62,7 +62,7 @@ def hla(monkeypatch):
 
     monkeypatch.setattr(torch.cuda, "stream", stream)
     monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: "current")
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(_hla, "_current_device", lambda: 0)
     monkeypatch.setattr(torch, "empty", empty)
     monkeypatch.setattr(_hla, "lib", Library)
     monkeypatch.setattr(_hla, "_ptr", lambda t: None)
@@ -107,7 +107,7 @@ def test_calls_run_on_their_tensors_device(hla, monkeypatch):
 
     ran = []
     monkeypatch.setattr(torch.cuda, "device", device)
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: now[0])
+    monkeypatch.setattr(hla.m, "_current_device", lambda: now[0])
     monkeypatch.setattr(torch.cuda, "current_stream", lambda d=None: types.SimpleNamespace(cuda_stream=100 + now[0]))
     monkeypatch.setattr(hla.m, "_raw_stream", lambda d: 100 + d)
     monkeypatch.setattr(hla.m, "_device", lambda *a: 1)
@@ -135,3 +135,26 @@ def test_calls_run_on_their_tensors_device(hla, monkeypatch):
     monkeypatch.setattr(Memory, "get_device", lambda self: 1)
     hla.m.Cache(cfg, 4, device="cuda:1")
     assert ran[-1] == ("hla_cache_init", 1, 101)
+
+
+def test_transposed_tensors_are_refused(monkeypatch):
+    """As many elements and as many dimensions, in another order: not the tensor that was asked for.
+    One of fewer or more dimensions is taken by its elements."""
+    from gated_delta_rule_transitions_b200 import _hla
+
+    class OnDevice(torch.Tensor):
+        is_cuda = True
+
+        def get_device(self):
+            return 0
+
+    make = lambda *s: torch.zeros(*s).as_subclass(OnDevice)
+    for shape in ((6, 4, 8), (192,), (24, 8), (6, 4, 8, 1)):
+        t = make(*shape)
+        assert _hla._arg(t, "x", torch.float32, (6, 4, 8), 0) == t.data_ptr()
+    for shape in ((4, 6, 8), (8, 4, 6), (1, 24, 8)):
+        with pytest.raises(ValueError, match="x: expected"):
+            _hla._arg(make(*shape), "x", torch.float32, (6, 4, 8), 0)
+    for shape in ((6, 4, 9), (191,), (0,)):
+        with pytest.raises(ValueError, match="x: expected"):
+            _hla._arg(make(*shape), "x", torch.float32, (6, 4, 8), 0)
