@@ -732,6 +732,21 @@ hla_status hla_cache_evict(const hla_config* cfg, const hla_cache* src, hla_cach
     return fail(HLA_ERR_INVALID_ARG, "dst shares %d of %d arrays with src (it is src itself, or has its own)", same,
                 all);
   e.in_place = same != 0;
+  if (!e.in_place) {
+    // slices of one cache, say: sequences that both hold would be read and written at once
+    const long BH = (long)e.B * e.H;
+    auto overlap = [](const void* s, long sn, const void* t, long tn) {
+      return s != nullptr && t != nullptr && (uintptr_t)s < (uintptr_t)t + tn && (uintptr_t)t < (uintptr_t)s + sn;
+    };
+    bool any = overlap(src->n_chunks, e.B * 4L, dst->n_chunks, e.B * 4L) ||
+               overlap(src->m_partial, e.B * 4L, dst->m_partial, e.B * 4L) ||
+               overlap(src->mass, BH * e.src_chunks * 4, dst->mass, BH * e.dst_chunks * 4);
+    for (int x = 0; x < e.n_arrays; ++x)
+      any |= overlap(e.src[x], BH * e.src_chunks * e.chunk_bytes[x], e.dst[x], BH * e.dst_chunks * e.chunk_bytes[x]);
+    for (int x = 0; x < e.n_open; ++x)
+      any |= overlap(e.open_src[x], BH * e.open_bytes[x], e.open_dst[x], BH * e.open_bytes[x]);
+    if (any) return fail(HLA_ERR_INVALID_ARG, "dst's arrays overlap src's without being them");
+  }
   HLA_CUDA(hla::launch_evict(e, (cudaStream_t)stream), "evict launch");
   return HLA_OK;
 }
