@@ -408,6 +408,7 @@ __global__ void __launch_bounds__(128, 5)
 #pragma unroll
         for (int e = 0; e < 4; ++e) finite_or_note(acc[0][e], 16 * (jb + lev) + (lane >> 2) + 8 * (e >> 1));
       }
+      __syncwarp();  // (the next product is the whole warp's)
       store16(Us + 16 * (jb + lev) * kP + 16 * jb + 8 * nh, kP, acc[0], -1.0f, lane);
     }
     __syncthreads();
@@ -963,6 +964,7 @@ __global__ void __launch_bounds__(Geo<kV>::kThreads, 1)
           }
         }
       }
+      __syncwarp();
       ok = __all_sync(0xFFFFFFFFu, tc::mbar_wait(doneA, par, abort_s));
       if (!ok) break;
       tc::tc_fence_after();
