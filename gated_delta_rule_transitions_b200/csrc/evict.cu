@@ -17,7 +17,8 @@
 //                      from a chunk kept[i] >= i, and reads run ahead of writes, so the move
 //                      is safe in place without any barrier.
 // The move is bound by HBM: 16 sequences x 16 heads, 384 of 512 chunks kept, 13.0 GB in 1.97 ms,
-// 1.0 of the measured copy rate; one sequence of 29 chunks 14.5 us, two launches' latency.
+// 1.0 of the measured copy rate; in place, where chunks that keep their index stay, 7.6 GB in
+// 1.16 ms, 0.99; one sequence of 29 chunks 14.6 us, two launches' latency.
 #include <cooperative_groups.h>
 
 #include "common.cuh"

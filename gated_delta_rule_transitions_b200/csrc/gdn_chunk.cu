@@ -13,10 +13,10 @@
 // gdn_scan_kernel then walks the chunks of one (sequence, head) and 16, 32 or 64 of its value
 // columns, three products a chunk, each waiting for the one before.
 //
-// What bounds it: the scan's chain of a chunk, 3,030 cycles with 16 columns and 6,000 with 64
-// (there shared memory's bandwidth as well); the tensor cores are active 16 % of the time.
-// Measured, 16 heads: 16384 tokens of one sequence 534 us (T and G 96), four sequences of
-// 4096 tokens 318 us (T and G 99).
+// What bounds it: the scan's chain of a chunk, 1.7 us with 16 columns and 3.5 with 64 (there
+// shared memory's bandwidth as well); the tensor cores are active 16 % of the time.
+// Measured, 16 heads: 16384 tokens of one sequence 532 us (T and G 96, the scan 443),
+// four sequences of 4096 tokens 319 us (99 and 224).
 //
 // Precision.  The state is float32 and stays so: it is held in registers, and what goes into
 // a product (S, R, U, T) goes in as three bf16 numbers, x = x1 + x2 + x3, each the eight bits
@@ -32,8 +32,8 @@
 // the same, so a token that is no number would spoil the 63 before it.  Therefore: gdn_wy_kernel
 // keeps T and G finite and writes an undefined gamma from the first token on whose key, decay or
 // beta is none; gdn_scan_kernel takes such tokens, and values that are none, as zeros, and makes
-// undefined what they reach.  (A bad query has a row of its own.  The checks cost 3 %: 16384
-// tokens 524 -> 535 us.)
+// undefined what they reach.  (A bad query has a row of its own.  The checks cost 2 %: 16384
+// tokens 524 -> 534 us.)
 #include <climits>
 
 #include "common.cuh"

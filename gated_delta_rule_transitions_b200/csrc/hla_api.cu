@@ -773,10 +773,12 @@ static hla_status check_gdn(const gdn_config* c) {
 // at some 36 tokens (16 heads: 16 sequences at 36 to 56, 64 at 37).  They seldom are: one prompt
 // among single tokens holds up rows for as long as it is, and single tokens in chunks cost a
 // chunk each.  So the kernels share the batch wherever that can pay.  Measured, 16 heads:
-// 127 x 1 + 2048 tokens 803 us by rows, 175 shared; 60 x 1 + 4 x 1000 tokens 226 by chunks, 127
-// shared.  What it costs a batch that is all alike: 64 x 30 tokens 132 by rows, 145 shared; 64 x
-// 49 tokens 165 by chunks, 175 shared.  From 128 tokens in the mean up, short sequences' chunks
-// are few beside the others' (128 x 200 tokens: 734 us by chunks, 763 shared).
+// 127 x 1 + 2048 tokens 803 us by rows, 181 shared; 60 x 1 + 4 x 1000 tokens 226 by chunks, 131
+// shared.  What it costs a batch that is all alike: 64 x 30 tokens 132 by rows, 144 shared; 64 x
+// 49 tokens 177 shared, 6 % more than by chunks.  From 128 tokens in the mean up, short sequences'
+// chunks are few beside the others' (128 x 200 tokens: 768 us by chunks, 4 % less than shared).
+// Above kGdnRankedSeqs sequences nothing is shared: every scan CTA ranks the lengths by itself, at a
+// cost that grows with their square (511 x 1 + 8192 tokens 0.72 ms, 512 x 1 + 8192 by rows 3.2 ms).
 constexpr int kGdnByRow = 36;
 static bool gdn_uses_chunks(const gdn_config* c, int32_t T) {
   if (c->dtype != HLA_BF16 || c->dk != 128 || c->decay_mode != HLA_DECAY_SCALAR) return false;

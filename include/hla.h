@@ -342,7 +342,7 @@ typedef struct gdn_config {
 size_t gdn_workspace_bytes(const gdn_config* cfg, int32_t T);
 
 /*
- * gdn_forward -- ragged sequences of any length through the rule, states in and out.
+ * gdn_forward -- ragged sequences of any length through the rule, states in and out (T at least 1).
  * In:  q, k [T,Hk,d], v [T,H,d] dtype; alpha [T,H] (CHANNEL: [T,H,d]) and beta [T,H]
  *      float32, alpha in [0,1] (these two, where scalar, only 4-byte aligned); cu_seqlens
  *      [n_seq + 1] int32 (device): sequence i is rows cu_seqlens[i] .. cu_seqlens[i+1] - 1
